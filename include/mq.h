@@ -364,6 +364,145 @@ mq_status mq_conv_backward_noalloc(const mq_conv *p, const mq_qtensor *w, const 
                                    const mq_qtensor *x, float *gw_dev, float *gx_dev,
                                    hipStream_t stream);
 
+/* ---- attention over an 8-bit key/value cache ------------------------------------------------
+ *
+ * A decoder's serving path around one paged cache: attention over whole prompts
+ * (mq_attn_prompt), the quantizing write of their keys and values (mq_kv_append), attention of
+ * the newly generated tokens over the cache (mq_attn_cached), and the eviction of the cached
+ * tokens that received the least attention (mq_kv_evict). The cache follows the library's block
+ * scaling: E4M3 codes, one scale per block of tokens and head.
+ */
+
+/* Element type of queries, keys, values and outputs. */
+typedef enum { MQ_F16 = 1, MQ_BF16 = 2 } mq_dtype;
+
+/* Tokens that share one scale of the cache. */
+#define MQ_KV_BLOCK 16
+
+/*
+ * Token vectors: `tokens` rows of `heads` vectors of `head_dim` elements of type `dtype`
+ * (mq_dtype). Element (t, h, d) is data[t * token_stride + h * head_stride + d] (strides in
+ * elements, so that the three parts of one fused projection can be passed as they lie). data
+ * must be 16-byte aligned and both strides multiples of 8 (MQ_ERR_ARG otherwise).
+ */
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;
+    int32_t tokens, heads, head_dim, dtype;
+} mq_rows;
+
+/*
+ * A paged cache of keys and values in 8 bits. num_pages pages of page_size tokens (a multiple
+ * of MQ_KV_BLOCK); head_dim 64, 96, 128, 192 or 256. With NB = page_size / 16:
+ *   k_codes  [num_pages][kv_heads][page_size][head_dim]   E4M3 (s|eeee|mmm, bias 7)
+ *   v_codes  [num_pages][kv_heads][NB][head_dim][16]      E4M3, the 16 tokens of a block together
+ *   k_scales, v_scales [num_pages][kv_heads][NB]          one byte e per block: the scale 2^(e-127)
+ * A key element's value is decode(code) * 2^(e-127). Scale bytes written by this library lie in
+ * [10, 247]; 255 marks a block that received a NaN or an infinity: its codes are 0, and every
+ * attention row that sees a token of the block is NaN.
+ * Token t of a sequence lies in page table[t / page_size], slot t % page_size. A table entry
+ * outside [0, num_pages) holds no tokens: nothing is read from it or written to it, and its
+ * tokens take no part in attention.
+ * k_codes and v_codes must be 16-byte aligned (MQ_ERR_ARG otherwise). No two sequences may share
+ * a page that one of them writes.
+ */
+typedef struct {
+    int32_t num_pages, page_size, kv_heads, head_dim;
+    uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
+} mq_kv_cache;
+
+/*
+ * mq_kv_append: quantize new keys and values into the cache behind each sequence's tokens.
+ * Sequence s has lens[s] tokens in the cache and receives rows [cu[s], cu[s+1]) of k and v
+ * (cu[0..n_seqs] ascending from 0 to k->tokens). Each block of 16 tokens and head that receives a
+ * token: with amax the largest magnitude of the new tokens in it,
+ *   e    = max(10, the smallest e with amax <= 448 * 2^(e-127), e_held)
+ *   code = CastE4M3(x * 2^(127-e))                 new tokens (nearest, ties to even)
+ *   code = CastE4M3(value(code) * 2^(e_held-e))    tokens that the block held
+ * (e_held, and held tokens, only where the block held tokens); slots of the block after its last
+ * token become 0. A NaN or an infinity among the new values, or e_held = 255, gives e = 255 and
+ * codes 0. Scaling by powers of two is exact, so each code is rounded once for each time its
+ * block's scale grows. Appending the same tokens to the same lens again changes nothing.
+ * table_dev: [n_seqs][max_pages] page numbers. lens_dev is not changed. Tokens whose position
+ *          reaches max_pages * page_size are dropped.
+ * Errors: MQ_ERR_ARG (null or misaligned pointer, negative size, unknown dtype, page_size no
+ *         multiple of 16), MQ_ERR_SHAPE (k, v and the cache disagree), MQ_ERR_UNSUPPORTED
+ *         (head_dim outside the set, 2^31 or more work items).
+ */
+mq_status mq_kv_append(const mq_kv_cache *cache, const mq_rows *k, const mq_rows *v,
+                       const int32_t *table_dev, const int32_t *lens_dev, const int32_t *cu_dev,
+                       int32_t n_seqs, int32_t max_pages, hipStream_t stream);
+
+/* Bytes of device workspace mq_attn_cached needs for these sizes (0 on invalid input). weights:
+ * 1 if the call adds up attention weights. */
+size_t mq_attn_cached_workspace_bytes(int32_t n_seqs, int32_t q_heads, int32_t kv_heads,
+                                      int32_t head_dim, int32_t q_len, int32_t max_len,
+                                      int32_t weights);
+
+/*
+ * mq_attn_cached: attention of each sequence's last q_len tokens over its cached tokens.
+ * Sequence s holds lens[s] tokens, its new ones (already appended) included. Row i of sequence s,
+ * i in [0, q_len), sees tokens t <= lens[s] - q_len + i; query head h reads key/value head
+ * h / (q_heads / kv_heads):
+ *   p[t] = softmax_t(scale * sum_d q[d] * K[t][d])     out[d] = sum_t p[t] * V[t][d]
+ * with the softmax and both sums in fp32 from exact products of the cache's values; p is rounded
+ * to bf16 for the second product (to two bf16 parts where dtype is MQ_F16). A row that sees no
+ * token is 0.
+ * q, out:  n_seqs * q_len rows, sequence by sequence.
+ * max_len: no sequence holds more tokens than this (longer ones are read up to it); 0 stands for
+ *          max_pages * page_size. It sizes the launch and the workspace.
+ * weights_dev: null, or fp32 [num_pages][kv_heads][page_size]: for each cached token and
+ *          key/value head, p summed over the head's query heads and the q_len rows is added to
+ *          the token's place (in a fixed order: results are deterministic).
+ * ws_dev / ws_bytes: device scratch, 16-byte aligned, of at least
+ *          mq_attn_cached_workspace_bytes(...) bytes (may be null where that is 0).
+ * Errors: MQ_ERR_ARG, MQ_ERR_SHAPE (q, out and the cache disagree; q_heads no multiple of
+ *         kv_heads), MQ_ERR_WORKSPACE, MQ_ERR_UNSUPPORTED (as for mq_kv_append).
+ */
+mq_status mq_attn_cached(const mq_kv_cache *cache, const mq_rows *q, const mq_rows *out,
+                         const int32_t *table_dev, const int32_t *lens_dev, int32_t n_seqs,
+                         int32_t max_pages, int32_t q_len, int32_t max_len, float scale,
+                         float *weights_dev, void *ws_dev, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * mq_attn_prompt: causal attention over whole prompts, packed one after another. Sequence s has
+ * rows [cu[s], cu[s+1]) of q, k, v and out; row i of a sequence sees its rows j <= i; query head
+ * h reads key/value head h / (q_heads / kv_heads):
+ *   p[j] = softmax_j(scale * sum_d q[d] * k[j][d])     out[d] = sum_j p[j] * v[j][d]
+ * with the softmax and both sums in fp32 and p rounded to dtype for the second product.
+ * max_len: no sequence is longer than this (rows past it are neither read nor written).
+ * Errors: as for mq_attn_cached (without a workspace).
+ */
+mq_status mq_attn_prompt(const mq_rows *q, const mq_rows *k, const mq_rows *v, const mq_rows *out,
+                         const int32_t *cu_dev, int32_t n_seqs, int32_t max_len, float scale,
+                         hipStream_t stream);
+
+/*
+ * mq_kv_evict: cut each sequence's cache back to at most `keep` tokens, head by head. Of a
+ * sequence's lens[s] tokens (all of them where lens[s] <= keep) each key/value head keeps the
+ * last min(recent, keep), and of the others those with the largest weights (equal weights: the
+ * lower position first; a NaN weight is below every other), in their order. They are copied to
+ * the first min(lens[s], keep) slots of new_table's pages:
+ *   e    = max of the scale bytes that the kept tokens of a new block come with
+ *   code = CastE4M3(value(code) * 2^(e_src - e))   (unchanged where e_src = e; all 0 if e = 255)
+ * and their weights with them; slots of a new block after its last token become 0 (weights too).
+ * new_table's pages must not be pages of `table_dev` or of each other. The old pages are left
+ * as they are, for the caller to free.
+ * weights_dev: fp32 [num_pages][kv_heads][page_size], as mq_attn_cached adds them up.
+ * table_dev [n_seqs][max_pages]; new_table_dev [n_seqs][new_max_pages], with
+ *          keep <= new_max_pages * page_size.
+ * new_lens_dev: [n_seqs], receives min(lens[s], keep).
+ * kept_dev: [n_seqs][kv_heads][keep], receives the kept tokens' former positions, ascending, -1
+ *          after the last.
+ * A kept token whose old page is outside [0, num_pages) is copied as code 0 with scale byte 10.
+ * Errors: MQ_ERR_ARG, MQ_ERR_SHAPE (keep does not fit new_table), MQ_ERR_UNSUPPORTED.
+ */
+mq_status mq_kv_evict(const mq_kv_cache *cache, float *weights_dev, const int32_t *table_dev,
+                      const int32_t *lens_dev, const int32_t *new_table_dev,
+                      int32_t *new_lens_dev, int32_t *kept_dev, int32_t n_seqs,
+                      int32_t max_pages, int32_t new_max_pages, int32_t keep, int32_t recent,
+                      hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

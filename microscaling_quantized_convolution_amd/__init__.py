@@ -25,6 +25,8 @@ MQ_QUANTIZE_AMAX_READY = 1   # mq_quantize flag: the workspace already holds thi
 MQ_SRC_DENSE, MQ_SRC_NCHW, MQ_SRC_OIHW = 0, 1, 2  # mq_quant_job.layout
 MQ_QUANTIZE_BATCH_MAX = 4
 MQ_NOALLOC_SCRATCH_BYTES = 32 << 20  # library-owned split-K scratch of mq_conv_backward_noalloc
+MQ_F16, MQ_BF16 = 1, 2  # mq_dtype: element type of the attention calls
+MQ_KV_BLOCK = 16        # tokens that share one scale of the key/value cache
 
 EXPORTS = (
     "mq_status_str", "mq_codes_bytes", "mq_scales_bytes", "mq_relayout_cbf",
@@ -33,6 +35,8 @@ EXPORTS = (
     "mq_wgrad_workspace_bytes",
     "mq_conv_wgrad", "mq_conv_dgrad", "mq_conv_backward", "mq_conv_backward_noalloc",
     "mq_conv_fwd_amax", "mq_conv_backward_amax",
+    "mq_kv_append", "mq_attn_cached_workspace_bytes", "mq_attn_cached", "mq_attn_prompt",
+    "mq_kv_evict",
 )
 
 
@@ -58,6 +62,19 @@ class mq_quant_job(ctypes.Structure):
 class mq_conv(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "Cin", "H", "W", "Cout", "Kh", "Kw",
                                               "stride_h", "stride_w", "pad_h", "pad_w")]
+
+
+class mq_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("tokens", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class mq_kv_cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -98,6 +115,13 @@ def _load() -> ctypes.CDLL:
     L.mq_conv_backward_amax.argtypes = [ctypes.POINTER(mq_conv), ctypes.POINTER(mq_qtensor),
                                         ctypes.POINTER(mq_qtensor), ctypes.POINTER(mq_qtensor),
                                         P, P, P, sz, P, sz, P]
+    R, C, f32 = ctypes.POINTER(mq_rows), ctypes.POINTER(mq_kv_cache), ctypes.c_float
+    L.mq_kv_append.argtypes = [C, R, R, P, P, P, i32, i32, P]
+    L.mq_attn_cached_workspace_bytes.restype = sz
+    L.mq_attn_cached_workspace_bytes.argtypes = [i32] * 7
+    L.mq_attn_cached.argtypes = [C, R, R, P, P, i32, i32, i32, i32, f32, P, P, sz, P]
+    L.mq_attn_prompt.argtypes = [R, R, R, R, P, i32, i32, f32, P]
+    L.mq_kv_evict.argtypes = [C, P, P, P, P, P, P, i32, i32, i32, i32, i32, P]
     for name in EXPORTS:
         getattr(L, name).restype = getattr(L, name).restype or ctypes.c_int
     return L
@@ -295,3 +319,165 @@ def out_hw(p: ConvLike) -> Tuple[int, int]:
     c = conv_struct(p)
     return ((c.H + 2 * c.pad_h - c.Kh) // c.stride_h + 1,
             (c.W + 2 * c.pad_w - c.Kw) // c.stride_w + 1)
+
+
+# ---- attention over an 8-bit key/value cache ---------------------------------------------------
+#
+# These calls are made once per layer and token, so their marshalling is kept short: checks that
+# the library cannot make itself (types, contiguity, device), then one foreign call.
+
+_DTYPES = {torch.float16: MQ_F16, torch.bfloat16: MQ_BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream if torch.version.hip else None
+
+
+def _rows(t: torch.Tensor, what: str) -> mq_rows:
+    """[tokens][heads][dim] view with a contiguous last dimension -> mq_rows."""
+    dt = _DTYPES.get(t.dtype)
+    if dt is None or t.dim() != 3 or not t.is_cuda or t.stride(2) != 1:
+        raise ValueError(f"{what}: expected a float16 or bfloat16 CUDA tensor [tokens][heads][dim] "
+                         f"with contiguous elements, got {tuple(t.shape)} {t.dtype} on {t.device}, "
+                         f"strides {t.stride()}")
+    n, h, d = t.shape
+    return mq_rows(t.data_ptr(), t.stride(0), t.stride(1), n, h, d, dt)
+
+
+def _dense(t: torch.Tensor, dtype: torch.dtype, shape, what: str) -> int:
+    """Address of a contiguous CUDA tensor of that type and shape."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} CUDA tensor {tuple(shape)}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _attn_stream(stream, device: torch.device):
+    """The given stream, or the device's current one; the device has to be the current one."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return _raw_stream(device.index) if stream is None else _stream(stream)
+
+
+class KVCache:
+    """A paged key/value cache in 8 bits (mq_kv_cache; the layouts are in include/mq.h).
+
+    Made from its four uint8 tensors, k_codes [pages][heads][page_size][dim],
+    v_codes [pages][heads][page_size / 16][dim][16], k_scales and v_scales
+    [pages][heads][page_size / 16], or by :meth:`empty`."""
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor,
+                 v_scales: torch.Tensor):
+        if k_codes.dim() != 4 or k_codes.shape[2] % MQ_KV_BLOCK:
+            raise ValueError(f"k_codes: expected [pages][heads][page_size][dim] with page_size a "
+                             f"multiple of {MQ_KV_BLOCK}, got {tuple(k_codes.shape)}")
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k_codes.shape
+        blocks = (self.num_pages, self.kv_heads, self.page_size // MQ_KV_BLOCK)
+        self.device = k_codes.device
+        self.k_codes, self.v_codes = k_codes, v_codes
+        self.k_scales, self.v_scales = k_scales, v_scales
+        u8 = torch.uint8
+        self.struct = mq_kv_cache(
+            self.num_pages, self.page_size, self.kv_heads, self.head_dim,
+            _dense(k_codes, u8, k_codes.shape, "k_codes"),
+            _dense(v_codes, u8, blocks + (self.head_dim, MQ_KV_BLOCK), "v_codes"),
+            _dense(k_scales, u8, blocks, "k_scales"), _dense(v_scales, u8, blocks, "v_scales"))
+        self._ref = ctypes.byref(self.struct)
+        self.weights_shape = torch.Size((self.num_pages, self.kv_heads, self.page_size))
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
+              device: Union[str, torch.device] = "cuda") -> "KVCache":
+        """A cache that holds nothing yet (its memory is not cleared: mq_kv_append writes whole
+        blocks)."""
+        new = lambda *shape: torch.empty(shape, dtype=torch.uint8, device=device)
+        blocks = (num_pages, kv_heads, page_size // MQ_KV_BLOCK)
+        return cls(new(num_pages, kv_heads, page_size, head_dim),
+                   new(*blocks, head_dim, MQ_KV_BLOCK), new(*blocks), new(*blocks))
+
+    def values(self) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Keys and values as fp32 [pages][heads][page_size][dim] (for inspection: every slot is
+        decoded, also those that hold no token)."""
+        out = []
+        for codes, scales in ((self.k_codes.view(*self.k_scales.shape, MQ_KV_BLOCK, -1),
+                               self.k_scales), (self.v_codes.transpose(3, 4), self.v_scales)):
+            e = scales.to(torch.int32)
+            f = torch.where(e == 255, torch.nan, torch.ldexp(torch.ones_like(e, dtype=torch.float32),
+                                                             e - 127))
+            out.append((codes.view(torch.float8_e4m3fn).float() * f[..., None, None])
+                       .reshape(self.k_codes.shape))
+        return out[0], out[1]
+
+
+def _table(table: torch.Tensor, n: int) -> int:
+    if table.dim() != 2:
+        raise ValueError(f"table: expected [sequences][pages], got {tuple(table.shape)}")
+    return _dense(table, torch.int32, (n, table.shape[1]), "table")
+
+
+def mq_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Tensor,
+                 lens: torch.Tensor, cu: torch.Tensor, stream=None):
+    """Quantize the packed keys and values k, v [tokens][kv_heads][dim] into the cache behind each
+    sequence's lens[s] tokens: sequence s receives rows cu[s]:cu[s + 1]. lens is not changed."""
+    n = lens.shape[0]
+    rk, rv = _rows(k, "k"), _rows(v, "v")
+    _check(_lib.mq_kv_append(cache._ref, rk, rv, _table(table, n),
+                             _dense(lens, torch.int32, (n,), "lens"),
+                             _dense(cu, torch.int32, (n + 1,), "cu"), n, table.shape[1],
+                             _attn_stream(stream, cache.device)), "mq_kv_append")
+
+
+def mq_attn_cached_workspace_bytes(n_seqs: int, q_heads: int, kv_heads: int, head_dim: int,
+                                   q_len: int, max_len: int, weights: bool = False) -> int:
+    return int(_lib.mq_attn_cached_workspace_bytes(n_seqs, q_heads, kv_heads, head_dim, q_len,
+                                                   max_len, int(weights)))
+
+
+def attn_cached_workspace(n_seqs: int, q_heads: int, kv_heads: int, head_dim: int, q_len: int,
+                          max_len: int, weights: bool = False,
+                          device: Union[str, torch.device] = "cuda") -> torch.Tensor:
+    """Device scratch for mq_attn_cached calls of these sizes."""
+    return torch.empty(mq_attn_cached_workspace_bytes(n_seqs, q_heads, kv_heads, head_dim, q_len,
+                                                      max_len, weights),
+                       dtype=torch.uint8, device=device)
+
+
+def mq_attn_cached(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor,
+                   out: torch.Tensor, ws: Optional[torch.Tensor], scale: float, q_len: int = 1,
+                   max_len: int = 0, weights: Optional[torch.Tensor] = None, stream=None):
+    """Attention of each sequence's last q_len tokens, q [sequences * q_len][q_heads][dim], over
+    its lens[s] cached tokens (these included), into out. weights (fp32, cache.weights_shape)
+    gains the attention each cached token received."""
+    n = lens.shape[0]
+    rq, ro = _rows(q, "q"), _rows(out, "out")
+    pw = None if weights is None else _dense(weights, torch.float32, cache.weights_shape, "weights")
+    pws = None if ws is None else _dense(ws, torch.uint8, ws.shape, "ws")
+    _check(_lib.mq_attn_cached(cache._ref, rq, ro, _table(table, n),
+                               _dense(lens, torch.int32, (n,), "lens"), n, table.shape[1], q_len,
+                               max_len, scale, pw, pws, 0 if ws is None else ws.numel(),
+                               _attn_stream(stream, cache.device)), "mq_attn_cached")
+
+
+def mq_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                   cu: torch.Tensor, max_len: int, scale: float, stream=None):
+    """Causal attention over packed prompts: rows cu[s]:cu[s + 1] of q, out [tokens][q_heads][dim]
+    and k, v [tokens][kv_heads][dim] are sequence s, none longer than max_len."""
+    n = cu.shape[0] - 1
+    rq, rk, rv, ro = _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), _rows(out, "out")
+    _check(_lib.mq_attn_prompt(rq, rk, rv, ro, _dense(cu, torch.int32, (n + 1,), "cu"), n, max_len,
+                               scale, _attn_stream(stream, q.device)), "mq_attn_prompt")
+
+
+def mq_kv_evict(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor,
+                new_table: torch.Tensor, new_lens: torch.Tensor, kept: torch.Tensor, recent: int,
+                stream=None):
+    """Keep at most kept.shape[2] tokens of each sequence and head, the `recent` last ones and those
+    with the largest weights, copied to the pages of new_table; kept [sequences][kv_heads][keep]
+    receives their former positions, new_lens the sequences' new lengths."""
+    n, keep = lens.shape[0], kept.shape[-1]
+    i32 = torch.int32
+    _check(_lib.mq_kv_evict(cache._ref,
+                            _dense(weights, torch.float32, cache.weights_shape, "weights"),
+                            _table(table, n), _dense(lens, i32, (n,), "lens"),
+                            _table(new_table, n), _dense(new_lens, i32, (n,), "new_lens"),
+                            _dense(kept, i32, (n, cache.kv_heads, keep), "kept"), n,
+                            table.shape[1], new_table.shape[1], keep, recent,
+                            _attn_stream(stream, cache.device)), "mq_kv_evict")

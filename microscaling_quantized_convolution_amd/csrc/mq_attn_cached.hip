@@ -1,0 +1,389 @@
+// mq_attn_cached.hip -- attention of a few new tokens over the 8-bit key/value cache.
+//
+// out = softmax(scale q K^T) V over one pass of the cache: each wave holds a running maximum m,
+// a running sum l and the unnormalised output O of 16 query rows (the query heads of one
+// key/value head times the new tokens) and takes 64 cached tokens at a time:
+//   S^T = K Q^T            v_mfma 16x16x32, the codes decoded exactly to dtype
+//   P   = 2^(S - m)        in fp32, on the accumulator registers
+//   O^T += V^T P^T         v_mfma 16x16x32 in bf16
+// The products are laid out so that no value changes lanes between them. In step t of the first
+// product, row m of the tile is token 4t + m%4 of the tile's block m/4; its result then leaves
+// lane group g = lane/16 with tokens 4t..4t+3 of block g, and after four steps with all 16
+// tokens of one block: the operand that the second product wants from that group, under one
+// scale of K and one of V. The cache keeps a block's values token by token within a dimension,
+// so the other operand is a 16-byte load.
+#include "mq_attn_device.hpp"
+
+namespace mq {
+namespace {
+
+constexpr int kTile = 64;  // tokens a wave takes at a time: one block for each lane group
+constexpr int kRows = 16;  // query rows of a workgroup
+constexpr int kWaves = 4;
+constexpr int kWantWorkgroups = 1024;
+
+struct CachedPlan {
+    int rows, row_tiles; // query rows of a key/value head, in tiles of kRows
+    int chunk, splits;   // tokens of a workgroup, workgroups along the cache
+    int slots;           // max_len up to whole tiles
+    size_t ml, part, fin, scores, bytes; // workspace offsets
+};
+
+__host__ __device__ inline CachedPlan cached_plan(int n, int q_heads, int kv_heads, int d, int q_len, int max_len,
+                       bool weights)
+{
+    CachedPlan p;
+    p.rows = q_heads / kv_heads * q_len;
+    p.row_tiles = (p.rows + kRows - 1) / kRows;
+    const int64_t x = (int64_t)n * kv_heads * p.row_tiles;
+    const int64_t tiles = ((int64_t)max_len + kTile - 1) / kTile;
+    // a workgroup's waves take at least one tile each; more workgroups than the chip holds at
+    // once would only add partial results
+    int64_t per = (tiles * x + kWantWorkgroups - 1) / kWantWorkgroups;
+    per = (per + kWaves - 1) / kWaves * kWaves;
+    if (per < kWaves) per = kWaves;
+    p.chunk = (int)(per * kTile > (1 << 30) ? 1 << 30 : per * kTile);
+    p.splits = (int)((tiles * kTile + p.chunk - 1) / p.chunk);
+    if (p.splits < 1) p.splits = 1;
+    p.slots = (int)(tiles * kTile);
+    const size_t units = (size_t)x * p.splits;
+    p.ml = 0;
+    p.part = p.splits > 1 ? p.ml + units * kRows * 8 : 0;
+    p.fin = p.splits > 1 ? p.part + units * kRows * d * 4 : 0;
+    p.scores = weights ? p.fin + (size_t)x * kRows * 8 : p.fin;
+    p.bytes = weights ? p.scores + (size_t)x * kRows * p.slots * 4 : p.fin;
+    return p;
+}
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+__device__ __forceinline__ int held_tokens(const CachedArgs &a, int s)
+{
+    const int64_t cap = (int64_t)a.max_pages * a.c.page;
+    const int c = cap < a.max_len ? (int)cap : a.max_len;
+    return clampi(a.lens[s], 0, c);
+}
+
+// The softmax's scale times a block's scale, 2^(e-127); NaN for e = 255.
+__device__ __forceinline__ float block_scale(float s, int e)
+{
+    return e == 255 ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(s, e - 127);
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(64 * kWaves) attn_cached_kernel(CachedArgs a, CachedPlan pl)
+{
+    typedef typename Elem<DT>::x8 x8;
+    constexpr int KS = D / 32;     // steps of 32 dimensions in the first product
+    constexpr bool WIDE = D % 64 == 0; // 16-byte loads of K: two steps each
+    constexpr int VT = D / 16;     // tiles of 16 dimensions in the second product
+    constexpr int LD = D + 4;      // row of the workgroup's sum in LDS, in floats
+    __shared__ __align__(16) float part_o[(kWaves - 1) * kRows * LD];
+    __shared__ float part_m[kWaves][kRows], part_l[kWaves][kRows];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const int x = blockIdx.x, rt = x % pl.row_tiles;
+    const int h = x / pl.row_tiles % a.c.heads, s = x / pl.row_tiles / a.c.heads;
+    const int len = held_tokens(a, s);
+    const int begin = (int)blockIdx.y * pl.chunk;
+    if (begin >= len && blockIdx.y) return;
+    const int end = len - begin < pl.chunk ? len : begin + pl.chunk;
+    const int group = a.q_heads / a.c.heads;
+    const int row = rt * kRows + n;
+    const int qi = row / group, qh = h * group + row % group;
+    const bool real = row < pl.rows;
+    // tokens this lane's row sees
+    const int see = real ? clampi(len - a.q_len + qi + 1, 0, len) : 0;
+    const int per = a.c.page / kKvBlock;
+    const int32_t *table = a.table + (int64_t)s * a.max_pages;
+
+    // block (of the cache) that holds the tokens from t on, or -1
+    const auto block_of = [&](int t) -> int64_t {
+        if (t >= end) return -1;
+        const int page = table[t / a.c.page];
+        if (page < 0 || page >= a.c.pages) return -1;
+        return ((int64_t)page * a.c.heads + h) * per + t % a.c.page / kKvBlock;
+    };
+
+    // the row's query, in the order in which the lanes hold K
+    x8 q[KS];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        const int d = WIDE ? i / 2 * 64 + g * 16 + i % 2 * 8 : i * 32 + g * 8;
+        u32x4_t v = {0, 0, 0, 0};
+        if (real) v = *(const u32x4_t *)(a.q.p + (int64_t)(s * a.q_len + qi) * a.q.ts + qh * a.q.hs + d);
+        q[i] = __builtin_bit_cast(x8, v);
+    }
+
+    f32x4_t o[VT];
+#pragma unroll
+    for (int i = 0; i < VT; ++i) o[i] = f32x4_t{0, 0, 0, 0};
+    float m = -INFINITY, l = 0.0f;
+
+    for (int t0 = begin + wave * kTile; t0 < end; t0 += kWaves * kTile) {
+        // K: rows 4t + n%4 of block n/4
+        const int64_t kb = block_of(t0 + (n >> 2) * kKvBlock);
+        const int64_t vb = block_of(t0 + g * kKvBlock);
+        u32x2_t k[4][KS];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint8_t *p = a.c.kc + (kb * kKvBlock + t * 4 + (n & 3)) * D;
+#pragma unroll
+            for (int i = 0; i < KS; i += WIDE ? 2 : 1) {
+                if constexpr (WIDE) {
+                    u32x4_t v = {0, 0, 0, 0};
+                    if (kb >= 0) v = *(const u32x4_t *)(p + i / 2 * 64 + g * 16);
+                    k[t][i] = u32x2_t{v[0], v[1]};
+                    k[t][i + 1] = u32x2_t{v[2], v[3]};
+                } else {
+                    k[t][i] = u32x2_t{0, 0};
+                    if (kb >= 0) k[t][i] = *(const u32x2_t *)(p + i * 32 + g * 8);
+                }
+            }
+        }
+        u32x4_t v[VT];
+        int ke = 0, ve = 0;
+        if (vb >= 0) {
+            ke = a.c.ks[vb];
+            ve = a.c.vs[vb];
+        }
+#pragma unroll
+        for (int i = 0; i < VT; ++i) {
+            v[i] = u32x4_t{0, 0, 0, 0};
+            if (vb >= 0) v[i] = *(const u32x4_t *)(a.c.vc + (vb * D + i * 16 + n) * kKvBlock);
+        }
+        // tokens of this lane's block that its row sees (0 where there is no block)
+        const int sees = vb >= 0 ? see - (t0 + g * kKvBlock) : 0;
+        const float kf = block_scale(a.scale_log2e, ke);
+        float sc[16];
+        float top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f32x4_t acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+                acc = Elem<DT>::mfma16(decode8<DT>(k[t][i][0], k[t][i][1]), q[i], acc);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                sc[4 * t + r] = 4 * t + r < sees ? acc[r] * kf : -INFINITY;
+                top = fmaxf(top, sc[4 * t + r]);
+            }
+        }
+        if (a.weights && real) {
+            float *dst = (float *)((char *)a.ws + pl.scores) + ((int64_t)x * kRows + n) * pl.slots +
+                         t0 + g * kKvBlock;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                *(f32x4_t *)(dst + 4 * t) = f32x4_t{sc[4 * t], sc[4 * t + 1], sc[4 * t + 2], sc[4 * t + 3]};
+        }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float m_new = fmaxf(m, top);
+        const float base = m_new == -INFINITY ? 0.0f : m_new; // a row that has seen nothing yet
+        const float keep = __builtin_amdgcn_exp2f(m - base);
+        m = m_new;
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < VT; ++i) o[i] *= keep;
+        const float vf = block_scale(1.0f, ve);
+        float p[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float e = __builtin_amdgcn_exp2f(sc[j] - base);
+            l += e;
+            p[j] = j < sees ? e * vf : 0.0f; // a masked place adds nothing, whatever lies there
+        }
+        if (t0 + kTile > end) { // slots past the last token hold anything
+            const int c = end - (t0 + g * kKvBlock);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int b = clampi(c - 4 * w, 0, 4);
+                const uint32_t mask = b == 4 ? ~0u : (1u << (8 * b)) - 1u;
+#pragma unroll
+                for (int i = 0; i < VT; ++i) v[i][w] &= mask;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            u32x4_t ph, pr;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a0 = p[8 * u + 2 * j], a1 = p[8 * u + 2 * j + 1];
+                ph[j] = Elem<MQ_BF16>::pack(a0, a1);
+                // the rest of p, so that both parts hold it to 16 bits (half-precision outputs)
+                pr[j] = Elem<MQ_BF16>::pack(a0 - __uint_as_float(ph[j] << 16),
+                                            a1 - __uint_as_float(ph[j] & 0xFFFF0000u));
+            }
+            const bf16x8_t hi = __builtin_bit_cast(bf16x8_t, ph), lo = __builtin_bit_cast(bf16x8_t, pr);
+#pragma unroll
+            for (int i = 0; i < VT; ++i) {
+                const bf16x8_t vv = decode8<MQ_BF16>(v[i][2 * u], v[i][2 * u + 1]);
+                o[i] = Elem<MQ_BF16>::mfma16(vv, hi, o[i]);
+                if constexpr (DT == MQ_F16) o[i] = Elem<MQ_BF16>::mfma16(vv, lo, o[i]);
+            }
+        }
+    }
+    // the four lane groups hold parts of l, the waves parts of everything
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) {
+        part_m[wave][n] = m;
+        part_l[wave][n] = l;
+    }
+    __syncthreads();
+    float top = part_m[0][n];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, part_m[w][n]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const float mine = __builtin_amdgcn_exp2f(m - base);
+    if (wave) {
+#pragma unroll
+        for (int i = 0; i < VT; ++i)
+            *(f32x4_t *)&part_o[((wave - 1) * kRows + n) * LD + i * 16 + g * 4] = o[i] * mine;
+    }
+    __syncthreads();
+    if (wave) return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += part_l[w][n] * __builtin_amdgcn_exp2f(part_m[w][n] - base);
+#pragma unroll
+    for (int i = 0; i < VT; ++i) {
+        o[i] *= mine;
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w)
+            o[i] += *(const f32x4_t *)&part_o[((w - 1) * kRows + n) * LD + i * 16 + g * 4];
+    }
+    if (!real) return;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (pl.splits == 1) {
+        uint16_t *dst = a.out + (int64_t)(s * a.q_len + qi) * a.out_ts + qh * a.out_hs;
+#pragma unroll
+        for (int i = 0; i < VT; ++i)
+            *(u32x2_t *)(dst + i * 16 + g * 4) = u32x2_t{Elem<DT>::pack(o[i][0] * inv, o[i][1] * inv),
+                                                         Elem<DT>::pack(o[i][2] * inv, o[i][3] * inv)};
+        if (a.weights && g == 0)
+            ((f32x2_t *)((char *)a.ws + pl.fin))[(int64_t)x * kRows + n] = f32x2_t{base, inv};
+        return;
+    }
+    const int64_t unit = (int64_t)x * pl.splits + blockIdx.y;
+    if (g == 0) ((f32x2_t *)((char *)a.ws + pl.ml))[unit * kRows + n] = f32x2_t{top, sum};
+    float *dst = (float *)((char *)a.ws + pl.part) + (unit * kRows + n) * D;
+#pragma unroll
+    for (int i = 0; i < VT; ++i) *(f32x4_t *)(dst + i * 16 + g * 4) = o[i];
+}
+
+// Joins the parts of a row along the cache: a wave to each row, two dimensions to each lane.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(CachedArgs a, CachedPlan pl)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int n = (int)(at % kRows);
+    const int64_t x = at / kRows;
+    if (x >= (int64_t)a.n * a.c.heads * pl.row_tiles) return;
+    const int rt = (int)(x % pl.row_tiles), h = (int)(x / pl.row_tiles % a.c.heads);
+    const int s = (int)(x / pl.row_tiles / a.c.heads);
+    const int row = rt * kRows + n;
+    if (row >= pl.rows) return;
+    const int group = a.q_heads / a.c.heads, qi = row / group, qh = h * group + row % group;
+    const int len = held_tokens(a, s);
+    const int parts = len > 0 ? (len + pl.chunk - 1) / pl.chunk : 1;
+    const f32x2_t *ml = (const f32x2_t *)((const char *)a.ws + pl.ml) + x * pl.splits * kRows + n;
+    const float *po = (const float *)((const char *)a.ws + pl.part) + (x * pl.splits * kRows + n) * D;
+    float top = -INFINITY;
+    for (int i = 0; i < parts; ++i) top = fmaxf(top, ml[(int64_t)i * kRows][0]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    constexpr int N = (D / 2 + 63) / 64;
+    f32x2_t acc[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = f32x2_t{0, 0};
+    float sum = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+        const f32x2_t v = ml[(int64_t)i * kRows];
+        const float f = __builtin_amdgcn_exp2f(v[0] - base);
+        sum += v[1] * f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int pair = j * 64 + lane;
+            if (pair < D / 2) acc[j] += f * *(const f32x2_t *)(po + (int64_t)i * kRows * D + pair * 2);
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t *dst = a.out + (int64_t)(s * a.q_len + qi) * a.out_ts + qh * a.out_hs;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int pair = j * 64 + lane;
+        if (pair < D / 2) *(uint32_t *)(dst + pair * 2) = Elem<DT>::pack(acc[j][0] * inv, acc[j][1] * inv);
+    }
+    if (a.weights && lane == 0)
+        ((f32x2_t *)((char *)a.ws + pl.fin))[x * kRows + n] = f32x2_t{base, inv};
+}
+
+// Adds each token's weights, summed over the rows in order, to its place.
+__global__ void __launch_bounds__(256) attn_weights_kernel(CachedArgs a, CachedPlan pl)
+{
+    const int t = blockIdx.y * 256 + threadIdx.x;
+    const int s = blockIdx.x / a.c.heads, h = blockIdx.x % a.c.heads;
+    if (t >= held_tokens(a, s)) return;
+    const int page = a.table[(int64_t)s * a.max_pages + t / a.c.page];
+    if (page < 0 || page >= a.c.pages) return;
+    const int64_t x0 = (int64_t)blockIdx.x * pl.row_tiles;
+    const float *sc = (const float *)((const char *)a.ws + pl.scores) + x0 * kRows * pl.slots + t;
+    const f32x2_t *fin = (const f32x2_t *)((const char *)a.ws + pl.fin) + x0 * kRows;
+    float sum = 0.0f;
+    for (int r = 0; r < pl.rows; ++r) {
+        const f32x2_t f = fin[r];
+        sum += __builtin_amdgcn_exp2f(sc[(int64_t)r * pl.slots] - f[0]) * f[1];
+    }
+    a.weights[((int64_t)page * a.c.heads + h) * a.c.page + t % a.c.page] += sum;
+}
+
+template <int DT, int D>
+hipError_t cached(const CachedArgs &a, hipStream_t st)
+{
+    const CachedPlan pl = cached_plan(a.n, a.q_heads, a.c.heads, D, a.q_len, a.max_len, a.weights != nullptr);
+    const int64_t x = (int64_t)a.n * a.c.heads * pl.row_tiles;
+    if (x * kRows > INT32_MAX || pl.splits > 65535 || pl.slots / 256 > 65534) return hipErrorInvalidValue;
+    attn_cached_kernel<DT, D><<<dim3((unsigned)x, (unsigned)pl.splits), 64 * kWaves, 0, st>>>(a, pl);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    if (pl.splits > 1) {
+        attn_join_kernel<DT, D><<<(unsigned)(x * kRows / 4), 256, 0, st>>>(a, pl);
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+    }
+    if (a.weights && pl.slots) {
+        attn_weights_kernel<<<dim3((unsigned)(a.n * a.c.heads), (unsigned)((pl.slots + 255) / 256)), 256, 0, st>>>(a, pl);
+        err = hipGetLastError();
+    }
+    return err;
+}
+
+template <int DT>
+hipError_t cached_dim(const CachedArgs &a, int d, hipStream_t st)
+{
+    switch (d) {
+    case 64: return cached<DT, 64>(a, st);
+    case 96: return cached<DT, 96>(a, st);
+    case 128: return cached<DT, 128>(a, st);
+    case 192: return cached<DT, 192>(a, st);
+    case 256: return cached<DT, 256>(a, st);
+    }
+    return hipErrorInvalidValue;
+}
+
+} // namespace
+
+size_t attn_cached_workspace(int n, int q_heads, int kv_heads, int d, int q_len, int max_len,
+                             bool weights)
+{
+    return cached_plan(n, q_heads, kv_heads, d, q_len, max_len, weights).bytes;
+}
+
+hipError_t launch_attn_cached(const CachedArgs &a, int d, int dtype, hipStream_t st)
+{
+    if (a.n == 0) return hipSuccess;
+    return dtype == MQ_BF16 ? cached_dim<MQ_BF16>(a, d, st) : cached_dim<MQ_F16>(a, d, st);
+}
+
+} // namespace mq
