@@ -26,7 +26,7 @@ struct CachedPlan {
     int rows, row_tiles; // query rows of a key/value head, in tiles of kRows
     int chunk, splits;   // tokens of a workgroup, workgroups along the cache
     int slots;           // max_len up to whole tiles
-    size_t ml, part, fin, scores, bytes; // workspace offsets
+    size_t ml, part, scores, bytes; // workspace offsets
 };
 
 __host__ __device__ inline CachedPlan cached_plan(int n, int q_heads, int kv_heads, int d, int q_len, int max_len,
@@ -48,10 +48,9 @@ __host__ __device__ inline CachedPlan cached_plan(int n, int q_heads, int kv_hea
     p.slots = (int)(tiles * kTile);
     const size_t units = (size_t)x * p.splits;
     p.ml = 0;
-    p.part = p.splits > 1 ? p.ml + units * kRows * 8 : 0;
-    p.fin = p.splits > 1 ? p.part + units * kRows * d * 4 : 0;
-    p.scores = weights ? p.fin + (size_t)x * kRows * 8 : p.fin;
-    p.bytes = weights ? p.scores + (size_t)x * kRows * p.slots * 4 : p.fin;
+    p.part = p.ml + (p.splits > 1 || weights ? units * kRows * 8 : 0);
+    p.scores = p.part + (p.splits > 1 ? units * kRows * d * 4 : 0);
+    p.bytes = p.scores + (weights ? (size_t)x * kRows * p.slots * 4 : 0);
     return p;
 }
 
@@ -262,81 +261,112 @@ __global__ void __launch_bounds__(64 * kWaves) attn_cached_kernel(CachedArgs a, 
         for (int i = 0; i < VT; ++i)
             *(u32x2_t *)(dst + i * 16 + g * 4) = u32x2_t{Elem<DT>::pack(o[i][0] * inv, o[i][1] * inv),
                                                          Elem<DT>::pack(o[i][2] * inv, o[i][3] * inv)};
-        if (a.weights && g == 0)
-            ((f32x2_t *)((char *)a.ws + pl.fin))[(int64_t)x * kRows + n] = f32x2_t{base, inv};
-        return;
     }
     const int64_t unit = (int64_t)x * pl.splits + blockIdx.y;
-    if (g == 0) ((f32x2_t *)((char *)a.ws + pl.ml))[unit * kRows + n] = f32x2_t{top, sum};
+    if ((pl.splits > 1 || a.weights) && g == 0)
+        ((f32x2_t *)((char *)a.ws + pl.ml))[unit * kRows + n] = f32x2_t{top, sum};
+    if (pl.splits == 1) return;
     float *dst = (float *)((char *)a.ws + pl.part) + (unit * kRows + n) * D;
 #pragma unroll
     for (int i = 0; i < VT; ++i) *(f32x4_t *)(dst + i * 16 + g * 4) = o[i];
 }
 
-// Joins the parts of a row along the cache: a wave to each row, two dimensions to each lane.
+// What is left once every part is done, in one launch: the first workgroups join the parts of a
+// query row along the cache (kJoinThreads / (D/4) parts at a time, four dimensions to a lane),
+// the others add the weights of 256 tokens, summed over the rows in order, to their places.
+constexpr int kJoinThreads = 256;
+
 template <int DT, int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(CachedArgs a, CachedPlan pl)
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, CachedPlan pl, int join)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int n = (int)(at % kRows);
-    const int64_t x = at / kRows;
-    if (x >= (int64_t)a.n * a.c.heads * pl.row_tiles) return;
-    const int rt = (int)(x % pl.row_tiles), h = (int)(x / pl.row_tiles % a.c.heads);
-    const int s = (int)(x / pl.row_tiles / a.c.heads);
-    const int row = rt * kRows + n;
-    if (row >= pl.rows) return;
-    const int group = a.q_heads / a.c.heads, qi = row / group, qh = h * group + row % group;
+    constexpr int Q = D / 4, G = kJoinThreads / Q; // lanes of a part, parts at a time
+    __shared__ __align__(16) float acc[G][D];
+    __shared__ f32x2_t row_ml[kJoinThreads];
+    const int tid = threadIdx.x;
+    const int group = a.q_heads / a.c.heads;
+    const f32x2_t *ml = (const f32x2_t *)((const char *)a.ws + pl.ml);
+
+    if ((int)blockIdx.x >= join) { // weights
+        const int b = (int)blockIdx.x - join, per = (pl.slots + kJoinThreads - 1) / kJoinThreads;
+        const int s = b / per / a.c.heads, h = b / per % a.c.heads, first = b % per * kJoinThreads;
+        const int len = held_tokens(a, s);
+        if (first >= len) return;
+        const int parts = (len + pl.chunk - 1) / pl.chunk, t = first + tid;
+        const int64_t x0 = ((int64_t)s * a.c.heads + h) * pl.row_tiles;
+        float sum = 0.0f;
+        for (int rt = 0; rt < pl.row_tiles; ++rt) {
+            // maximum and sum of the tile's rows: 16 lanes a row, each every 16th part
+            const int r = tid / 16;
+            const f32x2_t *p = ml + (x0 + rt) * pl.splits * kRows + r;
+            float top = -INFINITY, l = 0.0f;
+            for (int i = tid % 16; i < parts; i += 16) top = fmaxf(top, p[(int64_t)i * kRows][0]);
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+            const float base = top == -INFINITY ? 0.0f : top;
+            for (int i = tid % 16; i < parts; i += 16) {
+                const f32x2_t v = p[(int64_t)i * kRows];
+                l += v[1] * __builtin_amdgcn_exp2f(v[0] - base);
+            }
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) l += __shfl_xor(l, d);
+            __syncthreads();
+            if (tid % 16 == 0) row_ml[r] = f32x2_t{base, l == 0.0f ? 0.0f : 1.0f / l};
+            __syncthreads();
+            const int rows = pl.rows - rt * kRows < kRows ? pl.rows - rt * kRows : kRows;
+            const float *sc = (const float *)((const char *)a.ws + pl.scores) +
+                              (x0 + rt) * kRows * pl.slots + t;
+            if (t < len) {
+#pragma unroll 4
+                for (int q = 0; q < rows; ++q)
+                    sum += __builtin_amdgcn_exp2f(sc[(int64_t)q * pl.slots] - row_ml[q][0]) * row_ml[q][1];
+            }
+        }
+        if (t >= len) return;
+        const int page = a.table[(int64_t)s * a.max_pages + t / a.c.page];
+        if (page < 0 || page >= a.c.pages) return;
+        a.weights[((int64_t)page * a.c.heads + h) * a.c.page + t % a.c.page] += sum;
+        return;
+    }
+
+    const int r0 = blockIdx.x % pl.rows;
+    const int64_t sh = blockIdx.x / pl.rows; // sequence and head
+    const int h = (int)(sh % a.c.heads), s = (int)(sh / a.c.heads);
+    const int qi = r0 / group, qh = h * group + r0 % group;
+    const int64_t x = sh * pl.row_tiles + r0 / kRows;
     const int len = held_tokens(a, s);
     const int parts = len > 0 ? (len + pl.chunk - 1) / pl.chunk : 1;
-    const f32x2_t *ml = (const f32x2_t *)((const char *)a.ws + pl.ml) + x * pl.splits * kRows + n;
-    const float *po = (const float *)((const char *)a.ws + pl.part) + (x * pl.splits * kRows + n) * D;
-    float top = -INFINITY;
-    for (int i = 0; i < parts; ++i) top = fmaxf(top, ml[(int64_t)i * kRows][0]);
+    ml += x * pl.splits * kRows + r0 % kRows;
+    const float *po = (const float *)((const char *)a.ws + pl.part) +
+                      (x * pl.splits * kRows + r0 % kRows) * D;
+    const int lane = tid & 63;
+    // every wave finds the row's maximum and sum for itself
+    float top = -INFINITY, l = 0.0f;
+    for (int i = lane; i < parts; i += 64) top = fmaxf(top, ml[(int64_t)i * kRows][0]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     const float base = top == -INFINITY ? 0.0f : top;
-    constexpr int N = (D / 2 + 63) / 64;
-    f32x2_t acc[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] = f32x2_t{0, 0};
-    float sum = 0.0f;
-    for (int i = 0; i < parts; ++i) {
+    for (int i = lane; i < parts; i += 64) {
         const f32x2_t v = ml[(int64_t)i * kRows];
-        const float f = __builtin_amdgcn_exp2f(v[0] - base);
-        sum += v[1] * f;
+        l += v[1] * __builtin_amdgcn_exp2f(v[0] - base);
+    }
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int pair = j * 64 + lane;
-            if (pair < D / 2) acc[j] += f * *(const f32x2_t *)(po + (int64_t)i * kRows * D + pair * 2);
-        }
+    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int g = tid / Q, c = tid % Q;
+    if (g < G) {
+        f32x4_t o = {0, 0, 0, 0};
+#pragma unroll 4
+        for (int i = g; i < parts; i += G)
+            o += *(const f32x4_t *)(po + (int64_t)i * kRows * D + c * 4) *
+                 __builtin_amdgcn_exp2f(ml[(int64_t)i * kRows][0] - base);
+        *(f32x4_t *)&acc[g][c * 4] = o;
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t *dst = a.out + (int64_t)(s * a.q_len + qi) * a.out_ts + qh * a.out_hs;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int pair = j * 64 + lane;
-        if (pair < D / 2) *(uint32_t *)(dst + pair * 2) = Elem<DT>::pack(acc[j][0] * inv, acc[j][1] * inv);
-    }
-    if (a.weights && lane == 0)
-        ((f32x2_t *)((char *)a.ws + pl.fin))[x * kRows + n] = f32x2_t{base, inv};
-}
-
-// Adds each token's weights, summed over the rows in order, to its place.
-__global__ void __launch_bounds__(256) attn_weights_kernel(CachedArgs a, CachedPlan pl)
-{
-    const int t = blockIdx.y * 256 + threadIdx.x;
-    const int s = blockIdx.x / a.c.heads, h = blockIdx.x % a.c.heads;
-    if (t >= held_tokens(a, s)) return;
-    const int page = a.table[(int64_t)s * a.max_pages + t / a.c.page];
-    if (page < 0 || page >= a.c.pages) return;
-    const int64_t x0 = (int64_t)blockIdx.x * pl.row_tiles;
-    const float *sc = (const float *)((const char *)a.ws + pl.scores) + x0 * kRows * pl.slots + t;
-    const f32x2_t *fin = (const f32x2_t *)((const char *)a.ws + pl.fin) + x0 * kRows;
-    float sum = 0.0f;
-    for (int r = 0; r < pl.rows; ++r) {
-        const f32x2_t f = fin[r];
-        sum += __builtin_amdgcn_exp2f(sc[(int64_t)r * pl.slots] - f[0]) * f[1];
-    }
-    a.weights[((int64_t)page * a.c.heads + h) * a.c.page + t % a.c.page] += sum;
+    __syncthreads();
+    if (tid >= Q) return;
+    f32x4_t o = {0, 0, 0, 0};
+    for (int i = 0; i < G && i < parts; ++i) o += *(const f32x4_t *)&acc[i][tid * 4];
+    uint16_t *dst = a.out + (int64_t)(s * a.q_len + qi) * a.out_ts + qh * a.out_hs + tid * 4;
+    *(u32x2_t *)dst = u32x2_t{Elem<DT>::pack(o[0] * inv, o[1] * inv), Elem<DT>::pack(o[2] * inv, o[3] * inv)};
 }
 
 template <int DT, int D>
@@ -344,19 +374,16 @@ hipError_t cached(const CachedArgs &a, hipStream_t st)
 {
     const CachedPlan pl = cached_plan(a.n, a.q_heads, a.c.heads, D, a.q_len, a.max_len, a.weights != nullptr);
     const int64_t x = (int64_t)a.n * a.c.heads * pl.row_tiles;
-    if (x * kRows > INT32_MAX || pl.splits > 65535 || pl.slots / 256 > 65534) return hipErrorInvalidValue;
+    if (x * kRows > INT32_MAX || pl.splits > 65535 || pl.splits < 1) return hipErrorInvalidValue;
     attn_cached_kernel<DT, D><<<dim3((unsigned)x, (unsigned)pl.splits), 64 * kWaves, 0, st>>>(a, pl);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    if (pl.splits > 1) {
-        attn_join_kernel<DT, D><<<(unsigned)(x * kRows / 4), 256, 0, st>>>(a, pl);
-        if ((err = hipGetLastError()) != hipSuccess) return err;
-    }
-    if (a.weights && pl.slots) {
-        attn_weights_kernel<<<dim3((unsigned)(a.n * a.c.heads), (unsigned)((pl.slots + 255) / 256)), 256, 0, st>>>(a, pl);
-        err = hipGetLastError();
-    }
-    return err;
+    const int64_t join = pl.splits > 1 ? (int64_t)a.n * a.c.heads * pl.rows : 0;
+    const int64_t add = a.weights ? (int64_t)a.n * a.c.heads * ((pl.slots + kJoinThreads - 1) / kJoinThreads) : 0;
+    if (join + add > INT32_MAX) return hipErrorInvalidValue;
+    if (join + add == 0) return hipSuccess;
+    attn_join_kernel<DT, D><<<(unsigned)(join + add), kJoinThreads, 0, st>>>(a, pl, (int)join);
+    return hipGetLastError();
 }
 
 template <int DT>

@@ -198,32 +198,30 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-constexpr int kSelWaves = 16;
+constexpr int kSelWaves = 16, kSelKeys = 32, kSelBins = 2048;
 
-// One workgroup per sequence and head finds the kept tokens: the key of rank m among the
-// candidates by four 8-bit digits (histograms in LDS, one copy per wave), then two passes over
-// the tokens in order, each wave a contiguous stretch: counts, a sum over the waves, and the kept
-// positions written where they belong.
+// One workgroup per sequence and head finds the kept tokens. Each wave owns a contiguous stretch
+// of the candidates and reads their weights once; up to kSelKeys keys a lane (32768 tokens a
+// workgroup) stay in registers, the rest of a longer sequence is read again from the caches. The
+// key of rank `need` is found by three 11-bit digits of its distance from the smallest key,
+// shifted so that the largest distance just fits: the weights' exponents, nearly equal, then
+// spread over the bins instead of meeting in a few. Two more passes over the keys count what each
+// wave keeps and write it where it belongs.
 __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
 {
-    __shared__ uint32_t hist[kSelWaves][256];
-    __shared__ uint32_t pick[2]; // digit, rank within it
+    __shared__ uint32_t hist[kSelBins];
     __shared__ uint32_t part[kSelWaves][2];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ uint32_t pick[2]; // digit, rank within it
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int s = blockIdx.x / a.c.heads, h = blockIdx.x % a.c.heads;
     const int len = clampi(a.lens[s], 0, capacity(a.max_pages, a.c.page));
     const int take = len < a.keep ? len : a.keep;
     const int safe = a.recent < take ? a.recent : take;
     const int cand = len - safe; // tokens that compete
-    uint32_t need = take - safe; // how many of them stay
+    const uint32_t need = take - safe; // how many of them stay
     int32_t *kept = a.kept + (int64_t)blockIdx.x * a.keep;
     const int32_t *table = a.table + (int64_t)s * a.max_pages;
     if (h == 0 && tid == 0) a.new_lens[s] = take;
-    const auto key_of = [&](int t) -> uint32_t {
-        const int page = table[t / a.c.page];
-        if (page < 0 || page >= a.c.pages) return 0;
-        return weight_key(a.weights[((int64_t)page * a.c.heads + h) * a.c.page + t % a.c.page]);
-    };
     for (int i = take + tid; i < a.keep; i += blockDim.x) kept[i] = -1;
     for (int i = tid; i < safe; i += blockDim.x) kept[need + i] = cand + i;
     if (need == 0) return;
@@ -231,24 +229,60 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
         for (int i = tid; i < cand; i += blockDim.x) kept[i] = i;
         return;
     }
-    // the key `bound` that the token of rank need (from the largest) has; `ties` of its equals stay
-    uint32_t bound = 0, mask = 0, ties = need;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < kSelWaves * 256; i += blockDim.x) (&hist[0][0])[i] = 0;
-        __syncthreads();
-        for (int t = tid; t < cand; t += blockDim.x) {
-            const uint32_t k = key_of(t);
-            if ((k & mask) == bound) atomicAdd(&hist[wave][(k >> shift) & 255u], 1u);
-        }
-        __syncthreads();
-        if (wave == 0) { // digits 4*lane .. 4*lane+3, from the largest lane down
-            uint32_t c[4], sum = 0;
+    const int stretch = ((cand + kSelWaves - 1) / kSelWaves + 63) & ~63;
+    const int from = wave * stretch, to = from + stretch < cand ? from + stretch : cand;
+    const auto key_of = [&](int t) -> uint32_t {
+        const int page = table[t / a.c.page];
+        if (page < 0 || page >= a.c.pages) return 0;
+        return weight_key(a.weights[((int64_t)page * a.c.heads + h) * a.c.page + t % a.c.page]);
+    };
+    uint32_t keys[kSelKeys];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                c[j] = 0;
-                for (int w = 0; w < kSelWaves; ++w) c[j] += hist[w][lane * 4 + j];
-                sum += c[j];
-            }
+    for (int j = 0; j < kSelKeys; ++j) {
+        const int t = from + j * 64 + lane;
+        keys[j] = t < to ? key_of(t) : 0;
+    }
+    // f(key, first token of the wave's 64, whether this lane has one), over the wave's stretch
+    const auto each = [&](auto f) {
+#pragma unroll
+        for (int j = 0; j < kSelKeys; ++j)
+            if (from + j * 64 < to) f(keys[j], from + j * 64, from + j * 64 + lane < to);
+        for (int t = from + kSelKeys * 64; t < to; t += 64)
+            f(t + lane < to ? key_of(t + lane) : 0, t, t + lane < to);
+    };
+    // smallest and largest key
+    uint32_t lo = ~0u, hi = 0;
+    each([&](uint32_t k, int, bool live) {
+        if (live && k < lo) lo = k;
+        if (live && k > hi) hi = k;
+    });
+    lo = ~wave_max(~lo);
+    hi = wave_max(hi);
+    if (lane == 0) {
+        part[wave][0] = lo;
+        part[wave][1] = hi;
+    }
+    __syncthreads();
+    for (int w = 0; w < kSelWaves; ++w) {
+        lo = part[w][0] < lo ? part[w][0] : lo;
+        hi = part[w][1] > hi ? part[w][1] : hi;
+    }
+    // `bound`, the distance from lo that the token of rank need (from the largest) has; `ties` of
+    // its equals stay
+    uint32_t bound = 0, ties = need;
+    int top = 32 - __builtin_clz((hi - lo) | 1u); // bits not yet decided
+    while (top > 0) {
+        const int shift = top > 11 ? top - 11 : 0;
+        for (int i = tid; i < kSelBins; i += blockDim.x) hist[i] = 0;
+        __syncthreads();
+        each([&](uint32_t k, int, bool live) {
+            const uint32_t d = (k - lo) ^ bound; // decided bits equal: below 2^top
+            if (live && (top >= 32 || d >> top == 0)) atomicAdd(&hist[d >> shift], 1u);
+        });
+        __syncthreads();
+        if (wave == 0) { // 32 bins a lane, from the largest lane down
+            uint32_t sum = 0;
+            for (int j = 0; j < kSelBins / 64; ++j) sum += hist[lane * (kSelBins / 64) + j];
             uint32_t above = sum; // sum over this lane and those above it
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
@@ -257,32 +291,24 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
             }
             above -= sum;
             if (above < ties && above + sum >= ties) { // exactly one lane
-#pragma unroll
-                for (int j = 3; j >= 0; --j) {
-                    if (above < ties && above + c[j] >= ties) {
-                        pick[0] = lane * 4 + j;
-                        pick[1] = ties - above;
-                        break;
-                    }
-                    above += c[j];
-                }
+                int j = kSelBins / 64 - 1;
+                for (uint32_t c; above + (c = hist[lane * (kSelBins / 64) + j]) < ties; --j) above += c;
+                pick[0] = lane * (kSelBins / 64) + j;
+                pick[1] = ties - above;
             }
         }
         __syncthreads();
         bound |= pick[0] << shift;
         ties = pick[1];
-        mask |= 255u << shift;
+        top = shift;
         __syncthreads();
     }
-    // each wave's stretch of the candidates, a multiple of 64
-    const int stretch = ((cand + kSelWaves - 1) / kSelWaves + 63) & ~63;
-    const int from = wave * stretch, to = from + stretch < cand ? from + stretch : cand;
+    bound += lo;
     uint32_t over = 0, same = 0;
-    for (int t = from + lane; t - lane < to; t += 64) {
-        const uint32_t k = t < to ? key_of(t) : 0;
-        over += __popcll(__ballot(t < to && k > bound));
-        same += __popcll(__ballot(t < to && k == bound));
-    }
+    each([&](uint32_t k, int, bool live) {
+        over += __popcll(__ballot(live && k > bound));
+        same += __popcll(__ballot(live && k == bound));
+    });
     if (lane == 0) {
         part[wave][0] = over;
         part[wave][1] = same;
@@ -294,16 +320,15 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
         same += part[w][1];
     }
     const uint64_t below = ((uint64_t)1 << lane) - 1;
-    for (int t = from + lane; t - lane < to; t += 64) {
-        const uint32_t k = t < to ? key_of(t) : 0;
-        const uint64_t bo = __ballot(t < to && k > bound), bs = __ballot(t < to && k == bound);
+    each([&](uint32_t k, int t, bool live) {
+        const uint64_t bo = __ballot(live && k > bound), bs = __ballot(live && k == bound);
         const uint32_t so = over + __popcll(bo & below), ss = same + __popcll(bs & below);
         // equals that came before take the first places among the equals that stay
         const bool stays = (bo >> lane & 1) || ((bs >> lane & 1) && ss < ties);
-        if (stays) kept[so + (ss < ties ? ss : ties)] = t;
+        if (stays) kept[so + (ss < ties ? ss : ties)] = t + lane;
         over += __popcll(bo);
         same += __popcll(bs);
-    }
+    });
 }
 
 // One wave per new block, head and side: copies the 16 kept tokens at the largest of their
@@ -372,40 +397,58 @@ __global__ void __launch_bounds__(256) kv_move_kernel(EvictArgs a, int blocks)
         }
         return;
     }
+    // Values: a lane holds two dimensions, 16 bytes a block each. The kept tokens ascend, so those
+    // of one old block come together: each old block is loaded once, the next one while the
+    // tokens of this one move byte by byte (v_perm_b32, under uniform selectors).
     constexpr int N = (D / 2 + 63) / 64;
+    const uint32_t starts = (uint32_t)__ballot(lane < hi && from >= 0 && (lane == 0 || from != __shfl(from, lane ? lane - 1 : 0)));
+    const bool plain = !__any(lane < hi && by != 0) && e != 255;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int pair = i * 64 + lane;
         if (pair >= D / 2) continue;
-        uint32_t b0[kKvBlock], b1[kKvBlock];
+        const auto load = [&](int t, u32x4_t *x) {
+            const int64_t f = (int64_t)((uint32_t)__builtin_amdgcn_readlane((int)from, t)) |
+                              (int64_t)__builtin_amdgcn_readlane((int)(from >> 32), t) << 32;
+            const u32x4_t *p = (const u32x4_t *)(all + (f * D + pair * 2) * kKvBlock);
+            x[0] = p[0];
+            x[1] = p[1];
+        };
+        u32x4_t cur[2] = {}, next[2] = {}, out[2] = {};
+        if (starts) load(__builtin_ctz(starts), next);
 #pragma unroll
         for (int t = 0; t < kKvBlock; ++t) {
-            const int64_t f = (int64_t)__builtin_amdgcn_readlane((int)from, t) & 0xffffffffll |
-                              (int64_t)__builtin_amdgcn_readlane((int)(from >> 32), t) << 32;
+            if (starts >> t & 1) {
+                cur[0] = next[0];
+                cur[1] = next[1];
+                const uint32_t rest = starts & ~((2u << t) - 1);
+                if (rest) load(__builtin_ctz(rest), next);
+            }
+            if (t >= hi || __builtin_amdgcn_readlane((int)(from >> 32), t) < 0) continue; // 0
             const int sl = __builtin_amdgcn_readlane(slot, t);
-            b0[t] = b1[t] = 0;
-            if (f >= 0) {
-                const uint8_t *p = all + (f * D + pair * 2) * kKvBlock + sl;
-                b0[t] = p[0];
-                b1[t] = p[kKvBlock];
+            // byte sl%4 of the source word into byte t%4 of the result, the others as they are
+            const uint32_t sel = (0x03020100u & ~(0xFFu << (8 * (t % 4)))) |
+                                 (uint32_t)(4 + sl % 4) << (8 * (t % 4));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t w = sl < 8 ? (sl < 4 ? cur[k][0] : cur[k][1]) : (sl < 12 ? cur[k][2] : cur[k][3]);
+                out[k][t / 4] = __builtin_amdgcn_perm(w, out[k][t / 4], sel);
             }
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            u32x4_t out;
+            if (!plain) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                float v[4];
+                for (int w = 0; w < 4; ++w) {
+                    float v[4];
+                    decode4(out[k][w], v);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = 4 * w + j;
-                    v[j] = __builtin_amdgcn_cvt_f32_fp8((int)(k ? b1[t] : b0[t]), 0);
-                    v[j] = __builtin_amdgcn_ldexpf(v[j], __builtin_amdgcn_readlane(by, t));
-                    if (e == 255) v[j] = 0.0f;
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = e == 255 ? 0.0f : __builtin_amdgcn_ldexpf(v[j], __builtin_amdgcn_readlane(by, 4 * w + j));
+                    out[k][w] = encode4(v[0], v[1], v[2], v[3]);
                 }
-                out[w] = encode4(v[0], v[1], v[2], v[3]);
             }
-            *(u32x4_t *)(all + (blk * D + pair * 2 + k) * kKvBlock) = out;
+            *(u32x4_t *)(all + (blk * D + pair * 2 + k) * kKvBlock) = out[k];
         }
     }
 }
