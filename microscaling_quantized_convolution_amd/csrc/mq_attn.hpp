@@ -13,10 +13,14 @@ constexpr int kKvBlock = MQ_KV_BLOCK; // tokens per scale
 constexpr int kScaleMin = 10;         // smallest scale byte written: the step of the smallest
                                       // codes, 2^-9 * 2^(10-127), is the smallest normal fp32
 
-// A paged cache (mq_kv_cache; head_dim is a template parameter of the kernels).
+// A paged cache (mq_kv_cache; head_dim is a template parameter of the kernels). A position t is
+// divided by the page size as t * page_mul >> (31 + page_shift): with s = ceil(log2 page) and
+// mul = floor(2^(31+s) / page) + 1, mul * page exceeds 2^(31+s) by at most page <= 2^s, so the
+// quotient is exact for every t < 2^31.
 struct KvView {
     uint8_t *kc, *vc, *ks, *vs;
     int pages, page, heads;
+    uint32_t page_mul, page_shift;
 };
 
 // Token vectors (mq_rows; strides in elements).

@@ -33,7 +33,11 @@ bool ints_ok(const int32_t *p, int64_t n) { return n == 0 || (p && aligned(p, 4)
 
 mq::KvView view(const mq_kv_cache *c)
 {
-    return {c->k_codes, c->v_codes, c->k_scales, c->v_scales, c->num_pages, c->page_size, c->kv_heads};
+    uint32_t shift = 0;
+    while (((int64_t)1 << shift) < c->page_size) ++shift;
+    const uint64_t mul = ((uint64_t)1 << (31 + shift)) / (uint32_t)c->page_size + 1;
+    return {c->k_codes, c->v_codes, c->k_scales, c->v_scales, c->num_pages, c->page_size,
+            c->kv_heads, (uint32_t)mul, shift};
 }
 
 mq::RowsView view(const mq_rows *r)

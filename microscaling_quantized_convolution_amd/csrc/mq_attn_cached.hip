@@ -100,9 +100,9 @@ __global__ void __launch_bounds__(64 * kWaves) attn_cached_kernel(CachedArgs a, 
     // block (of the cache) that holds the tokens from t on, or -1
     const auto block_of = [&](int t) -> int64_t {
         if (t >= end) return -1;
-        const int page = table[t / a.c.page];
+        const int pi = page_of(a.c, t), page = table[pi];
         if (page < 0 || page >= a.c.pages) return -1;
-        return ((int64_t)page * a.c.heads + h) * per + t % a.c.page / kKvBlock;
+        return ((int64_t)page * a.c.heads + h) * per + slot_of(a.c, t, pi) / kKvBlock;
     };
 
     // the row's query, in the order in which the lanes hold K
@@ -322,9 +322,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
             }
         }
         if (t >= len) return;
-        const int page = a.table[(int64_t)s * a.max_pages + t / a.c.page];
+        const int pi = page_of(a.c, t), page = a.table[(int64_t)s * a.max_pages + pi];
         if (page < 0 || page >= a.c.pages) return;
-        a.weights[((int64_t)page * a.c.heads + h) * a.c.page + t % a.c.page] += sum;
+        a.weights[((int64_t)page * a.c.heads + h) * a.c.page + slot_of(a.c, t, pi)] += sum;
         return;
     }
 

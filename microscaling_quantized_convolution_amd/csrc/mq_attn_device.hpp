@@ -72,6 +72,45 @@ __device__ __forceinline__ typename Elem<DT>::x8 decode8(uint32_t w0, uint32_t w
     return __builtin_bit_cast(typename Elem<DT>::x8, v);
 }
 
+// Page of a table's row that holds position t >= 0, and the slot in it.
+__device__ __forceinline__ int page_of(const KvView &c, int t)
+{
+    return (int)((uint64_t)(uint32_t)t * c.page_mul >> (31 + c.page_shift));
+}
+__device__ __forceinline__ int slot_of(const KvView &c, int t, int page) { return t - page * c.page; }
+
+// Inclusive prefix sum over the wave's lanes (data-parallel moves within rows of 16 lanes, then
+// the rows' last lanes to the rows behind them).
+__device__ __forceinline__ int wave_prefix(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false); // 1 lane up within a row
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false); // lane 15 of a row to the next
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false); // lane 31 to the upper half
+    return v;
+}
+
+// Largest unsigned value of the wave, uniform.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    const auto step = [&](uint32_t o) { v = o > v ? o : v; };
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Set bits of a lane mask below this lane.
+__device__ __forceinline__ uint32_t bits_below(uint64_t m)
+{
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
 // Where unit `unit` lies when sequences 0..n-1 own count(s) >= 0 units each, in order: false if
 // it is past the last. The wave searches together, 64 sequences a step (one load each, a prefix
 // sum over the lanes), so ragged batches need no table from the host. The result is uniform.
@@ -81,12 +120,7 @@ __device__ __forceinline__ bool locate_unit(int unit, int n, Count count, int *s
     const int lane = threadIdx.x & 63;
     for (int base = 0; base < n; base += 64) {
         const int c = base + lane < n ? count(base + lane) : 0;
-        int incl = c;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(incl, d);
-            if (lane >= d) incl += up;
-        }
+        const int incl = wave_prefix(c);
         const uint64_t past = __ballot(incl > unit);
         if (past) {
             const int f = __builtin_ctzll(past);

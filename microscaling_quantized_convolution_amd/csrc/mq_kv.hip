@@ -6,6 +6,8 @@
 // read and written, so no two waves share a byte.
 #include "mq_attn_device.hpp"
 
+#include <type_traits>
+
 namespace mq {
 namespace {
 
@@ -14,6 +16,16 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
 {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
+// Four half-precision values of magnitude 448 or less as codes.
+__device__ __forceinline__ uint32_t encode4h(f16x2_t a, f16x2_t b)
+{
+    typedef __attribute__((ext_vector_type(2))) short s16x2_t;
+    s16x2_t w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, a, 1.0f, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, b, 1.0f, true);
+    return __builtin_bit_cast(uint32_t, w);
 }
 
 // The four values of a word of codes.
@@ -30,16 +42,6 @@ __device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b)
     typedef __attribute__((ext_vector_type(2))) uint16_t u16x2_t;
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
                                                                   __builtin_bit_cast(u16x2_t, b)));
-}
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
-{
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const uint32_t o = __shfl_xor(v, d);
-        v = o > v ? o : v;
-    }
-    return v;
 }
 
 // Scale byte of a block whose largest magnitude has the fp32 bits `b`: the smallest power of two
@@ -89,11 +91,11 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
     const int start = (held / kKvBlock + index) * kKvBlock; // the block's first token
     const int lo = clampi(held - start, 0, kKvBlock);
     const int hi = held + count - start < kKvBlock ? held + count - start : kKvBlock;
-    const int page = a.table[(int64_t)s * a.max_pages + start / a.c.page];
+    const int pi = page_of(a.c, start), page = a.table[(int64_t)s * a.max_pages + pi];
     if (page < 0 || page >= a.c.pages) return;
     const int h = job >> 1, side = job & 1;
     const int64_t blk = ((int64_t)page * a.c.heads + h) * (a.c.page / kKvBlock) +
-                        start % a.c.page / kKvBlock;
+                        slot_of(a.c, start, pi) / kKvBlock;
     const RowsView &src = side ? a.v : a.k;
     const uint16_t *rows = src.p + (int64_t)(first_of(s) - held + start) * src.ts + h * src.hs;
     uint8_t *codes = (side ? a.c.vc : a.c.kc) + blk * (kKvBlock * D);
@@ -198,17 +200,24 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-constexpr int kSelWaves = 16, kSelKeys = 32, kSelBins = 2048;
+constexpr int kSelWaves = 16, kSelSteps = 8, kSelBins = 2 * 64 * kSelWaves;
+constexpr int kSelStep = 256; // tokens a wave takes at a time, four neighbours to a lane
+
+typedef float f32x4_dword_t __attribute__((ext_vector_type(4), aligned(4)));
 
 // One workgroup per sequence and head finds the kept tokens. Each wave owns a contiguous stretch
-// of the candidates and reads their weights once; up to kSelKeys keys a lane (32768 tokens a
-// workgroup) stay in registers, the rest of a longer sequence is read again from the caches. The
-// key of rank `need` is found by three 11-bit digits of its distance from the smallest key,
-// shifted so that the largest distance just fits: the weights' exponents, nearly equal, then
-// spread over the bins instead of meeting in a few. Two more passes over the keys count what each
-// wave keeps and write it where it belongs.
+// of the candidates and reads their weights once, 16 bytes to a lane and all of them on their way
+// together; up to kSelSteps steps a wave (32768 tokens a workgroup) stay in LDS as keys, the rest
+// of a longer sequence is read again from the caches. The key of rank `need` is found by 11-bit
+// digits of its distance from the smallest key, shifted so that the largest distance just fits:
+// the weights' exponents, nearly equal, then spread over the bins instead of meeting in a few.
+// Two more passes over the keys count what each wave keeps and write it where it belongs. Bound
+// by the latency of these passes (the weights are 4 bytes a token): 32768 tokens took 110 us with
+// 8-bit digits of the keys read again in each pass, 57 us with keys in LDS but loaded one after
+// another.
 __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
 {
+    __shared__ __align__(16) uint32_t held[kSelWaves][kSelSteps * kSelStep];
     __shared__ uint32_t hist[kSelBins];
     __shared__ uint32_t part[kSelWaves][2];
     __shared__ uint32_t pick[2]; // digit, rank within it
@@ -229,33 +238,57 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
         for (int i = tid; i < cand; i += blockDim.x) kept[i] = i;
         return;
     }
-    const int stretch = ((cand + kSelWaves - 1) / kSelWaves + 63) & ~63;
+    const int stretch = ((cand + kSelWaves - 1) / kSelWaves + kSelStep - 1) / kSelStep * kSelStep;
     const int from = wave * stretch, to = from + stretch < cand ? from + stretch : cand;
-    const auto key_of = [&](int t) -> uint32_t {
-        const int page = table[t / a.c.page];
-        if (page < 0 || page >= a.c.pages) return 0;
-        return weight_key(a.weights[((int64_t)page * a.c.heads + h) * a.c.page + t % a.c.page]);
+    // weights of a lane's four tokens from t on (a multiple of 4: one block), NaN past the end
+    // or where there is no page
+    const auto weights_at = [&](int t) -> f32x4_t {
+        const float nan = __builtin_nanf("");
+        if (t >= to) return f32x4_t{nan, nan, nan, nan};
+        const int pi = page_of(a.c, t), page = table[pi];
+        if (page < 0 || page >= a.c.pages) return f32x4_t{nan, nan, nan, nan};
+        return *(const f32x4_dword_t *)(a.weights + ((int64_t)page * a.c.heads + h) * a.c.page + slot_of(a.c, t, pi));
     };
-    uint32_t keys[kSelKeys];
-#pragma unroll
-    for (int j = 0; j < kSelKeys; ++j) {
-        const int t = from + j * 64 + lane;
-        keys[j] = t < to ? key_of(t) : 0;
-    }
-    // f(key, first token of the wave's 64, whether this lane has one), over the wave's stretch
+    const auto keys_of = [&](f32x4_t w) {
+        return u32x4_t{weight_key(w[0]), weight_key(w[1]), weight_key(w[2]), weight_key(w[3])};
+    };
+    // f(keys of the lane's four tokens, the first of them, whether all of the wave's exist), over
+    // the wave's stretch
     const auto each = [&](auto f) {
-#pragma unroll
-        for (int j = 0; j < kSelKeys; ++j)
-            if (from + j * 64 < to) f(keys[j], from + j * 64, from + j * 64 + lane < to);
-        for (int t = from + kSelKeys * 64; t < to; t += 64)
-            f(t + lane < to ? key_of(t + lane) : 0, t, t + lane < to);
+        int t = from;
+        const auto one = [&](u32x4_t k) {
+            if (t + kSelStep <= to)
+                f(k, t + lane * 4, std::true_type());
+            else
+                f(k, t + lane * 4, std::false_type());
+        };
+        for (int i = 0; i < kSelSteps && t < to; ++i, t += kSelStep)
+            one(*(const u32x4_t *)&held[wave][t - from + lane * 4]);
+        for (; t < to; t += kSelStep) one(keys_of(weights_at(t + lane * 4)));
     };
     // smallest and largest key
     uint32_t lo = ~0u, hi = 0;
-    each([&](uint32_t k, int, bool live) {
-        if (live && k < lo) lo = k;
-        if (live && k > hi) hi = k;
-    });
+    const auto range = [&](u32x4_t k, int t) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (t + q < to && k[q] < lo) lo = k[q];
+            if (t + q < to && k[q] > hi) hi = k[q];
+        }
+    };
+    {
+        f32x4_t w[kSelSteps];
+#pragma unroll
+        for (int i = 0; i < kSelSteps; ++i) w[i] = weights_at(from + i * kSelStep + lane * 4);
+#pragma unroll
+        for (int i = 0; i < kSelSteps; ++i) {
+            if (from + i * kSelStep >= to) break;
+            const u32x4_t k = keys_of(w[i]);
+            *(u32x4_t *)&held[wave][i * kSelStep + lane * 4] = k;
+            range(k, from + i * kSelStep + lane * 4);
+        }
+        for (int t = from + kSelSteps * kSelStep + lane * 4; t < to; t += kSelStep)
+            range(keys_of(weights_at(t)), t);
+    }
     lo = ~wave_max(~lo);
     hi = wave_max(hi);
     if (lane == 0) {
@@ -263,192 +296,250 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
         part[wave][1] = hi;
     }
     __syncthreads();
-    for (int w = 0; w < kSelWaves; ++w) {
-        lo = part[w][0] < lo ? part[w][0] : lo;
-        hi = part[w][1] > hi ? part[w][1] : hi;
-    }
+    // every wave gathers the waves' parts on its lanes
+    const int peer = lane % kSelWaves;
+    lo = ~wave_max(~part[peer][0]);
+    hi = wave_max(part[peer][1]);
     // `bound`, the distance from lo that the token of rank need (from the largest) has; `ties` of
     // its equals stay
     uint32_t bound = 0, ties = need;
     int top = 32 - __builtin_clz((hi - lo) | 1u); // bits not yet decided
     while (top > 0) {
         const int shift = top > 11 ? top - 11 : 0;
-        for (int i = tid; i < kSelBins; i += blockDim.x) hist[i] = 0;
+        hist[tid] = hist[tid + kSelBins / 2] = 0;
         __syncthreads();
-        each([&](uint32_t k, int, bool live) {
-            const uint32_t d = (k - lo) ^ bound; // decided bits equal: below 2^top
-            if (live && (top >= 32 || d >> top == 0)) atomicAdd(&hist[d >> shift], 1u);
+        each([&](u32x4_t k, int t, auto full) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t d = (k[q] - lo) ^ bound; // decided bits equal: below 2^top
+                if ((full || t + q < to) && (top >= 32 || d >> top == 0)) atomicAdd(&hist[d >> shift], 1u);
+            }
         });
         __syncthreads();
-        if (wave == 0) { // 32 bins a lane, from the largest lane down
-            uint32_t sum = 0;
-            for (int j = 0; j < kSelBins / 64; ++j) sum += hist[lane * (kSelBins / 64) + j];
-            uint32_t above = sum; // sum over this lane and those above it
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint32_t o = __shfl_down(above, d);
-                if (lane + d < 64) above += o;
-            }
-            above -= sum;
-            if (above < ties && above + sum >= ties) { // exactly one lane
-                int j = kSelBins / 64 - 1;
-                for (uint32_t c; above + (c = hist[lane * (kSelBins / 64) + j]) < ties; --j) above += c;
-                pick[0] = lane * (kSelBins / 64) + j;
-                pick[1] = ties - above;
-            }
+        // two bins a lane, summed from the largest down: over the wave, then over the waves
+        const uint32_t c0 = hist[2 * tid], c1 = hist[2 * tid + 1];
+        const uint32_t upto = wave_prefix(c0 + c1);
+        if (lane == 63) part[wave][0] = upto;
+        __syncthreads();
+        const uint32_t sums = wave_prefix(lane < kSelWaves ? part[lane][0] : 0); // up to each wave
+        // tokens above each bin
+        const uint32_t over1 = __builtin_amdgcn_readlane(sums, 63) - __builtin_amdgcn_readlane(sums, wave) +
+                               __builtin_amdgcn_readlane(upto, 63) - upto;
+        const uint32_t over0 = over1 + c1;
+        if (over1 < ties && over1 + c1 >= ties) {
+            pick[0] = 2 * tid + 1;
+            pick[1] = ties - over1;
+        }
+        if (over0 < ties && over0 + c0 >= ties) {
+            pick[0] = 2 * tid;
+            pick[1] = ties - over0;
         }
         __syncthreads();
         bound |= pick[0] << shift;
         ties = pick[1];
         top = shift;
-        __syncthreads();
     }
     bound += lo;
     uint32_t over = 0, same = 0;
-    each([&](uint32_t k, int, bool live) {
-        over += __popcll(__ballot(live && k > bound));
-        same += __popcll(__ballot(live && k == bound));
+    each([&](u32x4_t k, int t, auto full) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            over += __popcll(__ballot((full || t + q < to) && k[q] > bound));
+            same += __popcll(__ballot((full || t + q < to) && k[q] == bound));
+        }
     });
-    if (lane == 0) {
+    if (lane == 0) { // the last reads of part[][0] lie before the loop's last barrier
         part[wave][0] = over;
         part[wave][1] = same;
     }
     __syncthreads();
-    over = same = 0;
-    for (int w = 0; w < wave; ++w) {
-        over += part[w][0];
-        same += part[w][1];
+    {
+        const uint32_t o = wave_prefix(lane < wave ? part[peer][0] : 0);
+        const uint32_t e = wave_prefix(lane < wave ? part[peer][1] : 0);
+        over = __builtin_amdgcn_readlane(o, 63);
+        same = __builtin_amdgcn_readlane(e, 63);
     }
-    const uint64_t below = ((uint64_t)1 << lane) - 1;
-    each([&](uint32_t k, int t, bool live) {
-        const uint64_t bo = __ballot(live && k > bound), bs = __ballot(live && k == bound);
-        const uint32_t so = over + __popcll(bo & below), ss = same + __popcll(bs & below);
-        // equals that came before take the first places among the equals that stay
-        const bool stays = (bo >> lane & 1) || ((bs >> lane & 1) && ss < ties);
-        if (stays) kept[so + (ss < ties ? ss : ties)] = t + lane;
-        over += __popcll(bo);
-        same += __popcll(bs);
+    each([&](u32x4_t k, int t, auto full) {
+        uint32_t so = over, ss = same; // before the lane's first token
+        bool is_over[4], is_same[4];
+        uint64_t any_same = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            is_over[q] = (full || t + q < to) && k[q] > bound;
+            is_same[q] = (full || t + q < to) && k[q] == bound;
+            const uint64_t bo = __ballot(is_over[q]);
+            so += bits_below(bo);
+            over += __popcll(bo);
+            any_same |= __ballot(is_same[q]);
+        }
+        if (any_same) { // rare: the equals of the bound
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint64_t bs = __ballot(is_same[q]);
+                ss += bits_below(bs);
+                same += __popcll(bs);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            // equals that came before take the first places among the equals that stay
+            const uint32_t at = so + (ss < ties ? ss : ties); // below need, if the weights hold still
+            if ((is_over[q] || (is_same[q] && ss < ties)) && at < need) kept[at] = t + q;
+            so += is_over[q];
+            ss += is_same[q];
+        }
     });
 }
 
-// One wave per new block, head and side: copies the 16 kept tokens at the largest of their
-// scales, and (the wave of the keys) their weights.
+// One wave per new block and head: copies the keys and values of 16 kept tokens at the largest
+// of their scales, and their weights. Bound by the bytes: a kept token's key is one row, but its
+// value lies with the 15 others of its old block, which comes whole.
 template <int D>
 __global__ void __launch_bounds__(256) kv_move_kernel(EvictArgs a, int blocks)
 {
+    constexpr int KC = (D + 63) / 64;          // 16-byte pieces of keys to a lane
+    constexpr int VC = (D / 2 + 63) / 64;      // pairs of dimensions of values to a lane
     const int lane = threadIdx.x & 63;
-    const int job = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (job >= 2 * a.c.heads) return;
-    const int h = job >> 1, side = job & 1;
+    const int h = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (h >= a.c.heads) return;
     const int s = blockIdx.x / blocks, start = blockIdx.x % blocks * kKvBlock;
+    const int pn = page_of(a.c, start);
+    const int to = a.new_table[(int64_t)s * a.new_max_pages + pn];
+    int t = -1; // lane i < 16: the i-th token's old position
+    if (lane < kKvBlock && start + lane < a.keep) t = a.kept[((int64_t)s * a.c.heads + h) * a.keep + start + lane];
     const int len = clampi(a.lens[s], 0, capacity(a.max_pages, a.c.page));
     const int take = len < a.keep ? len : a.keep;
-    if (start >= take) return;
+    if (start >= take || to < 0 || to >= a.c.pages) return;
     const int hi = take - start < kKvBlock ? take - start : kKvBlock;
-    const int to = a.new_table[(int64_t)s * a.new_max_pages + start / a.c.page];
-    if (to < 0 || to >= a.c.pages) return;
     const int per = a.c.page / kKvBlock;
-    const int64_t blk = ((int64_t)to * a.c.heads + h) * per + start % a.c.page / kKvBlock;
-    uint8_t *scales = side ? a.c.vs : a.c.ks;
-    uint8_t *all = side ? a.c.vc : a.c.kc;
-    // lane t < 16: where token t comes from (block, slot of the block, scale byte)
-    int64_t from = -1;
-    int slot = 0, e_src = 0;
-    if (lane < hi) {
-        const int t = a.kept[((int64_t)s * a.c.heads + h) * a.keep + start + lane];
-        e_src = kScaleMin;
-        if (t >= 0 && t < len) {
-            const int page = a.table[(int64_t)s * a.max_pages + t / a.c.page];
-            if (page >= 0 && page < a.c.pages) {
-                from = ((int64_t)page * a.c.heads + h) * per + t % a.c.page / kKvBlock;
-                slot = t % kKvBlock;
-                e_src = scales[from];
-            }
+    const int64_t blk = ((int64_t)to * a.c.heads + h) * per + slot_of(a.c, start, pn) / kKvBlock;
+    int64_t from = -1; // the token's old block
+    int slot = 0;      // and its slot there
+    if (t >= 0 && t < len) {
+        const int pi = page_of(a.c, t), page = a.table[(int64_t)s * a.max_pages + pi];
+        if (page >= 0 && page < a.c.pages) {
+            from = ((int64_t)page * a.c.heads + h) * per + slot_of(a.c, t, pi) / kKvBlock;
+            slot = t % kKvBlock;
         }
     }
-    const int e = (int)wave_max((uint32_t)e_src);
-    if (lane == 0) scales[blk] = (uint8_t)e;
-    if (side == 0 && lane < kKvBlock)
-        a.weights[blk * kKvBlock + lane] = from >= 0 ? a.weights[from * kKvBlock + slot] : 0.0f;
-    const int by = e_src - e; // per token, on its lane
+    const uint32_t live = (uint32_t)__ballot(from >= 0);
+    const int64_t before = __shfl_up(from, 1);
+    // tokens with which another old block begins (the kept tokens ascend)
+    const uint32_t starts = (uint32_t)__ballot(from >= 0 && (lane == 0 || before != from));
+    const auto block_at = [&](int i) {
+        return (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)from, i) |
+               (int64_t)__builtin_amdgcn_readlane((int)(from >> 32), i) << 32;
+    };
 
-    if (side == 0) {
-        constexpr int N = D / 32;
-        u32x2_t x[N];
+    // all of the keys and the first old block of the values are on their way before any is used
+    u32x4_t x[KC];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int t = (i * 64 + lane) / (D / 8), part = (i * 64 + lane) % (D / 8);
-            const int64_t f = __shfl(from, t);
-            const int sl = __shfl(slot, t);
-            x[i] = u32x2_t{0, 0};
-            if (f >= 0) x[i] = *(const u32x2_t *)(all + (f * kKvBlock + sl) * D + part * 8);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int t = (i * 64 + lane) / (D / 8), part = (i * 64 + lane) % (D / 8);
-            const int b = __shfl(by, t);
-            float v[8];
-            decode4(x[i][0], v);
-            decode4(x[i][1], v + 4);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = e == 255 ? 0.0f : __builtin_amdgcn_ldexpf(v[j], b);
-            *(u32x2_t *)(all + (blk * kKvBlock + t) * D + part * 8) =
-                u32x2_t{encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7])};
-        }
-        return;
+    for (int i = 0; i < KC; ++i) {
+        const int c = i * 64 + lane, tok = c / (D / 16), part = c % (D / 16);
+        const int64_t f = __shfl(from, tok);
+        const int sl = __shfl(slot, tok);
+        x[i] = u32x4_t{0, 0, 0, 0};
+        if (c < D && f >= 0) x[i] = *(const u32x4_t *)(a.c.kc + (f * kKvBlock + sl) * D + part * 16);
     }
-    // Values: a lane holds two dimensions, 16 bytes a block each. The kept tokens ascend, so those
-    // of one old block come together: each old block is loaded once, the next one while the
-    // tokens of this one move byte by byte (v_perm_b32, under uniform selectors).
-    constexpr int N = (D / 2 + 63) / 64;
-    const uint32_t starts = (uint32_t)__ballot(lane < hi && from >= 0 && (lane == 0 || from != __shfl(from, lane ? lane - 1 : 0)));
-    const bool plain = !__any(lane < hi && by != 0) && e != 255;
+    u32x4_t cur[VC][2] = {}, next[VC][2] = {};
+    const auto load = [&](int i) {
+        const int64_t f = block_at(i);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int pair = i * 64 + lane;
-        if (pair >= D / 2) continue;
-        const auto load = [&](int t, u32x4_t *x) {
-            const int64_t f = (int64_t)((uint32_t)__builtin_amdgcn_readlane((int)from, t)) |
-                              (int64_t)__builtin_amdgcn_readlane((int)(from >> 32), t) << 32;
-            const u32x4_t *p = (const u32x4_t *)(all + (f * D + pair * 2) * kKvBlock);
-            x[0] = p[0];
-            x[1] = p[1];
-        };
-        u32x4_t cur[2] = {}, next[2] = {}, out[2] = {};
-        if (starts) load(__builtin_ctz(starts), next);
-#pragma unroll
-        for (int t = 0; t < kKvBlock; ++t) {
-            if (starts >> t & 1) {
-                cur[0] = next[0];
-                cur[1] = next[1];
-                const uint32_t rest = starts & ~((2u << t) - 1);
-                if (rest) load(__builtin_ctz(rest), next);
+        for (int j = 0; j < VC; ++j)
+            if (D % 128 == 0 || j * 64 + lane < D / 2) {
+                const u32x4_t *p = (const u32x4_t *)(a.c.vc + (f * D + (j * 64 + lane) * 2) * kKvBlock);
+                next[j][0] = p[0];
+                next[j][1] = p[1];
             }
-            if (t >= hi || __builtin_amdgcn_readlane((int)(from >> 32), t) < 0) continue; // 0
-            const int sl = __builtin_amdgcn_readlane(slot, t);
-            // byte sl%4 of the source word into byte t%4 of the result, the others as they are
-            const uint32_t sel = (0x03020100u & ~(0xFFu << (8 * (t % 4)))) |
-                                 (uint32_t)(4 + sl % 4) << (8 * (t % 4));
+    };
+    if (starts) load(__builtin_ctz(starts));
+    int ek = 0, ev = 0;
+    float weight = 0.0f;
+    if (lane < hi) ek = ev = kScaleMin;
+    if (from >= 0) {
+        ek = a.c.ks[from];
+        ev = a.c.vs[from];
+        weight = a.weights[from * kKvBlock + slot];
+    }
+    if (lane < kKvBlock) a.weights[blk * kKvBlock + lane] = weight;
+    const int emk = (int)wave_max((uint32_t)ek), emv = (int)wave_max((uint32_t)ev);
+    if (lane == 0) {
+        a.c.ks[blk] = (uint8_t)emk;
+        a.c.vs[blk] = (uint8_t)emv;
+    }
+    // A token whose scale is smaller than the new block's is rescaled: decoded to half precision,
+    // times 2^(e_src - e), encoded again. The half holds every product that is not far below the
+    // smallest code exactly, so the encoding rounds once.
+    const float byk = __builtin_amdgcn_ldexpf(1.0f, ek - emk), byv = __builtin_amdgcn_ldexpf(1.0f, ev - emv);
+    const bool plain_k = !__any(lane < hi && ek != emk), plain_v = !__any(lane < hi && ev != emv);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t w = sl < 8 ? (sl < 4 ? cur[k][0] : cur[k][1]) : (sl < 12 ? cur[k][2] : cur[k][3]);
-                out[k][t / 4] = __builtin_amdgcn_perm(w, out[k][t / 4], sel);
-            }
+    for (int i = 0; i < KC; ++i) {
+        const int c = i * 64 + lane, tok = c / (D / 16), part = c % (D / 16);
+        if (!plain_k) {
+            const float by = __shfl(byk, tok);
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                x[i][w] = encode4h(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[i][w], by, false),
+                                   __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[i][w], by, true));
         }
+        if (emk == 255) x[i] = u32x4_t{0, 0, 0, 0};
+        if (c < D) *(u32x4_t *)(a.c.kc + (blk * kKvBlock + tok) * D + part * 16) = x[i];
+    }
+
+    // values: a lane holds pairs of dimensions, 16 bytes of a block each. Each old block is
+    // loaded once, the next one while the tokens of this one move byte by byte.
+    u32x4_t out[VC][2] = {};
+#pragma unroll
+    for (int i = 0; i < kKvBlock; ++i) {
+        if (starts >> i & 1) {
+#pragma unroll
+            for (int j = 0; j < VC; ++j) {
+                cur[j][0] = next[j][0];
+                cur[j][1] = next[j][1];
+            }
+            const uint32_t rest = starts & ~((2u << i) - 1);
+            if (rest) load(__builtin_ctz(rest));
+        }
+        if (!(live >> i & 1)) continue; // stays 0
+        const int sl = __builtin_amdgcn_readlane(slot, i);
+        // byte sl%4 of the source word into byte i%4 of the result, the others as they are
+        const uint32_t sel = (0x03020100u & ~(0xFFu << (8 * (i % 4)))) | (uint32_t)(4 + sl % 4) << (8 * (i % 4));
+        const auto move = [&](int w) {
+#pragma unroll
+            for (int j = 0; j < VC; ++j)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    out[j][k][i / 4] = __builtin_amdgcn_perm(cur[j][k][w], out[j][k][i / 4], sel);
+        };
+        switch (sl / 4) { // uniform
+        case 0: move(0); break;
+        case 1: move(1); break;
+        case 2: move(2); break;
+        default: move(3);
+        }
+    }
+    if (!plain_v) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            f16x2_t by[2];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                by[q / 2][q % 2] = (_Float16)__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(byv), 4 * w + q));
+#pragma unroll
+            for (int j = 0; j < VC; ++j)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    out[j][k][w] = encode4h(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(out[j][k][w], 1.0f, false) * by[0],
+                                            __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(out[j][k][w], 1.0f, true) * by[1]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VC; ++j) {
+        const int pair = j * 64 + lane;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            if (!plain) {
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    float v[4];
-                    decode4(out[k][w], v);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[j] = e == 255 ? 0.0f : __builtin_amdgcn_ldexpf(v[j], __builtin_amdgcn_readlane(by, 4 * w + j));
-                    out[k][w] = encode4(v[0], v[1], v[2], v[3]);
-                }
-            }
-            *(u32x4_t *)(all + (blk * D + pair * 2 + k) * kKvBlock) = out[k];
+            if (emv == 255) out[j][k] = u32x4_t{0, 0, 0, 0};
+            if (pair < D / 2) *(u32x4_t *)(a.c.vc + (blk * D + pair * 2 + k) * kKvBlock) = out[j][k];
         }
     }
 }
@@ -483,7 +574,7 @@ template <int D>
 hipError_t evict(const EvictArgs &a, hipStream_t st)
 {
     const int64_t pairs = (int64_t)a.n * a.c.heads, blocks = ((int64_t)a.keep + kKvBlock - 1) / kKvBlock;
-    const int64_t jobs = (2 * (int64_t)a.c.heads + 3) / 4;
+    const int64_t jobs = ((int64_t)a.c.heads + 3) / 4;
     if (pairs > INT32_MAX || blocks * a.n > INT32_MAX || jobs > 65535) return hipErrorInvalidValue;
     kv_select_kernel<<<(unsigned)pairs, 64 * kSelWaves, 0, st>>>(a);
     hipError_t err = hipGetLastError();
