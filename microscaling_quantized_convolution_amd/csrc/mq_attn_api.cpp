@@ -9,6 +9,12 @@ namespace {
 constexpr double kLog2e = 1.4426950408889634;
 constexpr int32_t kMaxTokens = 1 << 30; // positions of a sequence stay below this
 
+// The kernels number a cache's blocks in 32 bits.
+bool blocks_ok(const mq_kv_cache *c)
+{
+    return (int64_t)c->num_pages * c->kv_heads <= INT32_MAX / (c->page_size / MQ_KV_BLOCK);
+}
+
 bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 bool dim_ok(int32_t d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
@@ -68,7 +74,7 @@ mq_status mq_kv_append(const mq_kv_cache *cache, const mq_rows *k, const mq_rows
         return MQ_ERR_ARG;
     if (!same(k, v) || k->heads != v->heads || k->heads != cache->kv_heads || k->head_dim != cache->head_dim)
         return MQ_ERR_SHAPE;
-    if (!dim_ok(cache->head_dim) || (int64_t)max_pages * cache->page_size > kMaxTokens) return MQ_ERR_UNSUPPORTED;
+    if (!dim_ok(cache->head_dim) || !blocks_ok(cache) || (int64_t)max_pages * cache->page_size > kMaxTokens) return MQ_ERR_UNSUPPORTED;
     if (n_seqs == 0 || max_pages == 0 || k->tokens == 0) return MQ_OK;
     const mq::AppendArgs a = {view(cache), view(k), view(v), table, lens, cu, n_seqs, max_pages, k->tokens};
     return launched(mq::launch_kv_append(a, cache->head_dim, k->dtype, stream));
@@ -99,7 +105,7 @@ mq_status mq_attn_cached(const mq_kv_cache *cache, const mq_rows *q, const mq_ro
         return MQ_ERR_SHAPE;
     const int64_t cap = (int64_t)max_pages * cache->page_size;
     const int64_t top = max_len ? max_len : cap;
-    if (!dim_ok(cache->head_dim) || cap > kMaxTokens || top > kMaxTokens ||
+    if (!dim_ok(cache->head_dim) || !blocks_ok(cache) || cap > kMaxTokens || top > kMaxTokens ||
         (int64_t)(q->heads / cache->kv_heads) * q_len > INT32_MAX - 16)
         return MQ_ERR_UNSUPPORTED;
     if (n_seqs == 0) return MQ_OK;
@@ -142,7 +148,7 @@ mq_status mq_kv_evict(const mq_kv_cache *cache, float *weights, const int32_t *t
         !ints_ok(kept, (int64_t)n_seqs * keep))
         return MQ_ERR_ARG;
     if (keep > (int64_t)new_max_pages * cache->page_size) return MQ_ERR_SHAPE;
-    if (!dim_ok(cache->head_dim) || (int64_t)max_pages * cache->page_size > kMaxTokens) return MQ_ERR_UNSUPPORTED;
+    if (!dim_ok(cache->head_dim) || !blocks_ok(cache) || (int64_t)max_pages * cache->page_size > kMaxTokens) return MQ_ERR_UNSUPPORTED;
     if (n_seqs == 0) return MQ_OK;
     const mq::EvictArgs a = {view(cache), weights, table, lens, new_table, new_lens, kept, n_seqs,
                              max_pages, new_max_pages, keep, recent};

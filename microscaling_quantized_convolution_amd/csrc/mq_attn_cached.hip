@@ -78,17 +78,23 @@ __device__ __forceinline__ int tiles_of(const CachedArgs &a, int s)
     return (held_tokens(a, s) + kTile - 1) / kTile;
 }
 
-// Tiles of a workgroup: an equal share of all, and one for each wave at least.
-__device__ __forceinline__ int share(const CachedArgs &a, const CachedPlan &pl)
+// A workgroup's share of `total` tiles of the sequences' units: equal, and one tile for each wave
+// at least.
+__device__ __forceinline__ int share(int total, const CachedArgs &a, const CachedPlan &pl)
 {
-    int total = 0;
-    for (int base = 0; base < a.n; base += 64) {
-        const int s = base + (threadIdx.x & 63);
-        total += __builtin_amdgcn_readlane(wave_prefix(s < a.n ? tiles_of(a, s) : 0), 63);
-    }
-    total *= a.c.heads * pl.row_tiles;
-    const int per = (total + pl.groups - 1) / pl.groups;
+    const int per = (total * a.c.heads * pl.row_tiles + pl.groups - 1) / pl.groups;
     return per < kWaves ? kWaves : per;
+}
+
+// Tiles of sequences 0..s-1.
+__device__ __forceinline__ int tiles_before(const CachedArgs &a, int s)
+{
+    int sum = 0;
+    for (int base = 0; base < s; base += 64) {
+        const int q = base + (threadIdx.x & 63);
+        sum += __builtin_amdgcn_readlane(wave_prefix(q < s ? tiles_of(a, q) : 0), 63);
+    }
+    return sum;
 }
 
 // Parts of a unit: `first` is the list's first tile of the unit, which has `tiles` of them.
@@ -100,7 +106,7 @@ __device__ __forceinline__ void parts_of(int first, int tiles, int per, int unit
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(64 * kWaves) attn_cached_kernel(CachedArgs a, CachedPlan pl)
+__global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_kernel(CachedArgs a, CachedPlan pl)
 {
     typedef typename Elem<DT>::x8 x8;
     constexpr int KS = D / 32;         // steps of 32 dimensions in the first product
@@ -116,69 +122,85 @@ __global__ void __launch_bounds__(64 * kWaves) attn_cached_kernel(CachedArgs a, 
     const int group = a.q_heads / a.c.heads;
     const int blocks = a.c.page / kKvBlock;
 
-    int s, sub, tile, left; // sequence, unit of it, first tile; tiles of the workgroup to do
+    // A stretch of one unit's tokens: unit `sub` of sequence s, which holds `len` tokens.
+    struct Seg {
+        int s, sub, len, begin, end;
+    };
+    Seg c;
+    int left = 0; // tiles of the workgroup after those of c
     if (pl.groups) {
-        const int per = share(a, pl);
-        int index;
-        if (!locate_unit(blockIdx.x * per, a.n, [&](int q) { return tiles_of(a, q) * per_unit; }, &s, &index))
-            return;
-        const int tiles = tiles_of(a, s);
-        sub = index / tiles;
-        tile = index % tiles;
-        left = per;
+        const int len = lane < a.n ? held_tokens(a, lane) : 0; // of the first 64 sequences
+        const int incl = wave_prefix((len + kTile - 1) / kTile);
+        int total = __builtin_amdgcn_readlane(incl, 63);
+        if (a.n > 64) total = tiles_before(a, a.n);
+        const int per = share(total, a, pl);
+        const int first = blockIdx.x * per; // in the list, which counts each sequence per_unit times
+        if (first >= total * per_unit) return;
+        const int seq_tile = first / per_unit; // tiles of whole sequences at most this many before
+        int index, tiles;
+        if (a.n <= 64) {
+            c.s = __builtin_ctzll(__ballot(incl > seq_tile));
+            c.len = __builtin_amdgcn_readlane(len, c.s);
+            tiles = (c.len + kTile - 1) / kTile;
+            index = first - (__builtin_amdgcn_readlane(incl, c.s) - tiles) * per_unit;
+        } else {
+            locate_unit(seq_tile, a.n, [&](int q) { return tiles_of(a, q); }, &c.s, &index);
+            c.len = __builtin_amdgcn_readfirstlane(held_tokens(a, c.s));
+            tiles = (c.len + kTile - 1) / kTile;
+            index = first - (seq_tile - index) * per_unit;
+        }
+        c.sub = index / tiles;
+        const int tile = index % tiles, count = tiles - tile < per ? tiles - tile : per;
+        left = per - count;
+        c.begin = tile * kTile;
+        c.end = tile + count == tiles ? c.len : (tile + count) * kTile;
     } else {
-        s = blockIdx.x / per_unit;
-        sub = blockIdx.x % per_unit;
-        tile = 0;
-        left = 1 << 30;
+        c.s = blockIdx.x / per_unit;
+        c.sub = blockIdx.x % per_unit;
+        c.len = __builtin_amdgcn_readfirstlane(held_tokens(a, c.s));
+        c.begin = 0;
+        c.end = c.len;
     }
-    for (;;) { // the workgroup's units
-    const int len = held_tokens(a, s), tiles = (len + kTile - 1) / kTile;
-    const int unit = s * per_unit + sub;
-    const int h = sub / pl.row_tiles;
-    const int count = tiles - tile < left ? tiles - tile : left;
-    const int begin = tile * kTile;
-    const int end = begin + count * kTile < len ? begin + count * kTile : len;
-    const bool whole = count == tiles;
-    const int row = sub % pl.row_tiles * kRows + n;
-    const int qi = row / group, qh = h * group + row % group;
-    const bool real = row < pl.rows;
-    // tokens this lane's row sees
-    const int see = real ? clampi(len - a.q_len + qi + 1, 0, len) : 0;
-    const int32_t *table = a.table + (int64_t)s * a.max_pages;
-
-    // the row's query, in the order in which the lanes hold K
-    x8 q[KS];
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-        const int d = WIDE ? i / 2 * 64 + g * 16 + i % 2 * 8 : i * 32 + g * 8;
-        u32x4_t v = {0, 0, 0, 0};
-        if (real) v = *(const u32x4_t *)(a.q.p + (int64_t)(s * a.q_len + qi) * a.q.ts + qh * a.q.hs + d);
-        q[i] = __builtin_bit_cast(x8, v);
-    }
-
-    f32x4_t o[VT];
-#pragma unroll
-    for (int i = 0; i < VT; ++i) o[i] = f32x4_t{0, 0, 0, 0};
-    float m = -INFINITY, l = 0.0f;
 
     // A tile's loads are issued as soon as the registers of the tile before are free: K's after
-    // the first product, V's after the second, the page numbers one tile further ahead.
+    // the first product, V's after the second, also where the tile before is another unit's. The
+    // page numbers come through the scalar cache, so that waiting for them waits for no vector
+    // load.
     constexpr int STEP = kWaves * kTile;
-    const auto page_at = [&](int t) { return t < end ? table[page_of(a.c, t)] : -1; };
-    // block (of the cache) of the tokens from t on in that page, or -1
-    const auto block_at = [&](int page, int t) -> int64_t {
-        return page < 0 || page >= a.c.pages
-                   ? -1
-                   : ((int64_t)page * a.c.heads + h) * blocks + slot_of(a.c, t, page_of(a.c, t)) / kKvBlock;
-    };
     u32x2_t k[4][KS];
     u32x4_t v[VT];
     int ke, ve;
+    struct Blocks {
+        int b0, b1, b2, b3;
+    };
+    // blocks (of the cache) of the four 16-token parts of a tile, -1 where there is none
+    const auto tile_blocks = [&](const Seg &u, int t) {
+        typedef const int32_t __attribute__((address_space(4))) *scalar_t;
+        const scalar_t table = (scalar_t)(uintptr_t)(a.table + (int64_t)u.s * a.max_pages);
+        const int h = u.sub / pl.row_tiles;
+        int at[4], pi[4], page[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            at[i] = t + i * kKvBlock < u.end ? t + i * kKvBlock : u.end - 1;
+            pi[i] = page_of(a.c, at[i]);
+            page[i] = table[pi[i]];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b[i] = (page[i] * a.c.heads + h) * blocks + slot_of(a.c, at[i], pi[i]) / kKvBlock;
+            const bool live = ((uint32_t)page[i] < (uint32_t)a.c.pages) & (t + i * kKvBlock < u.end);
+            b[i] = live ? b[i] : -1;
+        }
+        return Blocks{b[0], b[1], b[2], b[3]};
+    };
+    const auto pick = [](const Blocks &r, int i) {
+        const int lo = i & 1 ? r.b1 : r.b0, hi = i & 1 ? r.b3 : r.b2;
+        return i & 2 ? hi : lo;
+    };
     // K rows 4t + n%4 of block n/4, and the scales of block g. What is no block is read as
     // block 0 and masked where it is used.
-    const auto load_k = [&](int64_t kb, int64_t vb) {
-        const uint8_t *p = a.c.kc + ((kb < 0 ? 0 : kb) * kKvBlock + (n & 3)) * D + g * (WIDE ? 16 : 8);
+    const auto load_k = [&](int kb, int vb) {
+        const uint8_t *p = a.c.kc + (int64_t)(kb < 0 ? 0 : kb) * (kKvBlock * D) + (n & 3) * D + g * (WIDE ? 16 : 8);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -194,20 +216,74 @@ __global__ void __launch_bounds__(64 * kWaves) attn_cached_kernel(CachedArgs a, 
         ke = a.c.ks[vb < 0 ? 0 : vb];
         ve = a.c.vs[vb < 0 ? 0 : vb];
     };
-    const auto load_v = [&](int64_t vb) {
-        const uint8_t *p = a.c.vc + ((vb < 0 ? 0 : vb) * D + n) * kKvBlock;
+    const auto load_v = [&](int vb) {
+        const uint8_t *p = a.c.vc + (int64_t)(vb < 0 ? 0 : vb) * (kKvBlock * D) + n * kKvBlock;
 #pragma unroll
         for (int i = 0; i < VT; ++i) v[i] = *(const u32x4_t *)(p + i * 16 * kKvBlock);
     };
-    int t0 = begin + wave * kTile;
-    const int tk = (n >> 2) * kKvBlock, tv = g * kKvBlock; // the lane's blocks of a tile
-    int64_t vb = block_at(page_at(t0 + tv), t0 + tv);
-    int page_k = page_at(t0 + STEP + tk), page_v = page_at(t0 + STEP + tv);
-    if (t0 < end) {
-        load_k(block_at(page_at(t0 + tk), t0 + tk), vb);
+    const int tv = g * kKvBlock; // the lane's block of a tile
+    int vb = -1;
+    bool loaded = false; // the wave's first tile of c is on its way
+
+    for (;;) { // the workgroup's units
+    const int unit = c.s * per_unit + c.sub;
+    const int h = c.sub / pl.row_tiles;
+    const bool whole = c.begin == 0 && c.end == c.len;
+    const int row = c.sub % pl.row_tiles * kRows + n;
+    const int qi = row / group, qh = h * group + row % group;
+    const bool real = row < pl.rows;
+    // tokens this lane's row sees
+    const int see = real ? clampi(c.len - a.q_len + qi + 1, 0, c.len) : 0;
+
+    // the row's query, in the order in which the lanes hold K
+    x8 q[KS];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        const int d = WIDE ? i / 2 * 64 + g * 16 + i % 2 * 8 : i * 32 + g * 8;
+        u32x4_t v = {0, 0, 0, 0};
+        if (real) v = *(const u32x4_t *)(a.q.p + (int64_t)(c.s * a.q_len + qi) * a.q.ts + qh * a.q.hs + d);
+        q[i] = __builtin_bit_cast(x8, v);
+    }
+
+    // The query is waited for here: left to its first use, inside the loop, the wait would empty
+    // the queue of loads in every step.
+    __builtin_amdgcn_s_waitcnt(0x0F70); // vmcnt(0)
+    f32x4_t o[VT];
+#pragma unroll
+    for (int i = 0; i < VT; ++i) o[i] = f32x4_t{0, 0, 0, 0};
+    float m = -INFINITY, l = 0.0f;
+
+    int t0 = c.begin + wave * kTile;
+    if (!loaded && t0 < c.end) {
+        const Blocks r = tile_blocks(c, t0);
+        vb = pick(r, g);
+        load_k(pick(r, n >> 2), vb);
         load_v(vb);
     }
-    for (; t0 < end; t0 += STEP) {
+    loaded = false;
+    // what the workgroup does next
+    Seg next = {a.n, 0, 0, 0, 0};
+    if (left > 0) {
+        next = c;
+        if (++next.sub == per_unit) { // the next sequence that holds tokens
+            next.sub = 0;
+            do {
+                ++next.s;
+                next.len = next.s < a.n ? __builtin_amdgcn_readfirstlane(held_tokens(a, next.s)) : 1;
+            } while (next.len == 0);
+        }
+        next.begin = 0;
+        next.end = next.len < left * kTile ? next.len : left * kTile;
+    }
+    for (; t0 < c.end; t0 += STEP) {
+        // the wave's next tile, of this unit or the next
+        const bool stay = t0 + STEP < c.end;
+        const Seg &u = stay ? c : next;
+        const int t1 = stay ? t0 + STEP : next.begin + wave * kTile;
+        const bool more = u.s < a.n && t1 < u.end;
+        Blocks r = {-1, -1, -1, -1};
+        if (more) r = tile_blocks(u, t1);
+
         // tokens of this lane's block that its row sees (0 where there is no block)
         const int sees = vb >= 0 ? see - (t0 + tv) : 0;
         const float kf = block_scale(a.scale_log2e, ke), vf = block_scale(1.0f, ve);
@@ -226,14 +302,13 @@ __global__ void __launch_bounds__(64 * kWaves) attn_cached_kernel(CachedArgs a, 
             }
         }
         // slots past the last token, and pages that do not exist, hold anything
-        const bool ragged = t0 + kTile > end || __any(vb < 0);
-        const int slots = vb >= 0 ? end - (t0 + tv) : 0;
-        const int t1 = t0 + STEP;
-        vb = block_at(page_v, t1 + tv);
-        const int64_t kb = block_at(page_k, t1 + tk);
-        page_k = page_at(t1 + STEP + tk);
-        page_v = page_at(t1 + STEP + tv);
-        if (t1 < end) load_k(kb, vb);
+        const bool ragged = t0 + kTile > c.end || __any(vb < 0);
+        const int slots = vb >= 0 ? c.end - (t0 + tv) : 0;
+        // Loaded also where there is no next tile (block 0 stands in): a load under a condition
+        // would be copied, and so waited for, where the paths meet.
+        vb = pick(r, g);
+        load_k(pick(r, n >> 2), vb);
+        loaded = more;
 
         if (a.weights && real) {
             float *dst = (float *)((char *)a.ws + pl.scores) + ((int64_t)unit * kRows + n) * pl.slots + t0 + tv;
@@ -287,7 +362,7 @@ __global__ void __launch_bounds__(64 * kWaves) attn_cached_kernel(CachedArgs a, 
                 if constexpr (DT == MQ_F16) o[i] = Elem<MQ_BF16>::mfma16(vv, lo, o[i]);
             }
         }
-        if (t1 < end) load_v(vb);
+        load_v(vb);
     }
     // the four lane groups hold parts of l, the waves parts of everything
     l += __shfl_xor(l, 16);
@@ -317,7 +392,7 @@ __global__ void __launch_bounds__(64 * kWaves) attn_cached_kernel(CachedArgs a, 
     if ((!whole || a.weights) && wave == 0 && g == 0)
         ((f32x2_t *)((char *)a.ws + pl.ml))[slot * kRows + n] = f32x2_t{top, sum};
     if (real) {
-        uint16_t *out = a.out + (int64_t)(s * a.q_len + qi) * a.out_ts + qh * a.out_hs;
+        uint16_t *out = a.out + (int64_t)(c.s * a.q_len + qi) * a.out_ts + qh * a.out_hs;
         float *part = (float *)((char *)a.ws + pl.part) + (slot * kRows + n) * D;
 #pragma unroll
         for (int j = 0; j < (VT + kWaves - 1) / kWaves; ++j) { // each wave finishes some dimensions
@@ -334,16 +409,9 @@ __global__ void __launch_bounds__(64 * kWaves) attn_cached_kernel(CachedArgs a, 
                 *(f32x4_t *)(part + i * 16 + g * 4) = v;
         }
     }
-    if (!pl.groups) return;
-    left -= count;
-    if (left <= 0) return;
-    tile = 0;
-    if (++sub == per_unit) { // the next sequence that holds tokens
-        sub = 0;
-        do {
-            if (++s == a.n) return;
-        } while (held_tokens(a, s) == 0);
-    }
+    if (next.s >= a.n) return;
+    left -= (next.end + kTile - 1) / kTile;
+    c = next;
     __syncthreads(); // part_o is read to the end
     }
 }
@@ -364,16 +432,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
     const f32x2_t *ml = (const f32x2_t *)((const char *)a.ws + pl.ml);
 
     const int per_unit = a.c.heads * pl.row_tiles;
-    const int per = pl.groups ? share(a, pl) : 0;
-    // where sequence s begins in the list of tiles
-    const auto list_start = [&](int s) {
-        int sum = 0;
-        for (int base = 0; base < s; base += 64) {
-            const int q = base + (tid & 63);
-            sum += __builtin_amdgcn_readlane(wave_prefix(q < s ? tiles_of(a, q) : 0), 63);
-        }
-        return sum * per_unit;
-    };
+    const int per = pl.groups ? share(tiles_before(a, a.n), a, pl) : 0;
 
     if ((int)blockIdx.x >= join) { // weights
         const int b = (int)blockIdx.x - join, chunks = (pl.slots + kJoinThreads - 1) / kJoinThreads;
@@ -382,7 +441,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
         if (first >= len) return;
         const int t = first + tid;
         const int64_t x0 = ((int64_t)s * a.c.heads + h) * pl.row_tiles;
-        const int start = pl.groups ? list_start(s) : 0;
+        const int start = pl.groups ? tiles_before(a, s) * per_unit : 0;
         float sum = 0.0f;
         for (int rt = 0; rt < pl.row_tiles; ++rt) {
             // maximum and sum of the tile's rows: 16 lanes a row, each every 16th part
@@ -427,7 +486,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
     const int sub = h * pl.row_tiles + r0 / kRows;
     const int tiles = tiles_of(a, s);
     int slot, parts;
-    parts_of(list_start(s) + sub * tiles, tiles, per, s * per_unit + sub, &slot, &parts);
+    parts_of(tiles_before(a, s) * per_unit + sub * tiles, tiles, per, s * per_unit + sub, &slot, &parts);
     if (parts == 1) return; // written by its only workgroup
     ml += (int64_t)slot * kRows + r0 % kRows;
     const float *po = (const float *)((const char *)a.ws + pl.part) + ((int64_t)slot * kRows + r0 % kRows) * D;
