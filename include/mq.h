@@ -491,7 +491,7 @@ mq_status mq_attn_prompt(const mq_rows *q, const mq_rows *k, const mq_rows *v, c
  * weights_dev: fp32 [num_pages][kv_heads][page_size], as mq_attn_cached adds them up.
  * table_dev [n_seqs][max_pages]; new_table_dev [n_seqs][new_max_pages], with
  *          keep <= new_max_pages * page_size.
- * new_lens_dev: [n_seqs], receives min(lens[s], keep).
+ * new_lens_dev: [n_seqs], receives min(lens[s], keep); not lens_dev itself (MQ_ERR_ARG).
  * kept_dev: [n_seqs][kv_heads][keep], receives the kept tokens' former positions, ascending, -1
  *          after the last.
  * A kept token whose old page is outside [0, num_pages) is copied as code 0 with scale byte 10.

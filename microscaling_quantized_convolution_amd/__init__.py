@@ -323,38 +323,42 @@ def out_hw(p: ConvLike) -> Tuple[int, int]:
 
 # ---- attention over an 8-bit key/value cache ---------------------------------------------------
 #
-# These calls are made once per layer and token, so their marshalling is kept short: checks that
-# the library cannot make itself (types, contiguity, device), then one foreign call.
+# These calls are made once per layer and token, so their marshalling is kept short (a few
+# attribute reads a tensor): checks that the library cannot make itself, types, contiguity and
+# device, then one foreign call.
 
 _DTYPES = {torch.float16: MQ_F16, torch.bfloat16: MQ_BF16}
-_raw_stream = torch._C._cuda_getCurrentRawStream if torch.version.hip else None
+if torch.version.hip:
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _rows(t: torch.Tensor, what: str) -> mq_rows:
+def _rows(t: torch.Tensor, what: str, device: int) -> mq_rows:
     """[tokens][heads][dim] view with a contiguous last dimension -> mq_rows."""
-    dt = _DTYPES.get(t.dtype)
-    if dt is None or t.dim() != 3 or not t.is_cuda or t.stride(2) != 1:
-        raise ValueError(f"{what}: expected a float16 or bfloat16 CUDA tensor [tokens][heads][dim] "
-                         f"with contiguous elements, got {tuple(t.shape)} {t.dtype} on {t.device}, "
-                         f"strides {t.stride()}")
+    dt, strides = _DTYPES.get(t.dtype), t.stride()
+    if dt is None or len(strides) != 3 or strides[2] != 1 or t.get_device() != device:
+        raise ValueError(f"{what}: expected a float16 or bfloat16 tensor [tokens][heads][dim] with "
+                         f"contiguous elements on cuda:{device} (the current device), got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {strides}")
     n, h, d = t.shape
-    return mq_rows(t.data_ptr(), t.stride(0), t.stride(1), n, h, d, dt)
+    return mq_rows(t.data_ptr(), strides[0], strides[1], n, h, d, dt)
 
 
-def _dense(t: torch.Tensor, dtype: torch.dtype, shape, what: str) -> int:
-    """Address of a contiguous CUDA tensor of that type and shape."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {dtype} CUDA tensor {tuple(shape)}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+def _dense(t: torch.Tensor, dtype: torch.dtype, shape, what: str, device: int) -> int:
+    """Address of a contiguous tensor of that type and shape on that device."""
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or
+            t.get_device() != device):
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor {tuple(shape)} on "
+                         f"cuda:{device} (the current device), got {tuple(t.shape)} {t.dtype} on "
+                         f"{t.device}, strides {t.stride()}")
     return t.data_ptr()
 
 
-def _attn_stream(stream, device: torch.device):
-    """The given stream, or the device's current one; the device has to be the current one."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return _raw_stream(device.index) if stream is None else _stream(stream)
+def _table(table: torch.Tensor, n: int, device: int) -> Tuple[int, int]:
+    """Address and width of a page table of n rows."""
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != n:
+        raise ValueError(f"table: expected [{n} sequences][pages], got {tuple(shape)}")
+    return _dense(table, torch.int32, shape, "table", device), shape[1]
 
 
 class KVCache:
@@ -371,16 +375,17 @@ class KVCache:
                              f"multiple of {MQ_KV_BLOCK}, got {tuple(k_codes.shape)}")
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k_codes.shape
         blocks = (self.num_pages, self.kv_heads, self.page_size // MQ_KV_BLOCK)
+        dev = k_codes.get_device()
         self.device = k_codes.device
         self.k_codes, self.v_codes = k_codes, v_codes
         self.k_scales, self.v_scales = k_scales, v_scales
         u8 = torch.uint8
         self.struct = mq_kv_cache(
             self.num_pages, self.page_size, self.kv_heads, self.head_dim,
-            _dense(k_codes, u8, k_codes.shape, "k_codes"),
-            _dense(v_codes, u8, blocks + (self.head_dim, MQ_KV_BLOCK), "v_codes"),
-            _dense(k_scales, u8, blocks, "k_scales"), _dense(v_scales, u8, blocks, "v_scales"))
-        self._ref = ctypes.byref(self.struct)
+            _dense(k_codes, u8, k_codes.shape, "k_codes", dev),
+            _dense(v_codes, u8, blocks + (self.head_dim, MQ_KV_BLOCK), "v_codes", dev),
+            _dense(k_scales, u8, blocks, "k_scales", dev), _dense(v_scales, u8, blocks, "v_scales", dev))
+        self._ref, self._dev = ctypes.byref(self.struct), dev
         self.weights_shape = torch.Size((self.num_pages, self.kv_heads, self.page_size))
 
     @classmethod
@@ -392,6 +397,12 @@ class KVCache:
         blocks = (num_pages, kv_heads, page_size // MQ_KV_BLOCK)
         return cls(new(num_pages, kv_heads, page_size, head_dim),
                    new(*blocks, head_dim, MQ_KV_BLOCK), new(*blocks), new(*blocks))
+
+    def ref(self, device: int):
+        """The structure, for a call on that device."""
+        if device != self._dev:
+            raise ValueError(f"cache on {self.device}, but the current device is cuda:{device}")
+        return self._ref
 
     def values(self) -> Tuple[torch.Tensor, torch.Tensor]:
         """Keys and values as fp32 [pages][heads][page_size][dim] (for inspection: every slot is
@@ -407,22 +418,20 @@ class KVCache:
         return out[0], out[1]
 
 
-def _table(table: torch.Tensor, n: int) -> int:
-    if table.dim() != 2:
-        raise ValueError(f"table: expected [sequences][pages], got {tuple(table.shape)}")
-    return _dense(table, torch.int32, (n, table.shape[1]), "table")
-
-
 def mq_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.Tensor,
                  lens: torch.Tensor, cu: torch.Tensor, stream=None):
     """Quantize the packed keys and values k, v [tokens][kv_heads][dim] into the cache behind each
     sequence's lens[s] tokens: sequence s receives rows cu[s]:cu[s + 1]. lens is not changed."""
-    n = lens.shape[0]
-    rk, rv = _rows(k, "k"), _rows(v, "v")
-    _check(_lib.mq_kv_append(cache._ref, rk, rv, _table(table, n),
-                             _dense(lens, torch.int32, (n,), "lens"),
-                             _dense(cu, torch.int32, (n + 1,), "cu"), n, table.shape[1],
-                             _attn_stream(stream, cache.device)), "mq_kv_append")
+    dev = _current_device()
+    shape = lens.shape
+    n = shape[0]
+    pt, width = _table(table, n, dev)
+    st = _lib.mq_kv_append(cache.ref(dev), _rows(k, "k", dev), _rows(v, "v", dev), pt,
+                           _dense(lens, torch.int32, shape, "lens", dev),
+                           _dense(cu, torch.int32, (n + 1,), "cu", dev), n, width,
+                           _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_kv_append")
 
 
 def mq_attn_cached_workspace_bytes(n_seqs: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -446,24 +455,34 @@ def mq_attn_cached(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: t
     """Attention of each sequence's last q_len tokens, q [sequences * q_len][q_heads][dim], over
     its lens[s] cached tokens (these included), into out. weights (fp32, cache.weights_shape)
     gains the attention each cached token received."""
-    n = lens.shape[0]
-    rq, ro = _rows(q, "q"), _rows(out, "out")
-    pw = None if weights is None else _dense(weights, torch.float32, cache.weights_shape, "weights")
-    pws = None if ws is None else _dense(ws, torch.uint8, ws.shape, "ws")
-    _check(_lib.mq_attn_cached(cache._ref, rq, ro, _table(table, n),
-                               _dense(lens, torch.int32, (n,), "lens"), n, table.shape[1], q_len,
-                               max_len, scale, pw, pws, 0 if ws is None else ws.numel(),
-                               _attn_stream(stream, cache.device)), "mq_attn_cached")
+    dev = _current_device()
+    shape = lens.shape
+    n = shape[0]
+    pt, width = _table(table, n, dev)
+    pw = (None if weights is None
+          else _dense(weights, torch.float32, cache.weights_shape, "weights", dev))
+    st = _lib.mq_attn_cached(cache.ref(dev), _rows(q, "q", dev), _rows(out, "out", dev), pt,
+                             _dense(lens, torch.int32, shape, "lens", dev), n, width, q_len,
+                             max_len, scale, pw,
+                             None if ws is None else _dense(ws, torch.uint8, ws.shape, "ws", dev),
+                             0 if ws is None else ws.numel(),
+                             _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_attn_cached")
 
 
 def mq_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
                    cu: torch.Tensor, max_len: int, scale: float, stream=None):
     """Causal attention over packed prompts: rows cu[s]:cu[s + 1] of q, out [tokens][q_heads][dim]
     and k, v [tokens][kv_heads][dim] are sequence s, none longer than max_len."""
-    n = cu.shape[0] - 1
-    rq, rk, rv, ro = _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), _rows(out, "out")
-    _check(_lib.mq_attn_prompt(rq, rk, rv, ro, _dense(cu, torch.int32, (n + 1,), "cu"), n, max_len,
-                               scale, _attn_stream(stream, q.device)), "mq_attn_prompt")
+    dev = _current_device()
+    shape = cu.shape
+    st = _lib.mq_attn_prompt(_rows(q, "q", dev), _rows(k, "k", dev), _rows(v, "v", dev),
+                             _rows(out, "out", dev), _dense(cu, torch.int32, shape, "cu", dev),
+                             shape[0] - 1, max_len, scale,
+                             _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_attn_prompt")
 
 
 def mq_kv_evict(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor,
@@ -472,12 +491,17 @@ def mq_kv_evict(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, weights
     """Keep at most kept.shape[2] tokens of each sequence and head, the `recent` last ones and those
     with the largest weights, copied to the pages of new_table; kept [sequences][kv_heads][keep]
     receives their former positions, new_lens the sequences' new lengths."""
-    n, keep = lens.shape[0], kept.shape[-1]
-    i32 = torch.int32
-    _check(_lib.mq_kv_evict(cache._ref,
-                            _dense(weights, torch.float32, cache.weights_shape, "weights"),
-                            _table(table, n), _dense(lens, i32, (n,), "lens"),
-                            _table(new_table, n), _dense(new_lens, i32, (n,), "new_lens"),
-                            _dense(kept, i32, (n, cache.kv_heads, keep), "kept"), n,
-                            table.shape[1], new_table.shape[1], keep, recent,
-                            _attn_stream(stream, cache.device)), "mq_kv_evict")
+    dev = _current_device()
+    i32, shape = torch.int32, lens.shape
+    n, keep = shape[0], kept.shape[-1]
+    pt, width = _table(table, n, dev)
+    pn, new_width = _table(new_table, n, dev)
+    st = _lib.mq_kv_evict(cache.ref(dev),
+                          _dense(weights, torch.float32, cache.weights_shape, "weights", dev), pt,
+                          _dense(lens, i32, shape, "lens", dev), pn,
+                          _dense(new_lens, i32, shape, "new_lens", dev),
+                          _dense(kept, i32, (n, cache.kv_heads, keep), "kept", dev), n, width,
+                          new_width, keep, recent,
+                          _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_kv_evict")

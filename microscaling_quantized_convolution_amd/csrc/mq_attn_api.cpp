@@ -145,7 +145,7 @@ mq_status mq_kv_evict(const mq_kv_cache *cache, float *weights, const int32_t *t
         return MQ_ERR_ARG;
     if (!ints_ok(table, (int64_t)n_seqs * max_pages) || !ints_ok(lens, n_seqs) ||
         !ints_ok(new_table, (int64_t)n_seqs * new_max_pages) || !ints_ok(new_lens, n_seqs) ||
-        !ints_ok(kept, (int64_t)n_seqs * keep))
+        !ints_ok(kept, (int64_t)n_seqs * keep) || (n_seqs && new_lens == lens))
         return MQ_ERR_ARG;
     if (keep > (int64_t)new_max_pages * cache->page_size) return MQ_ERR_SHAPE;
     if (!dim_ok(cache->head_dim) || !blocks_ok(cache) || (int64_t)max_pages * cache->page_size > kMaxTokens) return MQ_ERR_UNSUPPORTED;
