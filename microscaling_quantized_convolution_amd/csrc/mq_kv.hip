@@ -68,6 +68,8 @@ __device__ __forceinline__ int capacity(int max_pages, int page)
 // One wave per touched block, head and side (keys, values). Bound by the bytes: 2 B in and 1 B
 // out per element. The block's largest magnitude is found on the 16-bit patterns (their
 // magnitudes order like unsigned numbers), two at a time, while the elements stay in registers.
+// Every load is made, with the token clamped into the new ones, and what does not belong is
+// cleared afterwards: loads under a condition were waited for one by one.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
 {
@@ -110,8 +112,12 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int t = (i * 64 + lane) / (D / 8), part = (i * 64 + lane) % (D / 8);
-            x[i] = u32x4_t{0, 0, 0, 0};
-            if (t >= lo && t < hi) x[i] = *(const u32x4_t *)(rows + t * src.ts + part * 8);
+            x[i] = *(const u32x4_t *)(rows + clampi(t, lo, hi - 1) * src.ts + part * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int t = (i * 64 + lane) / (D / 8);
+            if (t < lo || t >= hi) x[i] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < 4; ++w) m = max16x2(m, x[i][w] & 0x7FFF7FFFu);
         }
@@ -150,15 +156,18 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int pair = i * 64 + lane;
+        const int pair = i * 64 + lane < D / 2 ? i * 64 + lane : 0;
+#pragma unroll
+        for (int t = 0; t < kKvBlock; ++t)
+            x[i][t] = *(const uint32_t *)(rows + clampi(t, lo, hi - 1) * src.ts + pair * 2);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int t = 0; t < kKvBlock; ++t) {
-            x[i][t] = 0;
-            if (t >= lo && t < hi && pair < D / 2)
-                x[i][t] = *(const uint32_t *)(rows + t * src.ts + pair * 2);
+            if (t < lo || t >= hi) x[i][t] = 0;
             m = max16x2(m, x[i][t] & 0x7FFF7FFFu);
         }
-    }
     m = wave_max(max16x2(m, m >> 16) & 0xFFFFu);
     const int e_new = scale_byte(__float_as_uint(Elem<DT>::f32((uint16_t)m)));
     const int e = e_new > e_held ? e_new : e_held;
