@@ -471,7 +471,8 @@ mq_status mq_attn_cached(const mq_kv_cache *cache, const mq_rows *q, const mq_ro
  *   p[j] = softmax_j(scale * sum_d q[d] * k[j][d])     out[d] = sum_j p[j] * v[j][d]
  * with the softmax and both sums in fp32 and p rounded to dtype for the second product.
  * max_len: no sequence is longer than this (rows past it are neither read nor written).
- * Errors: as for mq_attn_cached (without a workspace).
+ * Errors: as for mq_attn_cached (without a workspace); MQ_ERR_UNSUPPORTED also for a token_stride
+ *         of k or v above 2^24.
  */
 mq_status mq_attn_prompt(const mq_rows *q, const mq_rows *k, const mq_rows *v, const mq_rows *out,
                          const int32_t *cu_dev, int32_t n_seqs, int32_t max_len, float scale,

@@ -8,6 +8,7 @@ namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
 constexpr int32_t kMaxTokens = 1 << 30; // positions of a sequence stay below this
+constexpr int64_t kMaxStride = 1 << 24; // 64 rows of keys or values span less than 2^31 bytes
 
 // The kernels number a cache's blocks in 32 bits.
 bool blocks_ok(const mq_kv_cache *c)
@@ -128,7 +129,8 @@ mq_status mq_attn_prompt(const mq_rows *q, const mq_rows *k, const mq_rows *v, c
     if (!same(q, k) || !same(q, v) || !same(q, out) || q->heads != out->heads || k->heads != v->heads ||
         q->heads % k->heads)
         return MQ_ERR_SHAPE;
-    if (!dim_ok(q->head_dim) || max_len > kMaxTokens) return MQ_ERR_UNSUPPORTED;
+    if (!dim_ok(q->head_dim) || max_len > kMaxTokens || k->token_stride > kMaxStride || v->token_stride > kMaxStride)
+        return MQ_ERR_UNSUPPORTED;
     const mq::PromptArgs a = {view(q), view(k), view(v), static_cast<uint16_t *>(out->data), out->token_stride,
                               out->head_stride, cu, n_seqs, max_len, q->heads, k->heads, q->tokens,
                               (float)(scale * kLog2e), 0};
