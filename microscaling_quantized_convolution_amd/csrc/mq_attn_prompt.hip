@@ -14,70 +14,81 @@
 
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 namespace mq {
 namespace {
 
 constexpr int kM = 128, kN = 64;
 
-// Where 16-byte piece c of a row lies in LDS: rows are not padded (a wave writes 1 KB of them at
-// a time), the pieces of a row change places instead, so that 16 rows' pieces of one number
-// (keys, read 16 bytes a lane) and 4 rows' groups of four pieces (values, read 8 bytes a lane)
-// lie in different banks.
-template <int D> __device__ __forceinline__ int key_place(int row, int c)
-{
-    return c ^ (D == 64 || D == 192 ? row / 2 & 7 : (D == 96 ? row / 4 & 3 : row & 15));
-}
-template <int D> __device__ __forceinline__ int value_place(int row, int c)
-{
-    return c ^ (D == 64 || D == 192 ? (row / 2 & 1) << 2 : (D == 96 ? 0 : (row & 3) << 2));
-}
+// A tile of keys or values in LDS: kN rows of D/8 pieces of 16 bytes, not padded (a wave writes
+// 1 KB of them at a time). The pieces of a row change places instead, by an exclusive or of their
+// number with some bits of the row's: 16 rows' pieces of one number (keys, read 16 bytes a lane)
+// and 4 rows' groups of four pieces (values, read 8 bytes a lane) then lie in different banks.
+// The bits stay within `span` bytes, to which every row is aligned, so an address splits into
+// (lane's part ^ low part of the offset) + rest.
+template <int D> struct Place {
+    static constexpr int kspan = D % 128 == 0 ? 256 : (D % 64 == 0 ? 128 : 64);
+    static constexpr int vspan = kspan;
+    static __device__ __forceinline__ int key(int row)
+    {
+        return D % 128 == 0 ? row & 15 : (D % 64 == 0 ? row / 2 & 7 : row / 4 & 3);
+    }
+    static __device__ __forceinline__ int value(int row)
+    {
+        return D % 128 == 0 ? (row & 3) << 2 : (D % 64 == 0 ? (row / 2 & 1) << 2 : 0);
+    }
+};
 
 typedef __attribute__((ext_vector_type(8))) short s16x8_t;
 
-// V's operand of 16 tokens from `at` on and 32 dimensions: lane (column n = dimension, half hh)
-// receives tokens 4hh .. 4hh+3 and 8+4hh .. 8+4hh+3 of step u. The lane's own read is of token
-// t = 4hh + (n%16)/4, dimensions d = 16(n/16) + 4(n%4) onwards; the places of the 32 dimensions'
-// four pieces depend on t%4 (or t/2%2) alone, which no step changes.
+// Eight elements of a key from dimension 16c + 8hh on; `at`: the lane's row of the tile at c = 0.
 template <int D>
-__device__ __forceinline__ s16x8_t read_v(const uint16_t *vt, int t, int d, int u, int i)
+__device__ __forceinline__ u32x4_t read_k(uint32_t at, int c)
 {
-    typedef s16x4_t __attribute__((address_space(3))) *lp;
-    const uint16_t *at = vt + (u * 16 + t) * D + value_place<D>(t, i * 4 + d / 8) * 8 + d % 8;
-    const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)at);
-    const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(at + 8 * D));
+    typedef const __attribute__((address_space(3))) u32x4_t *lp;
+    constexpr int S = Place<D>::kspan;
+    return *(lp)(uintptr_t)((at ^ (uint32_t)(c * 32 % S)) + c * 32 / S * S);
+}
+
+// V's operand of 16 tokens (step u) and 32 dimensions (block i): lane (column n = dimension, half
+// hh) receives tokens 4hh .. 4hh+3 and 8+4hh .. 8+4hh+3. The lane's own read, at u = i = 0, is
+// `at`: token 4hh + (n%16)/4, dimensions 16(n/16) + 4(n%4) onwards.
+template <int D>
+__device__ __forceinline__ s16x8_t read_v(uint32_t at, int u, int i)
+{
+    typedef __attribute__((address_space(3))) s16x4_t *lp;
+    constexpr int S = Place<D>::vspan;
+    const uint32_t x = (at ^ (uint32_t)(i * 64 % S)) + i * 64 / S * S + u * 32 * D;
+    const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(uintptr_t)x);
+    const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(uintptr_t)(x + 16 * D));
     return __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // Bits of a 16-bit value's exponent: all set in a NaN or an infinity.
 template <int DT> constexpr uint32_t kExp = DT == MQ_BF16 ? 0x7F80u : 0x7C00u;
 
-// Any NaN or infinity among two packed values.
-template <int DT> __device__ __forceinline__ bool not_finite(uint32_t w)
-{
-    return (w & kExp<DT>) == kExp<DT> || ((w >> 16) & kExp<DT>) == kExp<DT>;
-}
-
-// The second product where V holds a NaN or an infinity and some tokens are masked: 0 times such
-// a value would reach rows that do not see it. The finite part goes the usual way; the rest is
-// counted per row and dimension over the tokens that the row sees, with 1 for each +inf, 128
-// for each -inf and 16384 for each NaN (64 tokens at most: the sums do not mix), and added as
-// what it amounts to. `sees`: bit j of lane (n, hh) stands for the j-th of its 32 tokens.
+// The second product where V may hold a NaN or an infinity and some tokens are masked: 0 times
+// such a value would reach rows that do not see it. The finite part goes the usual way (a finite
+// V gives the usual bits); the rest is counted per row and dimension over the tokens that the row
+// sees, with 1 for each +inf, 128 for each -inf and 16384 for each NaN (64 tokens at most: the
+// sums do not mix), and added as what it amounts to. `sees`: bit j of lane (n, hh) stands for the
+// j-th of its 32 tokens.
 template <int DT, int D>
-__device__ __forceinline__ void odd_product(const uint16_t *vt, int tv, int dv, const typename Elem<DT>::x8 *p,
-                                            uint32_t sees, f32x16_t *o)
+__device__ __forceinline__ void odd_product(uint32_t at, const typename Elem<DT>::x8 *p, uint32_t sees,
+                                            f32x16_t *o)
 {
     typedef typename Elem<DT>::x8 x8;
-    constexpr int DT32 = D / 32;
     const uint32_t codes[3] = {Elem<DT>::pack(1.0f, 0.0f), Elem<DT>::pack(128.0f, 0.0f),
                                Elem<DT>::pack(16384.0f, 0.0f)};
-    for (int i = 0; i < DT32; ++i) {
-        f32x16_t odd, add;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) odd[r] = add[r] = 0.0f;
+    for (int i = 0; i < D / 32; ++i) {
+        f32x16_t odd;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) odd[r] = 0.0f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            s16x8_t v = read_v<D>(vt, tv, dv, u, i), w, one;
+            s16x8_t v = read_v<D>(at, u, i), w, one;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t b = (uint16_t)v[j];
@@ -87,19 +98,16 @@ __device__ __forceinline__ void odd_product(const uint16_t *vt, int tv, int dv, 
                 v[j] = bad ? (short)0 : v[j];
                 one[j] = (short)(sees >> (8 * u + j) & 1u ? codes[0] : 0u);
             }
-            add = Elem<DT>::mfma32(__builtin_bit_cast(x8, v), p[u], add);
+            o[i] = Elem<DT>::mfma32(__builtin_bit_cast(x8, v), p[u], o[i]);
             odd = Elem<DT>::mfma32(__builtin_bit_cast(x8, w), __builtin_bit_cast(x8, one), odd);
         }
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const int c = (int)odd[r];
-            if (c & 127) add[r] += INFINITY;
-            if (c >> 7 & 127) add[r] -= INFINITY;
-            if (c >> 14) add[r] = __builtin_nanf("");
+            if (c & 127) o[i][r] += INFINITY;
+            if (c >> 7 & 127) o[i][r] -= INFINITY;
+            if (c >> 14) o[i][r] = __builtin_nanf("");
         }
-#pragma unroll
-        for (int k = 0; k < DT32; ++k) // o is held in registers: no indexing at run time
-            if (k == i) o[k] += add;
     }
 }
 
@@ -131,9 +139,9 @@ template <int DT, int D>
 __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_prompt_kernel(PromptArgs a)
 {
     typedef typename Elem<DT>::x8 x8;
-    constexpr int KS = D / 16, DT32 = D / 32, CH = D / 8;
+    constexpr int KS = D / 16, DT32 = D / 32, CH = D / 8, TILE = kN * D * 2;
     constexpr int LOADS = kN * CH / 256; // 1 KB pieces of a tile to each wave
-    __shared__ __align__(16) uint16_t ks[2][kN * D], vs[2][kN * D];
+    __shared__ __align__(256) uint16_t ks[2][kN * D], vs[2][kN * D];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, hh = lane >> 5;
     const int tiles = (a.max_len + kM - 1) / kM;
@@ -151,71 +159,84 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_prompt_kernel(Promp
     const int row = tile * kM + wave * 32 + n;
     const int end = (tile + 1) * kM < count ? (tile + 1) * kM : count;
 
+    // the wave's share of a tile: its 1 KB pieces, and where each lane's 16 bytes come from
     const uint16_t *kp = a.k.p + (int64_t)first * a.k.ts + kvh * a.k.hs;
     const uint16_t *vp = a.v.p + (int64_t)first * a.v.ts + kvh * a.v.hs;
     const uint32_t lds_k = lds_address(&ks[0][0]), lds_v = lds_address(&vs[0][0]);
-    const auto stage = [&](int t0, int buf) { // past the last token, the last one again
-        const uint16_t *kt = kp + (int64_t)t0 * a.k.ts, *vt = vp + (int64_t)t0 * a.v.ts;
-        const int last = count - 1 - t0;
+    const uint32_t kts = (uint32_t)a.k.ts * 2, vts = (uint32_t)a.v.ts * 2; // bytes
+    uint32_t from_k[LOADS], from_v[LOADS];
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int piece = (wave * LOADS + i) * 64 + lane, t = piece / CH, c = piece % CH;
-            const int from = t < last ? t : last;
-            const uint32_t to = (uint32_t)(buf * kN * D * 2 + (wave * LOADS + i) * 1024);
-            load_to_lds(kt, (uint32_t)from * (uint32_t)(a.k.ts * 2) + key_place<D>(t, c) * 16, lds_k + to);
-            load_to_lds(vt, (uint32_t)from * (uint32_t)(a.v.ts * 2) + value_place<D>(t, c) * 16, lds_v + to);
+    for (int i = 0; i < LOADS; ++i) {
+        const int piece = (wave * LOADS + i) * 64 + lane, t = piece / CH, c = piece % CH;
+        from_k[i] = (uint32_t)t * kts + (c ^ Place<D>::key(t)) * 16;
+        from_v[i] = (uint32_t)t * vts + (c ^ Place<D>::value(t)) * 16;
+    }
+    const auto stage = [&](const uint16_t *p, int64_t ts, const uint32_t *from, uint32_t lds, int i) {
+        if (i * kN >= end) return;
+        const uint16_t *at = p + (int64_t)(i * kN) * ts;
+        const uint32_t to = lds + (i & 1) * TILE + wave * LOADS * 1024;
+        const int last = count - 1 - i * kN;
+        if (last >= kN - 1) {
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) load_to_lds(at, from[j], to + j * 1024);
+        } else { // past the last token, the last one again
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) {
+                const int t = ((wave * LOADS + j) * 64 + lane) / CH;
+                load_to_lds(at, from[j] - (t > last ? (uint32_t)(t - last) * (uint32_t)(ts * 2) : 0u), to + j * 1024);
+            }
         }
     };
+    const auto stage_k = [&](int i) { stage(kp, a.k.ts, from_k, lds_k, i); };
+    const auto stage_v = [&](int i) { stage(vp, a.v.ts, from_v, lds_v, i); };
+    // the lane's places in a tile
+    const uint32_t at_k = (lds_k + n * (2 * D) + hh * 16) ^ (Place<D>::key(n) * 16);
+    const int tv = hh * 4 + (n & 15) / 4, dv = (n >> 4) * 16 + (n & 3) * 4;
+    const uint32_t at_v = (lds_v + tv * (2 * D) + dv * 2) ^ (Place<D>::value(tv) * 16);
 
     x8 q[KS];
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
-        u32x4_t v = {0, 0, 0, 0};
-        if (row < count) v = *(const u32x4_t *)(a.q.p + (int64_t)(first + row) * a.q.ts + h * a.q.hs + i * 16 + hh * 8);
+        const int r = row < count ? row : count - 1;
+        const u32x4_t v = *(const u32x4_t *)(a.q.p + (int64_t)(first + r) * a.q.ts + h * a.q.hs + i * 16 + hh * 8);
         q[i] = __builtin_bit_cast(x8, v ^ a.q_flip);
     }
-    stage(0, 0);
     f32x16_t o[DT32];
+    float m, l;
+    const auto begin = [&] {
 #pragma unroll
-    for (int i = 0; i < DT32; ++i)
+        for (int d = 0; d < DT32; ++d)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
-    float m = -INFINITY, l = 0.0f;
-    lds_barrier();
-
-    int buf = 0;
-    for (int t0 = 0; t0 < end; t0 += kN, buf ^= 1) {
-        if (t0) lds_barrier();
-        if (t0 + kN < end) stage(t0 + kN, buf ^ 1);
-        const uint16_t *kt = ks[buf], *vt = vs[buf];
-        const bool masked = t0 + kN > tile * kM; // some row of the workgroup does not see all tokens
-        bool odd = false;
-        if (masked) {
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const u32x4_t w = *(const u32x4_t *)&vt[(i * 256 + tid) * 8];
-                odd |= not_finite<DT>(w[0]) || not_finite<DT>(w[1]) || not_finite<DT>(w[2]) || not_finite<DT>(w[3]);
-            }
-            odd = __syncthreads_or(odd);
-        }
-        if (t0 > tile * kM + wave * 32 + 31) continue; // past this wave's last row
-        f32x16_t sc[2];
+            for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+        m = -INFINITY;
+        l = 0.0f;
+        stage_k(0);
+        stage_v(0);
+        stage_k(1);
+        lds_barrier();
+    };
+    // S^T of tile i
+    const auto scores = [&](int i, f32x16_t *sc) {
+        const uint32_t at = at_k + (i & 1) * TILE;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) sc[b][r] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                const x8 k = *(const x8 *)&kt[(b * 32 + n) * D + key_place<D>(n, i * 2 + hh) * 8];
-                sc[b] = Elem<DT>::mfma32(k, q[i], sc[b]);
-            }
+            for (int c = 0; c < KS; ++c)
+                sc[b] = Elem<DT>::mfma32(__builtin_bit_cast(x8, read_k<D>(at + b * 64 * D, c)), q[c], sc[b]);
         }
-        if (t0 + kN > tile * kM + wave * 32) { // tokens after some of the wave's rows
+    };
+    // place j of 32 in a lane's scores: its token of the tile
+    const auto token = [&](int b, int r) { return b * 32 + 8 * (r / 4) + 4 * hh + r % 4; };
+    // scores of tile i -> p, 16 tokens each; m, l and o follow
+    const auto softmax = [&](int i, auto masked, f32x16_t *sc, x8 *p) {
+        if (masked) { // tokens after some of the wave's rows
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (t0 + b * 32 + 8 * (r / 4) + 4 * hh + r % 4 > row) sc[b][r] = -INFINITY;
+                    if (i * kN + token(b, r) > row) sc[b][r] = -INFINITY;
         }
         float top = m;
 #pragma unroll
@@ -232,41 +253,71 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_prompt_kernel(Promp
             const float keep = grown ? __builtin_amdgcn_exp2f((was - m) * a.scale_log2e) : 1.0f;
             l *= keep;
 #pragma unroll
-            for (int i = 0; i < DT32; ++i) o[i] *= keep;
+            for (int d = 0; d < DT32; ++d) o[d] *= keep;
         }
         const float base = m == -INFINITY ? 0.0f : m * a.scale_log2e;
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                sc[b][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][r], a.scale_log2e, -base));
-                l += sc[b][r];
-            }
-        x8 p[4]; // 16 tokens each
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             u32x4_t pw;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                pw[j] = Elem<DT>::pack(sc[u / 2][u % 2 * 8 + 2 * j], sc[u / 2][u % 2 * 8 + 2 * j + 1]);
+            for (int j = 0; j < 4; ++j) {
+                const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u / 2][u % 2 * 8 + 2 * j], a.scale_log2e, -base));
+                const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u / 2][u % 2 * 8 + 2 * j + 1], a.scale_log2e, -base));
+                l += p0;
+                l += p1;
+                pw[j] = Elem<DT>::pack(p0, p1);
+            }
             p[u] = __builtin_bit_cast(x8, pw);
         }
-        const int tv = hh * 4 + (n & 15) / 4, dv = (n >> 4) * 16 + (n & 3) * 4;
-        if (masked && odd) {
+    };
+
+    // Tile i, whose scores are in sc, which then holds those of tile i + 1: the first product of
+    // the next tile keeps the matrix unit busy under this one's softmax.
+    f32x16_t sc[2];
+    const auto step = [&](int i, auto masked) {
+        lds_barrier(); // K of tile i + 1 and V of tile i are there; tile i - 1 is no longer read
+        stage_k(i + 2);
+        stage_v(i + 1);
+        f32x16_t cur[2] = {sc[0], sc[1]};
+        if (!masked || (i + 1) * kN < end) scores(i + 1, sc);
+        x8 p[4];
+        softmax(i, masked, cur, p);
+        const uint32_t at = at_v + (i & 1) * TILE;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int d = 0; d < DT32; ++d)
+                o[d] = Elem<DT>::mfma32(__builtin_bit_cast(x8, read_v<D>(at, u, d)), p[u], o[d]);
+    };
+    const int sure = tile * kM / kN; // tiles that all rows of the workgroup see
+    begin();
+    scores(0, sc);
+    for (int i = 0; i < sure; ++i) step(i, std::false_type());
+    for (int i = sure; i * kN < end; ++i) step(i, std::true_type());
+
+    // A NaN or an infinity of V at a masked place has made some result NaN. Then, and where one
+    // is due, everything is done again with the masked products taken apart.
+    float odd = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DT32; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) odd = __builtin_fmaf(o[d][r], 0.0f, odd);
+    if (__syncthreads_or(!(odd == 0.0f))) {
+        begin();
+        for (int i = 0; i * kN < end; ++i) {
+            lds_barrier();
+            if (i) stage_k(i + 1);
+            stage_v(i + 1);
+            x8 p[4];
+            scores(i, sc);
+            softmax(i, std::true_type(), sc, p);
             uint32_t sees = 0;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    sees |= (t0 + b * 32 + 8 * (r / 4) + 4 * hh + r % 4 <= row ? 1u : 0u) << (b * 16 + r);
-            odd_product<DT, D>(vt, tv, dv, p, sees, o);
-            continue;
+                for (int r = 0; r < 16; ++r) sees |= (i * kN + token(b, r) <= row ? 1u : 0u) << (b * 16 + r);
+            odd_product<DT, D>(at_v + (i & 1) * TILE, p, sees, o);
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int i = 0; i < DT32; ++i)
-                o[i] = Elem<DT>::mfma32(__builtin_bit_cast(x8, read_v<D>(vt, tv, dv, u, i)), p[u], o[i]);
     }
     l += __shfl_xor(l, 32);
     if (row >= count) return;
