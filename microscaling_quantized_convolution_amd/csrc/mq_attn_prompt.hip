@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_prompt_kernel(Promp
     if (tile * kM >= count) return;
     const int row = tile * kM + wave * 32 + n;
     const int end = (tile + 1) * kM < count ? (tile + 1) * kM : count;
+    const int wave_last = tile * kM + wave * 32 + 31 < end - 1 ? tile * kM + wave * 32 + 31 : end - 1;
 
     // the wave's share of a tile: its 1 KB pieces, and where each lane's 16 bytes come from
     const uint16_t *kp = a.k.p + (int64_t)first * a.k.ts + kvh * a.k.hs;
@@ -279,7 +280,8 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_prompt_kernel(Promp
         stage_k(i + 2);
         stage_v(i + 1);
         f32x16_t cur[2] = {sc[0], sc[1]};
-        if (!masked || (i + 1) * kN < end) scores(i + 1, sc);
+        if (!masked || (i + 1) * kN <= wave_last) scores(i + 1, sc);
+        if (masked && i * kN > wave_last) return; // past the wave's rows
         x8 p[4];
         softmax(i, masked, cur, p);
         const uint32_t at = at_v + (i & 1) * TILE;
