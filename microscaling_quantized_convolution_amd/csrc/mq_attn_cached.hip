@@ -446,6 +446,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
         for (int rt = 0; rt < pl.row_tiles; ++rt) {
             // maximum and sum of the tile's rows: 16 lanes a row, each every 16th part
             const int r = tid / 16;
+            const int rows = pl.rows - rt * kRows < kRows ? pl.rows - rt * kRows : kRows;
+            const float *sc = (const float *)((const char *)a.ws + pl.scores) + (x0 + rt) * kRows * pl.slots +
+                              (t < len ? t : first);
+            float score[kRows]; // on their way while the maxima are found
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) score[q] = sc[(int64_t)(q < rows ? q : 0) * pl.slots];
             int slot = (int)x0 + rt, parts = 1;
             if (pl.groups) parts_of(start + (h * pl.row_tiles + rt) * tiles, tiles, per, (int)x0 + rt, &slot, &parts);
             const f32x2_t *p = ml + (int64_t)slot * kRows + r;
@@ -463,14 +469,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
             __syncthreads();
             if (tid % 16 == 0) row_ml[r] = f32x2_t{base, l == 0.0f ? 0.0f : 1.0f / l};
             __syncthreads();
-            const int rows = pl.rows - rt * kRows < kRows ? pl.rows - rt * kRows : kRows;
-            const float *sc = (const float *)((const char *)a.ws + pl.scores) +
-                              (x0 + rt) * kRows * pl.slots + t;
-            if (t < len) {
-#pragma unroll 4
-                for (int q = 0; q < rows; ++q)
-                    sum += __builtin_amdgcn_exp2f(sc[(int64_t)q * pl.slots] - row_ml[q][0]) * row_ml[q][1];
-            }
+#pragma unroll
+            for (int q = 0; q < kRows; ++q)
+                if (q < rows) sum += __builtin_amdgcn_exp2f(score[q] - row_ml[q][0]) * row_ml[q][1];
         }
         if (t >= len) return;
         const int pi = page_of(a.c, t), page = a.table[(int64_t)s * a.max_pages + pi];

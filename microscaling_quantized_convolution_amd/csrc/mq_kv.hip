@@ -6,8 +6,6 @@
 // read and written, so no two waves share a byte.
 #include "mq_attn_device.hpp"
 
-#include <type_traits>
-
 namespace mq {
 namespace {
 
@@ -229,7 +227,7 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
     __shared__ __align__(16) uint32_t held[kSelWaves][kSelSteps * kSelStep];
     __shared__ uint32_t hist[kSelBins];
     __shared__ uint32_t part[kSelWaves][2];
-    __shared__ uint32_t pick[2]; // digit, rank within it
+    __shared__ uint32_t pick[4]; // digit, rank within it, tokens of that digit; tokens collected
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int s = blockIdx.x / a.c.heads, h = blockIdx.x % a.c.heads;
     const int len = clampi(a.lens[s], 0, capacity(a.max_pages, a.c.page));
@@ -261,19 +259,16 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
     const auto keys_of = [&](f32x4_t w) {
         return u32x4_t{weight_key(w[0]), weight_key(w[1]), weight_key(w[2]), weight_key(w[3])};
     };
-    // f(keys of the lane's four tokens, the first of them, whether all of the wave's exist), over
-    // the wave's stretch
+    // f(keys of the lane's four tokens, the first of them), over the wave's stretch
     const auto each = [&](auto f) {
-        int t = from;
-        const auto one = [&](u32x4_t k) {
-            if (t + kSelStep <= to)
-                f(k, t + lane * 4, std::true_type());
+        for (int t = from; t < to; t += kSelStep) {
+            u32x4_t k;
+            if (t - from < kSelSteps * kSelStep)
+                k = *(const u32x4_t *)&held[wave][t - from + lane * 4];
             else
-                f(k, t + lane * 4, std::false_type());
-        };
-        for (int i = 0; i < kSelSteps && t < to; ++i, t += kSelStep)
-            one(*(const u32x4_t *)&held[wave][t - from + lane * 4]);
-        for (; t < to; t += kSelStep) one(keys_of(weights_at(t + lane * 4)));
+                k = keys_of(weights_at(t + lane * 4));
+            f(k, t + lane * 4);
+        }
     };
     // smallest and largest key
     uint32_t lo = ~0u, hi = 0;
@@ -316,12 +311,13 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
     while (top > 0) {
         const int shift = top > 11 ? top - 11 : 0;
         hist[tid] = hist[tid + kSelBins / 2] = 0;
+        if (tid == 0) pick[3] = 0;
         __syncthreads();
-        each([&](u32x4_t k, int t, auto full) {
+        each([&](u32x4_t k, int t) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint32_t d = (k[q] - lo) ^ bound; // decided bits equal: below 2^top
-                if ((full || t + q < to) && (top >= 32 || d >> top == 0)) atomicAdd(&hist[d >> shift], 1u);
+                if (t + q < to && (top >= 32 || d >> top == 0)) atomicAdd(&hist[d >> shift], 1u);
             }
         });
         __syncthreads();
@@ -338,23 +334,54 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
         if (over1 < ties && over1 + c1 >= ties) {
             pick[0] = 2 * tid + 1;
             pick[1] = ties - over1;
+            pick[2] = c1;
         }
         if (over0 < ties && over0 + c0 >= ties) {
             pick[0] = 2 * tid;
             pick[1] = ties - over0;
+            pick[2] = c0;
         }
         __syncthreads();
         bound |= pick[0] << shift;
         ties = pick[1];
         top = shift;
+        if (pick[2] > 64 || top == 0) continue;
+        // few enough are left for a wave to rank them, one to a lane
+        const int left = (int)pick[2];
+        each([&](u32x4_t k, int t) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (t + q < to && ((k[q] - lo) ^ bound) >> top == 0) {
+                    const uint32_t at = atomicAdd(&pick[3], 1u);
+                    if (at < 64) hist[at] = k[q] - lo; // always, if the weights hold still
+                }
+        });
+        __syncthreads();
+        if (wave == 0) {
+            const uint32_t mine = hist[lane < left ? lane : 0];
+            uint32_t more = 0, equal = 0;
+            for (int j = 0; j < left; ++j) {
+                const uint32_t d = __builtin_amdgcn_readlane(mine, j);
+                more += d > mine;
+                equal += d == mine;
+            }
+            if (more < ties && more + equal >= ties) { // lanes of one distance agree
+                pick[0] = mine;
+                pick[1] = ties - more;
+            }
+        }
+        __syncthreads();
+        bound = pick[0];
+        ties = pick[1];
+        top = 0;
     }
     bound += lo;
     uint32_t over = 0, same = 0;
-    each([&](u32x4_t k, int t, auto full) {
+    each([&](u32x4_t k, int t) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            over += __popcll(__ballot((full || t + q < to) && k[q] > bound));
-            same += __popcll(__ballot((full || t + q < to) && k[q] == bound));
+            over += __popcll(__ballot(t + q < to && k[q] > bound));
+            same += __popcll(__ballot(t + q < to && k[q] == bound));
         }
     });
     if (lane == 0) { // the last reads of part[][0] lie before the loop's last barrier
@@ -368,14 +395,14 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
         over = __builtin_amdgcn_readlane(o, 63);
         same = __builtin_amdgcn_readlane(e, 63);
     }
-    each([&](u32x4_t k, int t, auto full) {
+    each([&](u32x4_t k, int t) {
         uint32_t so = over, ss = same; // before the lane's first token
         bool is_over[4], is_same[4];
         uint64_t any_same = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            is_over[q] = (full || t + q < to) && k[q] > bound;
-            is_same[q] = (full || t + q < to) && k[q] == bound;
+            is_over[q] = t + q < to && k[q] > bound;
+            is_same[q] = t + q < to && k[q] == bound;
             const uint64_t bo = __ballot(is_over[q]);
             so += bits_below(bo);
             over += __popcll(bo);
@@ -402,7 +429,9 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
 
 // One wave per new block and head: copies the keys and values of 16 kept tokens at the largest
 // of their scales, and their weights. Bound by the bytes: a kept token's key is one row, but its
-// value lies with the 15 others of its old block, which comes whole.
+// value lies with the 15 others of its old block, which comes whole. (Copying in the workgroup
+// that found the tokens, without a second launch, left 8 of 256 CUs to do it and was no faster
+// at 2 x 1000 tokens.)
 template <int D>
 __global__ void __launch_bounds__(256) kv_move_kernel(EvictArgs a, int blocks)
 {
