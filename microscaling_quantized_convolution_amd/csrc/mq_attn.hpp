@@ -63,7 +63,8 @@ struct PromptArgs {
     const int32_t *cu;
     int n, max_len, q_heads, kv_heads, total;
     float scale_log2e;
-    uint32_t q_flip; // set by the launch: sign bits to flip in pairs of query elements
+    uint32_t q_flip; // set by the launch: sign bits to flip in pairs of query elements,
+    int search;      // and whether the workgroups look for their tiles
 };
 
 // head_dim and dtype are checked by the caller; hipErrorInvalidValue where a launch would need

@@ -133,7 +133,7 @@ mq_status mq_attn_prompt(const mq_rows *q, const mq_rows *k, const mq_rows *v, c
         return MQ_ERR_UNSUPPORTED;
     const mq::PromptArgs a = {view(q), view(k), view(v), static_cast<uint16_t *>(out->data), out->token_stride,
                               out->head_stride, cu, n_seqs, max_len, q->heads, k->heads, q->tokens,
-                              (float)(scale * kLog2e), 0};
+                              (float)(scale * kLog2e), 0, 0};
     return launched(mq::launch_attn_prompt(a, q->head_dim, q->dtype, stream));
 }
 

@@ -144,17 +144,31 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_prompt_kernel(Promp
     __shared__ __align__(256) uint16_t ks[2][kN * D], vs[2][kN * D];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, hh = lane >> 5;
-    const int tiles = (a.max_len + kM - 1) / kM;
     // neighbouring workgroups go to different XCDs: those of one key/value head come to the same
     // one (with 8 heads), whose L2 then serves its keys and values
     const int group = a.q_heads / a.kv_heads;
     const int kvh = blockIdx.x % a.kv_heads, h = kvh * group + blockIdx.x / a.kv_heads % group;
-    const int s = blockIdx.x / a.q_heads % a.n;
-    const int tile = tiles - 1 - (int)(blockIdx.x / a.q_heads / a.n); // the longest rows first
-    int first = a.cu[s], count = a.cu[s + 1];
-    first = first < 0 ? 0 : (first > a.total ? a.total : first);
-    count = (count > a.total ? a.total : count) - first;
-    if (count > a.max_len) count = a.max_len;
+    const auto rows_of = [&](int q, int *first) {
+        const int f = a.cu[q], l = a.cu[q + 1];
+        *first = f < 0 ? 0 : (f > a.total ? a.total : f);
+        const int c = (l > a.total ? a.total : l) - *first;
+        return c > a.max_len ? a.max_len : c;
+    };
+    int s, tile, first;
+    const int unit = blockIdx.x / a.q_heads;
+    if (a.search) { // sequence by sequence, the longest rows of each first
+        int index;
+        if (!locate_unit(unit, a.n, [&](int q) {
+                const int c = rows_of(q, &first);
+                return c > 0 ? (c + kM - 1) / kM : 0;
+            }, &s, &index))
+            return;
+        tile = (rows_of(s, &first) + kM - 1) / kM - 1 - index;
+    } else { // the longest rows of all sequences first; a shorter sequence has no such tile
+        s = unit % a.n;
+        tile = (a.max_len + kM - 1) / kM - 1 - unit / a.n;
+    }
+    const int count = rows_of(s, &first);
     if (tile * kM >= count) return;
     const int row = tile * kM + wave * 32 + n;
     const int end = (tile + 1) * kM < count ? (tile + 1) * kM : count;
@@ -337,10 +351,15 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_prompt_kernel(Promp
 template <int DT, int D>
 hipError_t prompt(const PromptArgs &a, hipStream_t st)
 {
-    const int64_t tiles = ((int64_t)a.max_len + kM - 1) / kM;
-    const int64_t groups = tiles * a.n * a.q_heads;
+    // One workgroup for each tile that a sequence of max_len would have, as long as at most about
+    // three in four of them find nothing to do; else one for each that there can be, which
+    // search for theirs.
+    const int64_t direct = ((int64_t)a.max_len + kM - 1) / kM * a.n, there = (int64_t)a.total / kM + a.n;
+    PromptArgs b = a;
+    b.search = direct > 4 * there;
+    const int64_t groups = (b.search ? there : direct) * a.q_heads;
     if (groups > INT32_MAX) return hipErrorInvalidValue;
-    attn_prompt_kernel<DT, D><<<(unsigned)groups, 256, 0, st>>>(a);
+    attn_prompt_kernel<DT, D><<<(unsigned)groups, 256, 0, st>>>(b);
     return hipGetLastError();
 }
 

@@ -371,6 +371,17 @@ def test_prompt_heads(heads, group, lens):
     check_prompt(q, k, v, lens, 0.2, max_len=1000)
 
 
+def test_prompt_one_long_among_many_short():
+    """Far more tiles in max_len than in the sequences, which are more than a wave searches at a
+    time: the workgroups look for their tiles."""
+    gen, rng = torch.Generator().manual_seed(26), random.Random(26)
+    lens = [rng.choice([0, 1, 5, 40]) for _ in range(70)] + [390] + [rng.choice([0, 3]) for _ in range(30)]
+    q = randn(gen, sum(lens), 2, 64, dtype=BF16)
+    k, v = (randn(gen, sum(lens), 1, 64, dtype=BF16) for _ in range(2))
+    for max_len in (390, 20000):
+        check_prompt(q, k, v, lens, 0.125, max_len)
+
+
 def test_prompt_sharp_and_signed_scales():
     gen = torch.Generator().manual_seed(21)
     lens = [150, 90]
