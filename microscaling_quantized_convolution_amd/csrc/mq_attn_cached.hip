@@ -432,16 +432,32 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
     const f32x2_t *ml = (const f32x2_t *)((const char *)a.ws + pl.ml);
 
     const int per_unit = a.c.heads * pl.row_tiles;
-    const int per = pl.groups ? share(tiles_before(a, a.n), a, pl) : 0;
+    // what this workgroup works on
+    const bool adds = (int)blockIdx.x >= join; // weights
+    const int chunks = (pl.slots + kJoinThreads - 1) / kJoinThreads;
+    const int sh = adds ? ((int)blockIdx.x - join) / chunks : (int)blockIdx.x / pl.rows;
+    const int s = sh / a.c.heads, h = sh % a.c.heads;
+    // its sequence's tokens, the tiles of those before, and a workgroup's share of all
+    int len, before = 0, per = 0;
+    if (!pl.groups) {
+        len = held_tokens(a, s);
+    } else if (a.n <= 64) { // one load
+        const int lane = tid & 63, held = lane < a.n ? held_tokens(a, lane) : 0;
+        const int incl = wave_prefix((held + kTile - 1) / kTile);
+        len = __builtin_amdgcn_readlane(held, s);
+        before = __builtin_amdgcn_readlane(incl, s) - (len + kTile - 1) / kTile;
+        per = share(__builtin_amdgcn_readlane(incl, 63), a, pl);
+    } else {
+        len = held_tokens(a, s);
+        before = tiles_before(a, s);
+        per = share(tiles_before(a, a.n), a, pl);
+    }
+    const int tiles = (len + kTile - 1) / kTile;
 
-    if ((int)blockIdx.x >= join) { // weights
-        const int b = (int)blockIdx.x - join, chunks = (pl.slots + kJoinThreads - 1) / kJoinThreads;
-        const int s = b / chunks / a.c.heads, h = b / chunks % a.c.heads, first = b % chunks * kJoinThreads;
-        const int len = held_tokens(a, s), tiles = (len + kTile - 1) / kTile;
+    if (adds) {
+        const int first = ((int)blockIdx.x - join) % chunks * kJoinThreads, t = first + tid;
         if (first >= len) return;
-        const int t = first + tid;
-        const int64_t x0 = ((int64_t)s * a.c.heads + h) * pl.row_tiles;
-        const int start = pl.groups ? tiles_before(a, s) * per_unit : 0;
+        const int64_t x0 = (int64_t)sh * pl.row_tiles;
         float sum = 0.0f;
         for (int rt = 0; rt < pl.row_tiles; ++rt) {
             // maximum and sum of the tile's rows: 16 lanes a row, each every 16th part
@@ -453,7 +469,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
 #pragma unroll
             for (int q = 0; q < kRows; ++q) score[q] = sc[(int64_t)(q < rows ? q : 0) * pl.slots];
             int slot = (int)x0 + rt, parts = 1;
-            if (pl.groups) parts_of(start + (h * pl.row_tiles + rt) * tiles, tiles, per, (int)x0 + rt, &slot, &parts);
+            if (pl.groups) parts_of(before * per_unit + (h * pl.row_tiles + rt) * tiles, tiles, per, (int)x0 + rt, &slot, &parts);
             const f32x2_t *p = ml + (int64_t)slot * kRows + r;
             float top = -INFINITY, l = 0.0f;
             for (int i = tid % 16; i < parts; i += 16) top = fmaxf(top, p[(int64_t)i * kRows][0]);
@@ -481,13 +497,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
     }
 
     const int r0 = blockIdx.x % pl.rows;
-    const int64_t sh = blockIdx.x / pl.rows; // sequence and head
-    const int h = (int)(sh % a.c.heads), s = (int)(sh / a.c.heads);
     const int qi = r0 / group, qh = h * group + r0 % group;
     const int sub = h * pl.row_tiles + r0 / kRows;
-    const int tiles = tiles_of(a, s);
     int slot, parts;
-    parts_of(tiles_before(a, s) * per_unit + sub * tiles, tiles, per, s * per_unit + sub, &slot, &parts);
+    parts_of(before * per_unit + sub * tiles, tiles, per, s * per_unit + sub, &slot, &parts);
     if (parts == 1) return; // written by its only workgroup
     ml += (int64_t)slot * kRows + r0 % kRows;
     const float *po = (const float *)((const char *)a.ws + pl.part) + ((int64_t)slot * kRows + r0 % kRows) * D;
