@@ -22,18 +22,16 @@ constexpr int kRows = 16; // query rows of a workgroup
 constexpr int kWaves = 4;
 constexpr int kWholeTiles = 16;
 
-// Work is cut along the cache into as many equal stretches as there are workgroups on the chip at
-// a time: all tiles of all units (a unit is the kRows query rows of one sequence and key/value
-// head) form one list, in order, and workgroup w takes tiles [w * per, (w + 1) * per) of it,
-// whatever sequences they belong to. Lengths are known on the device only, so each workgroup
-// finds its place by a prefix sum over the sequences. A unit that lies in several workgroups is
-// joined from their parts by a second launch; workgroup w's part of unit u is in slot w + u of the
-// workspace (along the list one of the two grows by one, so no two parts share a slot).
-// Sequences of at most kWholeTiles tiles take a workgroup for each unit and no second launch: for
-// 300 tokens that saves 4 of 12 us.
+// Work is cut along the cache into pieces of at most `per` tiles, a workgroup to each: a unit (the
+// kRows query rows of one sequence and key/value head) has ceil(tiles / per) of them, and per is
+// the whole call's tiles shared out to as many workgroups as the chip holds at a time, up to whole
+// rounds of the waves. There are then at most units + groups pieces, which the host can launch
+// without the lengths; each workgroup finds its piece by prefix sums over the sequences, and those
+// past the last leave at once. A unit of several pieces is joined by a second launch.
+// Sequences of at most kWholeTiles tiles take a workgroup for each unit and no second launch.
 struct CachedPlan {
     int rows, row_tiles; // query rows of a key/value head, in tiles of kRows
-    int groups;          // workgroups; 0: one for each unit
+    int groups;          // workgroups that share the tiles; 0: one for each unit
     int slots;           // max_len up to whole tiles
     size_t ml, part, scores, bytes; // workspace offsets
 };
@@ -78,31 +76,23 @@ __device__ __forceinline__ int tiles_of(const CachedArgs &a, int s)
     return (held_tokens(a, s) + kTile - 1) / kTile;
 }
 
-// A workgroup's share of `total` tiles of the sequences' units: equal, and one tile for each wave
-// at least.
+// Tiles of a piece where the sequences' units have `total` tiles together.
 __device__ __forceinline__ int share(int total, const CachedArgs &a, const CachedPlan &pl)
 {
     const int per = (total * a.c.heads * pl.row_tiles + pl.groups - 1) / pl.groups;
-    return per < kWaves ? kWaves : per;
+    return (per < kWaves ? kWaves : per + kWaves - 1) / kWaves * kWaves;
 }
 
-// Tiles of sequences 0..s-1.
-__device__ __forceinline__ int tiles_before(const CachedArgs &a, int s)
+// Sum of f(sequence) over sequences 0..s-1.
+template <class F>
+__device__ __forceinline__ int sum_before(int s, F f)
 {
     int sum = 0;
     for (int base = 0; base < s; base += 64) {
         const int q = base + (threadIdx.x & 63);
-        sum += __builtin_amdgcn_readlane(wave_prefix(q < s ? tiles_of(a, q) : 0), 63);
+        sum += __builtin_amdgcn_readlane(wave_prefix(q < s ? f(q) : 0), 63);
     }
     return sum;
-}
-
-// Parts of a unit: `first` is the list's first tile of the unit, which has `tiles` of them.
-__device__ __forceinline__ void parts_of(int first, int tiles, int per, int unit, int *slot, int *count)
-{
-    const int w0 = first / per;
-    *slot = w0 + unit;
-    *count = tiles ? (first + tiles - 1) / per - w0 + 1 : 0;
 }
 
 template <int DT, int D>
@@ -122,50 +112,46 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
     const int group = a.q_heads / a.c.heads;
     const int blocks = a.c.page / kKvBlock;
 
-    // A stretch of one unit's tokens: unit `sub` of sequence s, which holds `len` tokens.
-    struct Seg {
-        int s, sub, len, begin, end;
-    };
-    Seg c;
-    int left = 0; // tiles of the workgroup after those of c
+    int s, sub, len, begin, end; // the piece: tokens begin..end-1 of unit `sub` of sequence s
     if (pl.groups) {
-        const int len = lane < a.n ? held_tokens(a, lane) : 0; // of the first 64 sequences
-        const int incl = wave_prefix((len + kTile - 1) / kTile);
-        int total = __builtin_amdgcn_readlane(incl, 63);
-        if (a.n > 64) total = tiles_before(a, a.n);
+        const int held = lane < a.n ? held_tokens(a, lane) : 0; // of the first 64 sequences
+        const int held_tiles = (held + kTile - 1) / kTile;
+        int total = __builtin_amdgcn_readlane(wave_prefix(held_tiles), 63);
+        if (a.n > 64) total = sum_before(a.n, [&](int q) { return tiles_of(a, q); });
         const int per = share(total, a, pl);
-        const int first = blockIdx.x * per; // in the list, which counts each sequence per_unit times
-        if (first >= total * per_unit) return;
-        const int seq_tile = first / per_unit; // tiles of whole sequences at most this many before
-        int index, tiles;
+        // pieces of one unit of each sequence, before this workgroup's (in whole sequences at
+        // most this many)
+        const int at = blockIdx.x / per_unit;
+        int index;
         if (a.n <= 64) {
-            c.s = __builtin_ctzll(__ballot(incl > seq_tile));
-            c.len = __builtin_amdgcn_readlane(len, c.s);
-            tiles = (c.len + kTile - 1) / kTile;
-            index = first - (__builtin_amdgcn_readlane(incl, c.s) - tiles) * per_unit;
+            const int own = (held_tiles + per - 1) / per, incl = wave_prefix(own);
+            const uint64_t after = __ballot(incl > at);
+            if (!after) return;
+            s = __builtin_ctzll(after);
+            len = __builtin_amdgcn_readlane(held, s);
+            index = at - (__builtin_amdgcn_readlane(incl, s) - __builtin_amdgcn_readlane(own, s));
         } else {
-            locate_unit(seq_tile, a.n, [&](int q) { return tiles_of(a, q); }, &c.s, &index);
-            c.len = __builtin_amdgcn_readfirstlane(held_tokens(a, c.s));
-            tiles = (c.len + kTile - 1) / kTile;
-            index = first - (seq_tile - index) * per_unit;
+            if (!locate_unit(at, a.n, [&](int q) { return (tiles_of(a, q) + per - 1) / per; }, &s, &index))
+                return;
+            len = __builtin_amdgcn_readfirstlane(held_tokens(a, s));
         }
-        c.sub = index / tiles;
-        const int tile = index % tiles, count = tiles - tile < per ? tiles - tile : per;
-        left = per - count;
-        c.begin = tile * kTile;
-        c.end = tile + count == tiles ? c.len : (tile + count) * kTile;
+        const int pieces = (len + kTile * per - 1) / (kTile * per);
+        index = index * per_unit + blockIdx.x % per_unit; // among the sequence's pieces
+        sub = index / pieces;
+        begin = index % pieces * per * kTile;
+        end = begin + per * kTile < len ? begin + per * kTile : len;
     } else {
-        c.s = blockIdx.x / per_unit;
-        c.sub = blockIdx.x % per_unit;
-        c.len = __builtin_amdgcn_readfirstlane(held_tokens(a, c.s));
-        c.begin = 0;
-        c.end = c.len;
+        s = blockIdx.x / per_unit;
+        sub = blockIdx.x % per_unit;
+        len = __builtin_amdgcn_readfirstlane(held_tokens(a, s));
+        begin = 0;
+        end = len;
     }
 
+    const int h = sub / pl.row_tiles;
     // A tile's loads are issued as soon as the registers of the tile before are free: K's after
-    // the first product, V's after the second, also where the tile before is another unit's. The
-    // page numbers come through the scalar cache, so that waiting for them waits for no vector
-    // load.
+    // the first product, V's after the second. The page numbers come through the scalar cache,
+    // so that waiting for them waits for no vector load.
     constexpr int STEP = kWaves * kTile;
     u32x2_t k[4][KS];
     u32x4_t v[VT];
@@ -174,21 +160,20 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
         int b0, b1, b2, b3;
     };
     // blocks (of the cache) of the four 16-token parts of a tile, -1 where there is none
-    const auto tile_blocks = [&](const Seg &u, int t) {
+    const auto tile_blocks = [&](int t) {
         typedef const int32_t __attribute__((address_space(4))) *scalar_t;
-        const scalar_t table = (scalar_t)(uintptr_t)(a.table + (int64_t)u.s * a.max_pages);
-        const int h = u.sub / pl.row_tiles;
+        const scalar_t table = (scalar_t)(uintptr_t)(a.table + (int64_t)s * a.max_pages);
         int at[4], pi[4], page[4], b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            at[i] = t + i * kKvBlock < u.end ? t + i * kKvBlock : u.end - 1;
+            at[i] = t + i * kKvBlock < end ? t + i * kKvBlock : end - 1;
             pi[i] = page_of(a.c, at[i]);
             page[i] = table[pi[i]];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             b[i] = (page[i] * a.c.heads + h) * blocks + slot_of(a.c, at[i], pi[i]) / kKvBlock;
-            const bool live = ((uint32_t)page[i] < (uint32_t)a.c.pages) & (t + i * kKvBlock < u.end);
+            const bool live = ((uint32_t)page[i] < (uint32_t)a.c.pages) & (t + i * kKvBlock < end);
             b[i] = live ? b[i] : -1;
         }
         return Blocks{b[0], b[1], b[2], b[3]};
@@ -223,17 +208,12 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
     };
     const int tv = g * kKvBlock; // the lane's block of a tile
     int vb = -1;
-    bool loaded = false; // the wave's first tile of c is on its way
-
-    for (;;) { // the workgroup's units
-    const int unit = c.s * per_unit + c.sub;
-    const int h = c.sub / pl.row_tiles;
-    const bool whole = c.begin == 0 && c.end == c.len;
-    const int row = c.sub % pl.row_tiles * kRows + n;
+    const bool whole = begin == 0 && end == len;
+    const int row = sub % pl.row_tiles * kRows + n;
     const int qi = row / group, qh = h * group + row % group;
     const bool real = row < pl.rows;
     // tokens this lane's row sees
-    const int see = real ? clampi(c.len - a.q_len + qi + 1, 0, c.len) : 0;
+    const int see = real ? clampi(len - a.q_len + qi + 1, 0, len) : 0;
 
     // the row's query, in the order in which the lanes hold K
     x8 q[KS];
@@ -241,7 +221,7 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
     for (int i = 0; i < KS; ++i) {
         const int d = WIDE ? i / 2 * 64 + g * 16 + i % 2 * 8 : i * 32 + g * 8;
         u32x4_t v = {0, 0, 0, 0};
-        if (real) v = *(const u32x4_t *)(a.q.p + (int64_t)(c.s * a.q_len + qi) * a.q.ts + qh * a.q.hs + d);
+        if (real) v = *(const u32x4_t *)(a.q.p + (int64_t)(s * a.q_len + qi) * a.q.ts + qh * a.q.hs + d);
         q[i] = __builtin_bit_cast(x8, v);
     }
 
@@ -253,36 +233,16 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
     for (int i = 0; i < VT; ++i) o[i] = f32x4_t{0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
 
-    int t0 = c.begin + wave * kTile;
-    if (!loaded && t0 < c.end) {
-        const Blocks r = tile_blocks(c, t0);
+    int t0 = begin + wave * kTile;
+    if (t0 < end) {
+        const Blocks r = tile_blocks(t0);
         vb = pick(r, g);
         load_k(pick(r, n >> 2), vb);
         load_v(vb);
     }
-    loaded = false;
-    // what the workgroup does next
-    Seg next = {a.n, 0, 0, 0, 0};
-    if (left > 0) {
-        next = c;
-        if (++next.sub == per_unit) { // the next sequence that holds tokens
-            next.sub = 0;
-            do {
-                ++next.s;
-                next.len = next.s < a.n ? __builtin_amdgcn_readfirstlane(held_tokens(a, next.s)) : 1;
-            } while (next.len == 0);
-        }
-        next.begin = 0;
-        next.end = next.len < left * kTile ? next.len : left * kTile;
-    }
-    for (; t0 < c.end; t0 += STEP) {
-        // the wave's next tile, of this unit or the next
-        const bool stay = t0 + STEP < c.end;
-        const Seg &u = stay ? c : next;
-        const int t1 = stay ? t0 + STEP : next.begin + wave * kTile;
-        const bool more = u.s < a.n && t1 < u.end;
+    for (; t0 < end; t0 += STEP) {
         Blocks r = {-1, -1, -1, -1};
-        if (more) r = tile_blocks(u, t1);
+        if (t0 + STEP < end) r = tile_blocks(t0 + STEP);
 
         // tokens of this lane's block that its row sees (0 where there is no block)
         const int sees = vb >= 0 ? see - (t0 + tv) : 0;
@@ -302,16 +262,15 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
             }
         }
         // slots past the last token, and pages that do not exist, hold anything
-        const bool ragged = t0 + kTile > c.end || __any(vb < 0);
-        const int slots = vb >= 0 ? c.end - (t0 + tv) : 0;
+        const bool ragged = t0 + kTile > end || __any(vb < 0);
+        const int slots = vb >= 0 ? end - (t0 + tv) : 0;
         // Loaded also where there is no next tile (block 0 stands in): a load under a condition
         // would be copied, and so waited for, where the paths meet.
         vb = pick(r, g);
         load_k(pick(r, n >> 2), vb);
-        loaded = more;
 
         if (a.weights && real) {
-            float *dst = (float *)((char *)a.ws + pl.scores) + ((int64_t)unit * kRows + n) * pl.slots + t0 + tv;
+            float *dst = (float *)((char *)a.ws + pl.scores) + ((int64_t)(s * per_unit + sub) * kRows + n) * pl.slots + t0 + tv;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 *(f32x4_t *)(dst + 4 * t) = f32x4_t{sc[4 * t], sc[4 * t + 1], sc[4 * t + 2], sc[4 * t + 3]};
@@ -388,11 +347,11 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
         sum += part_l[w][n] * f[w];
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t slot = pl.groups ? unit + blockIdx.x : unit;
+    const int64_t slot = blockIdx.x;
     if ((!whole || a.weights) && wave == 0 && g == 0)
         ((f32x2_t *)((char *)a.ws + pl.ml))[slot * kRows + n] = f32x2_t{top, sum};
     if (real) {
-        uint16_t *out = a.out + (int64_t)(c.s * a.q_len + qi) * a.out_ts + qh * a.out_hs;
+        uint16_t *out = a.out + (int64_t)(s * a.q_len + qi) * a.out_ts + qh * a.out_hs;
         float *part = (float *)((char *)a.ws + pl.part) + (slot * kRows + n) * D;
 #pragma unroll
         for (int j = 0; j < (VT + kWaves - 1) / kWaves; ++j) { // each wave finishes some dimensions
@@ -408,11 +367,6 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
             else
                 *(f32x4_t *)(part + i * 16 + g * 4) = v;
         }
-    }
-    if (next.s >= a.n) return;
-    left -= (next.end + kTile - 1) / kTile;
-    c = next;
-    __syncthreads(); // part_o is read to the end
     }
 }
 
@@ -437,22 +391,25 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
     const int chunks = (pl.slots + kJoinThreads - 1) / kJoinThreads;
     const int sh = adds ? ((int)blockIdx.x - join) / chunks : (int)blockIdx.x / pl.rows;
     const int s = sh / a.c.heads, h = sh % a.c.heads;
-    // its sequence's tokens, the tiles of those before, and a workgroup's share of all
-    int len, before = 0, per = 0;
+    // its sequence's tokens, the pieces of one unit of it and of those before
+    int len, before = s, pieces = 1;
     if (!pl.groups) {
         len = held_tokens(a, s);
     } else if (a.n <= 64) { // one load
         const int lane = tid & 63, held = lane < a.n ? held_tokens(a, lane) : 0;
-        const int incl = wave_prefix((held + kTile - 1) / kTile);
+        const int tiles = (held + kTile - 1) / kTile;
+        const int per = share(__builtin_amdgcn_readlane(wave_prefix(tiles), 63), a, pl);
+        const int own = (tiles + per - 1) / per, incl = wave_prefix(own);
         len = __builtin_amdgcn_readlane(held, s);
-        before = __builtin_amdgcn_readlane(incl, s) - (len + kTile - 1) / kTile;
-        per = share(__builtin_amdgcn_readlane(incl, 63), a, pl);
+        pieces = __builtin_amdgcn_readlane(own, s);
+        before = __builtin_amdgcn_readlane(incl, s) - pieces;
     } else {
+        const int per = share(sum_before(a.n, [&](int q) { return tiles_of(a, q); }), a, pl);
+        const auto pieces_of = [&](int q) { return (tiles_of(a, q) + per - 1) / per; };
         len = held_tokens(a, s);
-        before = tiles_before(a, s);
-        per = share(tiles_before(a, a.n), a, pl);
+        pieces = pieces_of(s);
+        before = sum_before(s, pieces_of);
     }
-    const int tiles = (len + kTile - 1) / kTile;
 
     if (adds) {
         const int first = ((int)blockIdx.x - join) % chunks * kJoinThreads, t = first + tid;
@@ -468,15 +425,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
             float score[kRows]; // on their way while the maxima are found
 #pragma unroll
             for (int q = 0; q < kRows; ++q) score[q] = sc[(int64_t)(q < rows ? q : 0) * pl.slots];
-            int slot = (int)x0 + rt, parts = 1;
-            if (pl.groups) parts_of(before * per_unit + (h * pl.row_tiles + rt) * tiles, tiles, per, (int)x0 + rt, &slot, &parts);
-            const f32x2_t *p = ml + (int64_t)slot * kRows + r;
+            const int64_t slot = (int64_t)before * per_unit + (h * pl.row_tiles + rt) * pieces;
+            const f32x2_t *p = ml + slot * kRows + r;
             float top = -INFINITY, l = 0.0f;
-            for (int i = tid % 16; i < parts; i += 16) top = fmaxf(top, p[(int64_t)i * kRows][0]);
+            for (int i = tid % 16; i < pieces; i += 16) top = fmaxf(top, p[(int64_t)i * kRows][0]);
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
             const float base = top == -INFINITY ? 0.0f : top;
-            for (int i = tid % 16; i < parts; i += 16) {
+            for (int i = tid % 16; i < pieces; i += 16) {
                 const f32x2_t v = p[(int64_t)i * kRows];
                 l += v[1] * __builtin_amdgcn_exp2f(v[0] - base);
             }
@@ -499,19 +455,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
     const int r0 = blockIdx.x % pl.rows;
     const int qi = r0 / group, qh = h * group + r0 % group;
     const int sub = h * pl.row_tiles + r0 / kRows;
-    int slot, parts;
-    parts_of(before * per_unit + sub * tiles, tiles, per, s * per_unit + sub, &slot, &parts);
-    if (parts == 1) return; // written by its only workgroup
-    ml += (int64_t)slot * kRows + r0 % kRows;
-    const float *po = (const float *)((const char *)a.ws + pl.part) + ((int64_t)slot * kRows + r0 % kRows) * D;
+    if (pieces == 1) return; // written by its only workgroup
+    const int64_t slot = (int64_t)before * per_unit + sub * pieces;
+    ml += slot * kRows + r0 % kRows;
+    const float *po = (const float *)((const char *)a.ws + pl.part) + (slot * kRows + r0 % kRows) * D;
     const int lane = tid & 63;
     // every wave finds the row's maximum and sum for itself
     float top = -INFINITY, l = 0.0f;
-    for (int i = lane; i < parts; i += 64) top = fmaxf(top, ml[(int64_t)i * kRows][0]);
+    for (int i = lane; i < pieces; i += 64) top = fmaxf(top, ml[(int64_t)i * kRows][0]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     const float base = top == -INFINITY ? 0.0f : top;
-    for (int i = lane; i < parts; i += 64) {
+    for (int i = lane; i < pieces; i += 64) {
         const f32x2_t v = ml[(int64_t)i * kRows];
         l += v[1] * __builtin_amdgcn_exp2f(v[0] - base);
     }
@@ -522,7 +477,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
     if (g < G) {
         f32x4_t o = {0, 0, 0, 0};
 #pragma unroll 4
-        for (int i = g; i < parts; i += G)
+        for (int i = g; i < pieces; i += G)
             o += *(const f32x4_t *)(po + (int64_t)i * kRows * D + c * 4) *
                  __builtin_amdgcn_exp2f(ml[(int64_t)i * kRows][0] - base);
         *(f32x4_t *)&acc[g][c * 4] = o;
@@ -530,7 +485,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
     __syncthreads();
     if (tid >= Q) return;
     f32x4_t o = {0, 0, 0, 0};
-    for (int i = 0; i < G && i < parts; ++i) o += *(const f32x4_t *)&acc[i][tid * 4];
+    for (int i = 0; i < G && i < pieces; ++i) o += *(const f32x4_t *)&acc[i][tid * 4];
     uint16_t *dst = a.out + (int64_t)(s * a.q_len + qi) * a.out_ts + qh * a.out_hs + tid * 4;
     *(u32x2_t *)dst = u32x2_t{Elem<DT>::pack(o[0] * inv, o[1] * inv), Elem<DT>::pack(o[2] * inv, o[3] * inv)};
 }
@@ -540,9 +495,9 @@ hipError_t cached(const CachedArgs &a, hipStream_t st)
 {
     const CachedPlan pl = cached_plan(a.n, a.q_heads, a.c.heads, D, a.q_len, a.max_len, a.weights != nullptr);
     const int64_t units = (int64_t)a.n * a.c.heads * pl.row_tiles;
-    // the list of tiles, and a slot for each unit and workgroup, are counted in 32 bits
+    // tiles, and the pieces of all units, are counted in 32 bits
     if (units * (pl.slots / kTile + 1) + resident(D) > INT32_MAX) return hipErrorInvalidValue;
-    const unsigned grid = (unsigned)(pl.groups ? pl.groups : units);
+    const unsigned grid = (unsigned)(units + pl.groups);
     attn_cached_kernel<DT, D><<<grid, 64 * kWaves, 0, st>>>(a, pl);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
