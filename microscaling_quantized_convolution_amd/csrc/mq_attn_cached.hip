@@ -12,6 +12,11 @@
 // tokens of one block: the operand that the second product wants from that group, under one
 // scale of K and one of V. The cache keeps a block's values token by token within a dimension,
 // so the other operand is a 16-byte load.
+//
+// Bound by the bytes of the cache, read once: 131071 tokens, 32 query heads on 8 of 128, are 269 MB
+// in 53 us, 5.1 TB/s (reads of 8 KB pieces in any order reach 5.8 on this card; the whole call
+// takes 58 us). 32 sequences of up to 4096 tokens, 107 MB, take 30 us: their longest unit is 64
+// tiles of one workgroup, one after another at 0.4 us each.
 #include "mq_attn_device.hpp"
 
 namespace mq {
@@ -20,15 +25,24 @@ namespace {
 constexpr int kTile = 64; // tokens a wave takes at a time: one block for each lane group
 constexpr int kRows = 16; // query rows of a workgroup
 constexpr int kWaves = 4;
-constexpr int kWholeTiles = 16;
+constexpr int kCus = 256;
 
-// Work is cut along the cache into pieces of at most `per` tiles, a workgroup to each: a unit (the
-// kRows query rows of one sequence and key/value head) has ceil(tiles / per) of them, and per is
-// the whole call's tiles shared out to as many workgroups as the chip holds at a time, up to whole
-// rounds of the waves. There are then at most units + groups pieces, which the host can launch
-// without the lengths; each workgroup finds its piece by prefix sums over the sequences, and those
-// past the last leave at once. A unit of several pieces is joined by a second launch.
-// Sequences of at most kWholeTiles tiles take a workgroup for each unit and no second launch.
+// Work is cut along the cache into pieces, a workgroup to each. With `per` the whole call's tiles
+// shared out to as many workgroups as the chip holds at a time, a unit (the kRows query rows of
+// one sequence and key/value head) has as many equal pieces as tiles / per rounds to, one at
+// least, in whole rounds of the waves (rounded up instead: 32 sequences of 1000 to 2000 tokens,
+// 16 heads on 4 of 256, 35 us in place of 28; others within 10% either way). There are then at
+// most units + groups pieces, which the host can launch without the lengths; each workgroup finds
+// its piece by prefix sums over the sequences, and those past the last leave at once. A unit of
+// several pieces is joined by a second launch.
+//
+// Without pieces, a workgroup takes a whole unit and there is no second launch (3 us and more).
+// That is done where no sequence has more than 16 tiles, or at most 64 and there is a unit for
+// every CU: then the units keep the chip busy by themselves unless a few of them hold most of the
+// tokens. Whole against cut, 32 query heads on 8 of 128: 1 x 1000 tokens 10.0 and 10.8 us, 1 x
+// 2000 15.2 and 10.7; 16 sequences (128 units) of 1 to 4000 tokens 25 and 20.7; 32 (256 units) of
+// 1 to 2000 16.6 and 21.5, of 1 to 4000 26.8 and 31.5, one of 4000 among 500s 24.8 and 18.2; 64 of
+// 2000 to 4000 76 and 80.
 struct CachedPlan {
     int rows, row_tiles; // query rows of a key/value head, in tiles of kRows
     int groups;          // workgroups that share the tiles; 0: one for each unit
@@ -36,8 +50,10 @@ struct CachedPlan {
     size_t ml, part, scores, bytes; // workspace offsets
 };
 
-// Workgroups that fit the 256 CUs together (by registers: 3, 2 or 1 to a CU).
-constexpr int resident(int d) { return 256 * (d <= 64 ? 3 : (d <= 128 ? 2 : 1)); }
+// Workgroups that fit the 256 CUs together (by registers: 3, 2 or 1 to a CU). Tiles shared out to
+// half or twice as many, heads of 128: 1 x 131071 tokens 58.3 and 60.6 us against 57.8; 16
+// sequences of 1 to 4000 tokens 24 and 24 against 20.
+constexpr int resident(int d) { return kCus * (d <= 64 ? 3 : (d <= 128 ? 2 : 1)); }
 
 CachedPlan cached_plan(int n, int q_heads, int kv_heads, int d, int q_len, int max_len, bool weights)
 {
@@ -46,7 +62,7 @@ CachedPlan cached_plan(int n, int q_heads, int kv_heads, int d, int q_len, int m
     p.row_tiles = (p.rows + kRows - 1) / kRows;
     const int64_t units = (int64_t)n * kv_heads * p.row_tiles;
     const int64_t tiles = ((int64_t)max_len + kTile - 1) / kTile;
-    p.groups = tiles <= kWholeTiles ? 0 : resident(d);
+    p.groups = tiles <= 16 || (tiles <= 64 && units >= kCus) ? 0 : resident(d);
     p.slots = (int)(tiles * kTile);
     const size_t parts = (size_t)units + p.groups;
     p.ml = 0;
@@ -76,11 +92,21 @@ __device__ __forceinline__ int tiles_of(const CachedArgs &a, int s)
     return (held_tokens(a, s) + kTile - 1) / kTile;
 }
 
-// Tiles of a piece where the sequences' units have `total` tiles together.
+// A workgroup's share of `total` tiles of the sequences' units.
+template <int D>
 __device__ __forceinline__ int share(int total, const CachedArgs &a, const CachedPlan &pl)
 {
-    const int per = (total * a.c.heads * pl.row_tiles + pl.groups - 1) / pl.groups;
-    return (per < kWaves ? kWaves : per + kWaves - 1) / kWaves * kWaves;
+    const int per = (total * a.c.heads * pl.row_tiles + resident(D) - 1) / resident(D);
+    return per < kWaves ? kWaves : per;
+}
+
+// Pieces of a unit of `tiles` tiles, of *size tiles each (the last one may have fewer).
+__device__ __forceinline__ int cut(int tiles, int per, int *size)
+{
+    const int want = (int)((float)tiles * __builtin_amdgcn_rcpf((float)per) + 0.5f);
+    const int count = want < 1 ? 1 : want;
+    *size = ((tiles + count - 1) / count + kWaves - 1) / kWaves * kWaves;
+    return tiles ? (tiles + *size - 1) / *size : 0;
 }
 
 // Sum of f(sequence) over sequences 0..s-1.
@@ -96,7 +122,7 @@ __device__ __forceinline__ int sum_before(int s, F f)
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_kernel(CachedArgs a, CachedPlan pl)
+__global__ void __launch_bounds__(64 * kWaves, resident(D) / kCus) attn_cached_kernel(CachedArgs a, CachedPlan pl)
 {
     typedef typename Elem<DT>::x8 x8;
     constexpr int KS = D / 32;         // steps of 32 dimensions in the first product
@@ -118,28 +144,30 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
         const int held_tiles = (held + kTile - 1) / kTile;
         int total = __builtin_amdgcn_readlane(wave_prefix(held_tiles), 63);
         if (a.n > 64) total = sum_before(a.n, [&](int q) { return tiles_of(a, q); });
-        const int per = share(total, a, pl);
+        const int per = share<D>(total, a, pl);
         // pieces of one unit of each sequence, before this workgroup's (in whole sequences at
         // most this many)
         const int at = blockIdx.x / per_unit;
-        int index;
+        int index, pieces, size;
         if (a.n <= 64) {
-            const int own = (held_tiles + per - 1) / per, incl = wave_prefix(own);
+            const int own = cut(held_tiles, per, &size), incl = wave_prefix(own);
             const uint64_t after = __ballot(incl > at);
             if (!after) return;
             s = __builtin_ctzll(after);
             len = __builtin_amdgcn_readlane(held, s);
-            index = at - (__builtin_amdgcn_readlane(incl, s) - __builtin_amdgcn_readlane(own, s));
+            pieces = __builtin_amdgcn_readlane(own, s);
+            size = __builtin_amdgcn_readlane(size, s);
+            index = at - (__builtin_amdgcn_readlane(incl, s) - pieces);
         } else {
-            if (!locate_unit(at, a.n, [&](int q) { return (tiles_of(a, q) + per - 1) / per; }, &s, &index))
+            if (!locate_unit(at, a.n, [&](int q) { return cut(tiles_of(a, q), per, &size); }, &s, &index))
                 return;
             len = __builtin_amdgcn_readfirstlane(held_tokens(a, s));
+            pieces = cut((len + kTile - 1) / kTile, per, &size);
         }
-        const int pieces = (len + kTile * per - 1) / (kTile * per);
         index = index * per_unit + blockIdx.x % per_unit; // among the sequence's pieces
         sub = index / pieces;
-        begin = index % pieces * per * kTile;
-        end = begin + per * kTile < len ? begin + per * kTile : len;
+        begin = index % pieces * size * kTile;
+        end = begin + size * kTile < len ? begin + size * kTile : len;
     } else {
         s = blockIdx.x / per_unit;
         sub = blockIdx.x % per_unit;
@@ -309,7 +337,8 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
             for (int j = 0; j < 4; ++j) {
                 const float a0 = p[8 * u + 2 * j], a1 = p[8 * u + 2 * j + 1];
                 ph[j] = Elem<MQ_BF16>::pack(a0, a1);
-                // the rest of p, so that both parts hold it to 16 bits (half-precision outputs)
+                // bf16 holds p to 2^-9, as the bf16 output will be; for half-precision outputs the
+                // rest of p goes in as a second part, and both hold it to 2^-17
                 pr[j] = Elem<MQ_BF16>::pack(a0 - __uint_as_float(ph[j] << 16),
                                             a1 - __uint_as_float(ph[j] & 0xFFFF0000u));
             }
@@ -372,7 +401,9 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / 256) attn_cached_ke
 
 // What is left once every part is done, in one launch: the first workgroups join the parts of a
 // query row along the cache (kJoinThreads / (D/4) parts at a time, four dimensions to a lane),
-// the others add the weights of 256 tokens, summed over the rows in order, to their places.
+// the others add the weights of 256 tokens, summed over the rows in order, to their places. Bound
+// by the latency of the launch and of three loads that wait for each other (lengths, maxima and
+// sums, parts): 5 us at 131071 tokens, 7 us with the weights of 8 x 8190.
 constexpr int kJoinThreads = 256;
 
 template <int DT, int D>
@@ -392,20 +423,20 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
     const int sh = adds ? ((int)blockIdx.x - join) / chunks : (int)blockIdx.x / pl.rows;
     const int s = sh / a.c.heads, h = sh % a.c.heads;
     // its sequence's tokens, the pieces of one unit of it and of those before
-    int len, before = s, pieces = 1;
+    int len, size, before = s, pieces = 1;
     if (!pl.groups) {
         len = held_tokens(a, s);
     } else if (a.n <= 64) { // one load
         const int lane = tid & 63, held = lane < a.n ? held_tokens(a, lane) : 0;
         const int tiles = (held + kTile - 1) / kTile;
-        const int per = share(__builtin_amdgcn_readlane(wave_prefix(tiles), 63), a, pl);
-        const int own = (tiles + per - 1) / per, incl = wave_prefix(own);
+        const int per = share<D>(__builtin_amdgcn_readlane(wave_prefix(tiles), 63), a, pl);
+        const int own = cut(tiles, per, &size), incl = wave_prefix(own);
         len = __builtin_amdgcn_readlane(held, s);
         pieces = __builtin_amdgcn_readlane(own, s);
         before = __builtin_amdgcn_readlane(incl, s) - pieces;
     } else {
-        const int per = share(sum_before(a.n, [&](int q) { return tiles_of(a, q); }), a, pl);
-        const auto pieces_of = [&](int q) { return (tiles_of(a, q) + per - 1) / per; };
+        const int per = share<D>(sum_before(a.n, [&](int q) { return tiles_of(a, q); }), a, pl);
+        const auto pieces_of = [&](int q) { return cut(tiles_of(a, q), per, &size); };
         len = held_tokens(a, s);
         pieces = pieces_of(s);
         before = sum_before(s, pieces_of);

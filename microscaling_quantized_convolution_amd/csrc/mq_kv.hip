@@ -9,7 +9,6 @@
 namespace mq {
 namespace {
 
-
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
 {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
@@ -63,8 +62,13 @@ __device__ __forceinline__ int capacity(int max_pages, int page)
 
 // ---- append --------------------------------------------------------------------------------
 //
+// code = x / 2^(e-127) in E4M3, rounded to nearest, under the smallest power of two that brings the
+// block's largest magnitude to 448 or less: the cache's 8 bits are the one rounding here. A block
+// that holds tokens already keeps the larger of both scales, its old codes are rounded again.
+//
 // One wave per touched block, head and side (keys, values). Bound by the bytes: 2 B in and 1 B
-// out per element. The block's largest magnitude is found on the 16-bit patterns (their
+// out per element; 65536 tokens of 8 heads of 128 are 403 MB in 81 us, 4.95 TB/s (a large copy
+// reaches 5.16). A step of a few tokens takes 8 us, all of it call and launch. The block's largest magnitude is found on the 16-bit patterns (their
 // magnitudes order like unsigned numbers), two at a time, while the elements stay in registers.
 // Every load is made, with the token clamped into the new ones, and what does not belong is
 // cleared afterwards: loads under a condition were waited for one by one.
@@ -218,10 +222,11 @@ typedef float f32x4_dword_t __attribute__((ext_vector_type(4), aligned(4)));
 // of a longer sequence is read again from the caches. The key of rank `need` is found by 11-bit
 // digits of its distance from the smallest key, shifted so that the largest distance just fits:
 // the weights' exponents, nearly equal, then spread over the bins instead of meeting in a few.
-// Two more passes over the keys count what each wave keeps and write it where it belongs. Bound
-// by the latency of these passes (the weights are 4 bytes a token): 32768 tokens took 110 us with
-// 8-bit digits of the keys read again in each pass, 57 us with keys in LDS but loaded one after
-// another.
+// Once at most 64 candidates share the decided digits, one wave ranks them instead (2 x 1000
+// tokens, the whole call: 14.0 -> 12.4 us). Two more passes over the keys count what each wave
+// keeps and write it where it belongs. Bound by the latency of these passes (the weights are 4
+// bytes a token): 32768 tokens of 8 sequences of 8 heads take 25 us; 110 with 8-bit digits of the
+// keys, read again in each pass, 57 with keys in LDS but loaded one after another.
 __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
 {
     __shared__ __align__(16) uint32_t held[kSelWaves][kSelSteps * kSelStep];
@@ -429,7 +434,9 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
 
 // One wave per new block and head: copies the keys and values of 16 kept tokens at the largest
 // of their scales, and their weights. Bound by the bytes: a kept token's key is one row, but its
-// value lies with the 15 others of its old block, which comes whole. (Copying in the workgroup
+// value lies with the 15 others of its old block, which comes whole: 8 x 8192 tokens kept of
+// 32768, 8 heads of 128, move 265 MB in 58 us, 4.6 TB/s (101 us with each block loaded only when
+// its tokens' turn came). (Copying in the workgroup
 // that found the tokens, without a second launch, left 8 of 256 CUs to do it and was no faster
 // at 2 x 1000 tokens.)
 template <int D>
