@@ -225,7 +225,7 @@ typedef float f32x4_dword_t __attribute__((ext_vector_type(4), aligned(4)));
 // Once at most 64 candidates share the decided digits, one wave ranks them instead (2 x 1000
 // tokens, the whole call: 14.0 -> 12.4 us). Two more passes over the keys count what each wave
 // keeps and write it where it belongs. Bound by the latency of these passes (the weights are 4
-// bytes a token): 32768 tokens of 8 sequences of 8 heads take 25 us; 110 with 8-bit digits of the
+// bytes a token): up to 32768 tokens, 8 sequences of 8 heads, take 26 us; 110 with 8-bit digits of the
 // keys, read again in each pass, 57 with keys in LDS but loaded one after another.
 __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
 {
@@ -434,9 +434,9 @@ __global__ void __launch_bounds__(64 * kSelWaves) kv_select_kernel(EvictArgs a)
 
 // One wave per new block and head: copies the keys and values of 16 kept tokens at the largest
 // of their scales, and their weights. Bound by the bytes: a kept token's key is one row, but its
-// value lies with the 15 others of its old block, which comes whole: 8 x 8192 tokens kept of
-// 32768, 8 heads of 128, move 265 MB in 58 us, 4.6 TB/s (101 us with each block loaded only when
-// its tokens' turn came). (Copying in the workgroup
+// value lies with the 15 others of its old block, which comes whole: 8 sequences of up to
+// 32768 tokens cut to 8192, 8 heads of 128, move 287 MB (counted) in 58 us, 4.9 TB/s (101 us with
+// each block loaded only when its tokens' turn came). (Copying in the workgroup
 // that found the tokens, without a second launch, left 8 of 256 CUs to do it and was no faster
 // at 2 x 1000 tokens.)
 template <int D>

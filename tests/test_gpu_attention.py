@@ -209,6 +209,17 @@ def test_cached_split(dtype):
     check_cached(cache, table, lens, q, 2, 0.125, max_len=0)  # the table's width
 
 
+@pytest.mark.parametrize("n,heads", [(70, 1), (130, 2)])
+def test_cached_many_ragged_sequences(n, heads):
+    """More sequences than a wave has lanes, some of them empty: few heads, so that long sequences
+    are cut along the cache, and enough for a workgroup to take a whole long sequence."""
+    lens = [(37 * i) % 90 for i in range(n)]
+    lens[3], lens[65], lens[n - 1] = 1500, 1100, 700
+    cache, table = filled(37, lens, 32, heads, 64)
+    q = randn(torch.Generator().manual_seed(14), n, 2 * heads, 64, dtype=BF16)
+    check_cached(cache, table, lens, q, 1, 0.125)
+
+
 def test_cached_sharp_and_signed_scales():
     """One token takes nearly all the weight; a negative and a zero scale."""
     lens = [100, 33]
