@@ -14,8 +14,8 @@
 // so the other operand is a 16-byte load.
 //
 // Bound by the bytes of the cache, read once: 131071 tokens, 32 query heads on 8 of 128, are 269 MB
-// in 53 us, 5.1 TB/s (reads of 8 KB pieces in any order reach 5.8 on this card; the whole call
-// takes 58 us). 32 sequences of up to 4096 tokens, 107 MB, take 30 us: their longest unit is 64
+// in 51 to 53 us, 5.1 to 5.3 TB/s (reads of 8 KB pieces in any order reach 5.8 on this card; the
+// whole call takes 56 to 58 us). 32 sequences of up to 4096 tokens, 107 MB, take 30 us: their longest unit is 64
 // tiles of one workgroup, one after another at 0.4 us each.
 #include "mq_attn_device.hpp"
 
