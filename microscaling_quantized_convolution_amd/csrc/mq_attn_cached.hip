@@ -15,8 +15,8 @@
 //
 // Bound by the bytes of the cache, read once: 131071 tokens, 32 query heads on 8 of 128, are 269 MB
 // in 51 to 53 us, 5.1 to 5.3 TB/s (reads of 8 KB pieces in any order reach 5.8 on this card; the
-// whole call takes 56 to 58 us). 32 sequences of up to 4096 tokens, 107 MB, take 30 us: their longest unit is 64
-// tiles of one workgroup, one after another at 0.4 us each.
+// whole call takes 56 to 58 us). 32 sequences of up to 4096 tokens, 107 MB, take 30 us: their
+// longest unit is 64 tiles of one workgroup, one after another at 0.4 us each.
 #include "mq_attn_device.hpp"
 
 namespace mq {
@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / kCus) attn_cached_k
         load_k(pick(r, n >> 2), vb);
 
         if (a.weights && real) {
-            float *dst = (float *)((char *)a.ws + pl.scores) + ((int64_t)(s * per_unit + sub) * kRows + n) * pl.slots + t0 + tv;
+            float *dst = (float *)((char *)a.ws + pl.scores) +
+                         ((int64_t)(s * per_unit + sub) * kRows + n) * pl.slots + t0 + tv;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 *(f32x4_t *)(dst + 4 * t) = f32x4_t{sc[4 * t], sc[4 * t + 1], sc[4 * t + 2], sc[4 * t + 3]};

@@ -13,9 +13,9 @@
 // the next tile runs beside this one's softmax.
 //
 // Bound by the matrix instructions, and by power: 2 x 8192 tokens, 32 query heads on 8 of 128, are
-// 1.10 TFLOP in 1.06 to 1.08 ms, 1020 to 1040 TFLOP/s, where a product of 8192 x 8192 matrices reaches 1260. The
-// matrix units are busy for 55% of the cycles, the vector units for another 55%, and the clock
-// falls to 1.8 GHz. 8 prompts of up to 2047 tokens (69 GFLOP) take 102 us: the last tiles leave
+// 1.10 TFLOP in 1.06 to 1.08 ms, 1020 to 1040 TFLOP/s, where a product of 8192 x 8192 matrices
+// reaches 1260. The matrix units are busy for 55% of the cycles, the vector units for another 55%,
+// and the clock falls to 1.8 GHz. 8 prompts of up to 2047 tokens (69 GFLOP) take 102 us: the last tiles leave
 // CUs idle, and the diagonal ones are half masked. 32 rows to a wave let one operand read serve
 // 32x32x16 products at two workgroups a CU; of 256 threads each, they cover each other's barriers.
 //
