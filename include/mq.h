@@ -470,7 +470,9 @@ mq_status mq_attn_cached(const mq_kv_cache *cache, const mq_rows *q, const mq_ro
  * rows [cu[s], cu[s+1]) of q, k, v and out; row i of a sequence sees its rows j <= i; query head
  * h reads key/value head h / (q_heads / kv_heads):
  *   p[j] = softmax_j(scale * sum_d q[d] * k[j][d])     out[d] = sum_j p[j] * v[j][d]
- * with the softmax and both sums in fp32 and p rounded to dtype for the second product.
+ * with the softmax and both sums in fp32 and p rounded to dtype for the second product: by 2^-8 of
+ * itself at most for MQ_BF16; for MQ_F16 by 2^-11 of itself, or where that is more by 2^-28 of the
+ * largest p in the row's same 64 tokens (64 i <= j < 64 (i + 1)).
  * max_len: no sequence is longer than this (rows past it are neither read nor written).
  * Errors: as for mq_attn_cached (without a workspace); MQ_ERR_UNSUPPORTED also for a token_stride
  *         of k or v above 2^24.

@@ -19,8 +19,11 @@
 // CUs idle, and the diagonal ones are half masked. 32 rows to a wave let one operand read serve
 // 32x32x16 products at two workgroups a CU; of 256 threads each, they cover each other's barriers.
 //
-// P is rounded to dtype (values of 2^8 or less, relative error 2^-9 or 2^-12) because the second
-// product takes 16-bit operands; m, l and O stay in fp32, and l sums P before it is rounded.
+// P is rounded to dtype because the second product takes 16-bit operands; m, l and O stay in fp32,
+// and l sums P before it is rounded. bf16: relative error 2^-8 at any size. f16: 2^-11 down to 2^-14
+// and steps of 2^-24 below, so P is held large: it is 2^11 where a score equals m, and m follows the
+// tiles' largest scores down as well as up (see Range). A token's P is then off by 2^-11 of itself
+// or 2^-28 of the largest P of its tile and row, whichever is more.
 #include "mq_attn_device.hpp"
 
 #include <cfloat>
@@ -121,6 +124,18 @@ __device__ __forceinline__ void odd_product(uint32_t at, const typename Elem<DT>
         }
     }
 }
+
+// Where P lies for each type, in powers of two; P is 2^bias where a score equals m.
+//   grow   m follows a tile's largest score up where that exceeds it by more
+//   fall   and down where that stays below it by more (f16 alone: bf16 has the range of fp32)
+//   span   but not past this much below the row's largest score: P stays a factor of 2^span below
+//          its peak in fp32 (O at most 2^(span + grow + bias + 16) times the tokens), and what lies
+//          further down is less than the smallest f16 even with the largest values
+// f16: P reaches 2^(grow + bias) = 2^15, below its largest number.
+template <int DT> struct Range {
+    static constexpr float grow = DT == MQ_F16 ? 4.0f : 8.0f, bias = DT == MQ_F16 ? 11.0f : 0.0f;
+    static constexpr float fall = 8.0f, span = 64.0f;
+};
 
 // 64 lanes x 16 bytes from base + off (bytes, per lane) to 1 KB of LDS at byte `lds`. The caller
 // waits (vmcnt) before the data is read. Nothing is returned in registers.
@@ -228,13 +243,13 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_prompt_kernel(Promp
         q[i] = __builtin_bit_cast(x8, v ^ a.q_flip);
     }
     f32x16_t o[DT32];
-    float m, l;
+    float m, l, peak; // peak (f16): the row's largest score so far
     const auto begin = [&] {
 #pragma unroll
         for (int d = 0; d < DT32; ++d)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
-        m = -INFINITY;
+        m = peak = -INFINITY;
         l = 0.0f;
         stage_k(0);
         stage_v(0);
@@ -264,24 +279,28 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_prompt_kernel(Promp
                 for (int r = 0; r < 16; ++r)
                     if (i * kN + token(b, r) > row) sc[b][r] = -INFINITY;
         }
-        float top = m;
+        float top = DT == MQ_F16 ? -INFINITY : m;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[b][r]);
         top = fmaxf(top, __shfl_xor(top, 32));
-        // m follows the largest score only where that has grown by a factor of 2^8 in p (or is the
-        // first): until then p stays at 2^8 or below and nothing need be rescaled
-        const bool grown = (top - m) * a.scale_log2e > 8.0f || (m == -INFINITY && top > m);
-        if (__any(grown)) {
+        // m follows the largest score only where that has grown by more than 2^grow in p (or is the
+        // first): until then p stays in range and nothing need be rescaled
+        bool moved = (top - m) * a.scale_log2e > Range<DT>::grow || (m == -INFINITY && top > m);
+        if constexpr (DT == MQ_F16) {
+            peak = fmaxf(peak, top);
+            moved |= (m - top) * a.scale_log2e > Range<DT>::fall && (peak - top) * a.scale_log2e < Range<DT>::span;
+        }
+        if (__any(moved)) {
             const float was = m;
-            if (grown) m = top; // row by row: no row's bits depend on another's scores
-            const float keep = grown ? __builtin_amdgcn_exp2f((was - m) * a.scale_log2e) : 1.0f;
+            if (moved) m = top; // row by row: no row's bits depend on another's scores
+            const float keep = moved ? __builtin_amdgcn_exp2f((was - m) * a.scale_log2e) : 1.0f;
             l *= keep;
 #pragma unroll
             for (int d = 0; d < DT32; ++d) o[d] *= keep;
         }
-        const float base = m == -INFINITY ? 0.0f : m * a.scale_log2e;
+        const float base = m == -INFINITY ? 0.0f : m * a.scale_log2e - Range<DT>::bias;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             u32x4_t pw;

@@ -1,0 +1,83 @@
+"""GPU tests of the attention calls where the numbers' range decides: probabilities many orders below
+the largest, against the definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import attn_reference as ref
+import microscaling_quantized_convolution_amd as mq
+
+pytestmark = pytest.mark.gpu
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ---- probabilities far below the largest -------------------------------------------------------
+
+def prompt_bound(q, k, v, scale):
+    """(out, bound) of one prompt of q [n][heads][dim] on one key/value head. On top of the bound
+    for p rounded relative to itself, half precision has an absolute step: p is at least 2^-8 of its
+    scale in the largest of each 64 tokens that a row sees, that scale is 2^11 and the smallest
+    numbers are 2^-24 apart, so a token's p is off by 2^-25-11+8 = 2^-28 of that largest."""
+    n, heads, dim = q.shape
+    see = torch.ones(n, n, dtype=torch.bool).tril()
+    kk, vv = k[:, 0].double(), v[:, 0].double()
+    count = torch.arange(1, n + 1)[:, None]
+    out = torch.zeros(q.shape, dtype=torch.float64)
+    bound = torch.zeros_like(out)
+    tiles = -(-n // 64)
+    for h in range(heads):
+        qq = q[:, h].double()
+        p = torch.softmax(torch.where(see, qq @ kk.t() * scale, -math.inf), 1)
+        out[:, h] = p @ vv
+        size = torch.where(see, qq.abs() @ kk.abs().t() * abs(scale), 0.0).amax(1, keepdim=True)
+        bound[:, h] = ref.attn_bound(out[:, h], p @ vv.abs(), ref.U[q.dtype],
+                                     ref.score_error(dim, size), count, ref.U[q.dtype])
+        if q.dtype == F16:
+            for t in range(tiles):
+                part = slice(64 * t, min(n, 64 * t + 64))
+                top = torch.where(see[:, part], p[:, part], 0.0).amax(1, keepdim=True)
+                bound[:, h] += 2.0 ** -28 * top * (see[:, part].double() @ vv[part].abs())
+    return out, bound
+
+
+def hold_prompt(logits, size, dim, dtype, seed):
+    """A prompt whose token t has about logits[t] in every row and values of about size[t]."""
+    gen = torch.Generator().manual_seed(seed)
+    n = len(logits)
+    q, k = (0.3 * torch.randn(n, h, dim, generator=gen) for h in (2, 1))
+    q[..., 0], k[:, 0, 0] = 8.0, torch.tensor(logits, dtype=torch.float32)
+    v = torch.randn(n, 1, dim, generator=gen).abs() * torch.tensor(size)[:, None, None]
+    q, k, v = (x.to(dtype) for x in (q, k, v))
+    want, bound = prompt_bound(q, k, v, 0.125)
+    out = torch.full(q.shape, math.nan, dtype=dtype, device="cuda")
+    mq.mq_attn_prompt(q.cuda(), k.cuda(), v.cuda(), out, ints([0, n]), n, 0.125)
+    err = (out.cpu().double() - want).abs()
+    worst = (err / bound).max().item()
+    assert (err <= bound).all(), f"{worst} of the bound, {err.max()}"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("above", [6.0, 14.0, 18.0, 22.0, 30.0])
+@pytest.mark.parametrize("at", [0, 700])
+def test_prompt_under_one_heavy_token(dtype, dim, above, at):
+    """One token takes nearly all the weight but has no value: the result is what the others, `above`
+    below it, give."""
+    logits, size = [0.0] * 1500, [512.0] * 1500
+    logits[at], size[at] = above, 0.0
+    hold_prompt(logits, size, dim, dtype, int(above) + dim + at)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_prompt_steps_down_and_up(dtype):
+    """Scores that fall by 9 and by 30 from 96 tokens to the next, and rise again, the values growing
+    as the probabilities fall."""
+    steps = [0, -9, -18, -27, -36, -6, -36, -20, -50, -10, 2, -7]
+    logits = [float(s) for s in steps for _ in range(96)]
+    size = [min(2.0 ** 12, math.exp(-0.25 * s)) for s in logits]  # 16 times that is a finite half
+    hold_prompt(logits, size, 64, dtype, 5)
