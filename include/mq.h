@@ -404,7 +404,7 @@ typedef struct {
  * outside [0, num_pages) holds no tokens: nothing is read from it or written to it, and its
  * tokens take no part in attention.
  * k_codes and v_codes must be 16-byte aligned (MQ_ERR_ARG otherwise). No two sequences may share
- * a page that one of them writes.
+ * a page that one of them writes (mq_kv_append, and the new pages of mq_kv_evict).
  */
 typedef struct {
     int32_t num_pages, page_size, kv_heads, head_dim;
@@ -454,7 +454,10 @@ size_t mq_attn_cached_workspace_bytes(int32_t n_seqs, int32_t q_heads, int32_t k
  *          max_pages * page_size. It sizes the launch and the workspace.
  * weights_dev: null, or fp32 [num_pages][kv_heads][page_size]: for each cached token and
  *          key/value head, p summed over the head's query heads and the q_len rows is added to
- *          the token's place (in a fixed order: results are deterministic).
+ *          the token's place. Sequences may read the same pages: the places gain what all of them
+ *          give. The order is fixed, so results are deterministic, where such a page lies at the
+ *          same place of their rows of table_dev (a common beginning); what a page gains at
+ *          different places of the table is added in any order.
  * ws_dev / ws_bytes: device scratch, 16-byte aligned, of at least
  *          mq_attn_cached_workspace_bytes(...) bytes (may be null where that is 0).
  * Errors: MQ_ERR_ARG, MQ_ERR_SHAPE (q, out and the cache disagree; q_heads no multiple of

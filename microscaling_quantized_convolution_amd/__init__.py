@@ -454,7 +454,7 @@ def mq_attn_cached(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: t
                    max_len: int = 0, weights: Optional[torch.Tensor] = None, stream=None):
     """Attention of each sequence's last q_len tokens, q [sequences * q_len][q_heads][dim], over
     its lens[s] cached tokens (these included), into out. weights (fp32, cache.weights_shape)
-    gains the attention each cached token received."""
+    gains the attention each cached token received, from every sequence that reads its page."""
     dev = _current_device()
     shape = lens.shape
     n = shape[0]
