@@ -19,6 +19,8 @@
 // longest unit is 64 tiles of one workgroup, one after another at 0.4 us each.
 #include "mq_attn_device.hpp"
 
+#include <cfloat>
+
 namespace mq {
 namespace {
 
@@ -26,6 +28,7 @@ constexpr int kTile = 64; // tokens a wave takes at a time: one block for each l
 constexpr int kRows = 16; // query rows of a workgroup
 constexpr int kWaves = 4;
 constexpr int kCus = 256;
+constexpr float kUnseen = -FLT_MAX; // in the kept scores: a token that the row does not see
 
 // Work is cut along the cache into pieces, a workgroup to each. With `per` the whole call's tiles
 // shared out to as many workgroups as the chip holds at a time, a unit (the kRows query rows of
@@ -307,7 +310,8 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / kCus) attn_cached_k
                          ((int64_t)(s * per_unit + sub) * kRows + n) * pl.slots + t0 + tv;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                *(f32x4_t *)(dst + 4 * t) = f32x4_t{sc[4 * t], sc[4 * t + 1], sc[4 * t + 2], sc[4 * t + 3]};
+                *(f32x4_t *)(dst + 4 * t) = f32x4_t{4 * t < sees ? sc[4 * t] : kUnseen, 4 * t + 1 < sees ? sc[4 * t + 1] : kUnseen,
+                                                    4 * t + 2 < sees ? sc[4 * t + 2] : kUnseen, 4 * t + 3 < sees ? sc[4 * t + 3] : kUnseen};
         }
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -491,8 +495,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
                 if (tid % 16 == 0) row_ml[r] = f32x2_t{base, l == 0.0f ? 0.0f : 1.0f / l};
                 __syncthreads();
 #pragma unroll
-                for (int i = 0; i < kRows; ++i)
-                    if (i < rows) sum += __builtin_amdgcn_exp2f(score[i] - row_ml[i][0]) * row_ml[i][1];
+                for (int i = 0; i < kRows; ++i) {
+                    if (i >= rows) continue;
+                    const float p = __builtin_amdgcn_exp2f(score[i] - row_ml[i][0]) * row_ml[i][1];
+                    // nothing from a row that does not see the token: the row may be NaN
+                    sum += score[i] != kUnseen ? p : 0.0f;
+                }
             }
             return sum;
         };

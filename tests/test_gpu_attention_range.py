@@ -1,5 +1,5 @@
 """GPU tests of the attention calls where the numbers' range decides: probabilities many orders below
-the largest, against the definition in 64 bits."""
+the largest against the definition in 64 bits, and rows without a finite result."""
 import math
 
 import pytest
@@ -7,6 +7,7 @@ import torch
 
 import attn_reference as ref
 import microscaling_quantized_convolution_amd as mq
+from test_gpu_attention import filled, randn, run_cached
 
 pytestmark = pytest.mark.gpu
 BF16, F16 = torch.bfloat16, torch.float16
@@ -81,3 +82,29 @@ def test_prompt_steps_down_and_up(dtype):
     logits = [float(s) for s in steps for _ in range(96)]
     size = [min(2.0 ** 12, math.exp(-0.25 * s)) for s in logits]  # 16 times that is a finite half
     hold_prompt(logits, size, 64, dtype, 5)
+
+
+# ---- rows that are NaN -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens", [[70, 33], [70, 1500]])
+def test_weights_of_tokens_that_a_nan_row_does_not_see(lens):
+    """A row whose query holds a NaN gives NaN to the tokens that it sees and nothing to later ones."""
+    q_len, page = 4, 16
+    cache, table = filled(61, lens, page, 2, 64)
+    q = randn(torch.Generator().manual_seed(31), 2 * q_len, 4, 64, dtype=BF16)
+    got = []
+    for rows in ((), ((0, 1), (q_len + 1, 2))):  # row 0 of sequence 0, row 1 of sequence 1
+        for r, qh in rows:
+            q[r, qh, 3] = math.nan
+        w = torch.zeros(cache["k"].shape[:3], device="cuda")
+        run_cached(cache, table, lens, q, q_len, 0.125, w)
+        got.append(w.cpu())
+    clean, bad = got
+    for s, i, h in ((0, 0, 0), (1, 1, 1)):
+        sees = lens[s] - q_len + i + 1
+        at = [(table[s][t // page], t % page) for t in range(lens[s])]
+        for t, (p, slot) in enumerate(at):
+            assert math.isnan(bad[p, h, slot]) == (t < sees), t
+            if t >= sees:
+                assert bad[p, h, slot] == clean[p, h, slot] and clean[p, h, slot] > 0
+            assert bad[p, 1 - h, slot] == clean[p, 1 - h, slot]
