@@ -129,6 +129,14 @@ __device__ __forceinline__ int sum_before(int s, F f)
     return sum;
 }
 
+// What a row's result is multiplied by. The sum is 0 only where the row saw no token (maximum -inf,
+// result 0), or where all its scores are -inf (the maximum is then the lowest number: NaN).
+__device__ __forceinline__ float inverse(float sum, float top)
+{
+    if (sum != 0.0f) return 1.0f / sum;
+    return top == -INFINITY ? 0.0f : __builtin_nanf("");
+}
+
 template <int DT, int D>
 __global__ void __launch_bounds__(64 * kWaves, resident(D) / kCus) attn_cached_kernel(CachedArgs a, CachedPlan pl)
 {
@@ -284,7 +292,7 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / kCus) attn_cached_k
         const int sees = vb >= 0 ? see - (t0 + tv) : 0;
         const float kf = block_scale(a.scale_log2e, ke), vf = block_scale(1.0f, ve);
         float sc[16];
-        float top = -INFINITY;
+        float top = sees > 0 ? -FLT_MAX : -INFINITY; // -inf: a row that has seen nothing yet
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             f32x4_t acc = {0, 0, 0, 0};
@@ -316,7 +324,7 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / kCus) attn_cached_k
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         const float m_new = fmaxf(m, top);
-        const float base = m_new == -INFINITY ? 0.0f : m_new; // a row that has seen nothing yet
+        const float base = m_new == -INFINITY ? 0.0f : m_new;
         if (__any(m_new > m)) { // some row's maximum grew
             const float keep = __builtin_amdgcn_exp2f(m - base);
             l *= keep;
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / kCus) attn_cached_k
         f[w] = __builtin_amdgcn_exp2f(part_m[w][n] - base);
         sum += part_l[w][n] * f[w];
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = inverse(sum, top);
     const int64_t slot = blockIdx.x;
     if ((!whole || a.weights) && wave == 0 && g == 0)
         ((f32x2_t *)((char *)a.ws + pl.ml))[slot * kRows + n] = f32x2_t{top, sum};
@@ -492,7 +500,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
 #pragma unroll
                 for (int d = 1; d < 16; d <<= 1) l += __shfl_xor(l, d);
                 __syncthreads();
-                if (tid % 16 == 0) row_ml[r] = f32x2_t{base, l == 0.0f ? 0.0f : 1.0f / l};
+                if (tid % 16 == 0) row_ml[r] = f32x2_t{base, inverse(l, top)};
                 __syncthreads();
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) {
@@ -590,7 +598,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(CachedArgs a, C
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = inverse(l, top);
     const int g = tid / Q, c = tid % Q;
     if (g < G) {
         f32x4_t o = {0, 0, 0, 0};

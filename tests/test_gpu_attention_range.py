@@ -108,3 +108,24 @@ def test_weights_of_tokens_that_a_nan_row_does_not_see(lens):
             if t >= sees:
                 assert bad[p, h, slot] == clean[p, h, slot] and clean[p, h, slot] > 0
             assert bad[p, 1 - h, slot] == clean[p, 1 - h, slot]
+
+
+@pytest.mark.parametrize("n", [40, 1500])
+def test_rows_whose_scores_are_all_minus_infinity(n):
+    """The softmax of scores that are all -inf is NaN, as it is over a prompt; a row that sees no
+    token stays 0, and so does what it gives."""
+    cache, table = ref.empty_cache(2 + n // 16, 16, 1, 64), [list(range(2 + n // 16)), [-1] * (2 + n // 16)]
+    k = torch.ones(n, 1, 64, dtype=BF16)
+    ref.append(cache, k, k, table, [0, 0], [0, n, n])
+    q = torch.zeros(2, 2, 64, dtype=BF16)
+    q[:, 0, 5], q[:, 1, 5] = -math.inf, 1.0
+    w = torch.zeros(cache["k"].shape[:3], device="cuda")
+    out = run_cached(cache, table, [n, n], q, 1, 1.0)
+    assert torch.isnan(out[0, 0]).all() and torch.equal(out[0, 1], torch.ones(64, dtype=BF16))
+    assert not out[1].any()
+    assert torch.equal(run_cached(cache, table, [n, n], q, 1, 1.0, w).nan_to_num(7.0), out.nan_to_num(7.0))
+    row = w.cpu()[:, 0].flatten()
+    assert torch.isnan(row[:n]).all() and not row[n:].any()
+    whole = torch.empty(n, 2, 64, dtype=BF16, device="cuda")
+    mq.mq_attn_prompt(q[:1].expand(n, 2, 64).contiguous().cuda(), k.cuda(), k.cuda(), whole, ints([0, n]), n, 1.0)
+    assert torch.isnan(whole[:, 0]).all() and (whole[:, 1] == 1.0).all()
