@@ -502,7 +502,8 @@ mq_status mq_attn_prompt(const mq_rows *q, const mq_rows *k, const mq_rows *v, c
  * kept_dev: [n_seqs][kv_heads][keep], receives the kept tokens' former positions, ascending, -1
  *          after the last.
  * A kept token whose old page is outside [0, num_pages) is copied as code 0 with scale byte 10.
- * Errors: MQ_ERR_ARG, MQ_ERR_SHAPE (keep does not fit new_table), MQ_ERR_UNSUPPORTED.
+ * Errors: MQ_ERR_ARG, MQ_ERR_SHAPE (keep does not fit new_table), MQ_ERR_UNSUPPORTED (also keep
+ *         above 2^30).
  */
 mq_status mq_kv_evict(const mq_kv_cache *cache, float *weights_dev, const int32_t *table_dev,
                       const int32_t *lens_dev, const int32_t *new_table_dev,

@@ -150,7 +150,9 @@ mq_status mq_kv_evict(const mq_kv_cache *cache, float *weights, const int32_t *t
         !ints_ok(kept, (int64_t)n_seqs * keep) || (n_seqs && new_lens == lens))
         return MQ_ERR_ARG;
     if (keep > (int64_t)new_max_pages * cache->page_size) return MQ_ERR_SHAPE;
-    if (!dim_ok(cache->head_dim) || !blocks_ok(cache) || (int64_t)max_pages * cache->page_size > kMaxTokens) return MQ_ERR_UNSUPPORTED;
+    if (!dim_ok(cache->head_dim) || !blocks_ok(cache) || (int64_t)max_pages * cache->page_size > kMaxTokens ||
+        keep > kMaxTokens)
+        return MQ_ERR_UNSUPPORTED;
     if (n_seqs == 0) return MQ_OK;
     const mq::EvictArgs a = {view(cache), weights, table, lens, new_table, new_lens, kept, n_seqs,
                              max_pages, new_max_pages, keep, recent};
