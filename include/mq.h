@@ -434,8 +434,9 @@ mq_status mq_kv_append(const mq_kv_cache *cache, const mq_rows *k, const mq_rows
                        int32_t n_seqs, int32_t max_pages, hipStream_t stream);
 
 /* Bytes of device workspace mq_attn_cached needs for these sizes (0 on invalid input, and where
- * none is needed). max_len: the call's, or max_pages * page_size where the call passes 0. weights:
- * 1 if the call adds up attention weights. */
+ * none is needed), and for any call with the same heads and fewer sequences, new tokens or a
+ * smaller max_len, with or without weights. max_len: the call's, or max_pages * page_size where the
+ * call passes 0. weights: 1 if a call adds up attention weights. */
 size_t mq_attn_cached_workspace_bytes(int32_t n_seqs, int32_t q_heads, int32_t kv_heads,
                                       int32_t head_dim, int32_t q_len, int32_t max_len,
                                       int32_t weights);

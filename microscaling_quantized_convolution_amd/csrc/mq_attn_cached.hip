@@ -53,10 +53,21 @@ struct CachedPlan {
     size_t ml, part, scores, bytes; // workspace offsets
 };
 
+constexpr int kTilesWhole = 16, kTilesOrCut = 64; // tiles of a sequence, in the rule above
+
 // Workgroups that fit the 256 CUs together (by registers: 3, 2 or 1 to a CU). Tiles shared out to
 // half or twice as many, heads of 128: 1 x 131071 tokens 58.3 and 60.6 us against 57.8; 16
 // sequences of 1 to 4000 tokens 24 and 24 against 20.
 constexpr int resident(int d) { return kCus * (d <= 64 ? 3 : (d <= 128 ? 2 : 1)); }
+
+void place_workspace(CachedPlan &p, int64_t units, int d, bool weights)
+{
+    const size_t parts = (size_t)units + p.groups;
+    p.ml = 0;
+    p.part = p.ml + (p.groups || weights ? parts * kRows * 8 : 0);
+    p.scores = p.part + (p.groups ? parts * kRows * d * 4 : 0);
+    p.bytes = p.scores + (weights ? (size_t)units * kRows * p.slots * 4 : 0);
+}
 
 CachedPlan cached_plan(int n, int q_heads, int kv_heads, int d, int q_len, int max_len, bool weights)
 {
@@ -65,13 +76,9 @@ CachedPlan cached_plan(int n, int q_heads, int kv_heads, int d, int q_len, int m
     p.row_tiles = (p.rows + kRows - 1) / kRows;
     const int64_t units = (int64_t)n * kv_heads * p.row_tiles;
     const int64_t tiles = ((int64_t)max_len + kTile - 1) / kTile;
-    p.groups = tiles <= 16 || (tiles <= 64 && units >= kCus) ? 0 : resident(d);
+    p.groups = tiles <= kTilesWhole || (tiles <= kTilesOrCut && units >= kCus) ? 0 : resident(d);
     p.slots = (int)(tiles * kTile);
-    const size_t parts = (size_t)units + p.groups;
-    p.ml = 0;
-    p.part = p.ml + (p.groups || weights ? parts * kRows * 8 : 0);
-    p.scores = p.part + (p.groups ? parts * kRows * d * 4 : 0);
-    p.bytes = p.scores + (weights ? (size_t)units * kRows * p.slots * 4 : 0);
+    place_workspace(p, units, d, weights);
     return p;
 }
 
@@ -653,7 +660,13 @@ hipError_t cached_dim(const CachedArgs &a, int d, hipStream_t st)
 size_t attn_cached_workspace(int n, int q_heads, int kv_heads, int d, int q_len, int max_len,
                              bool weights)
 {
-    return cached_plan(n, q_heads, kv_heads, d, q_len, max_len, weights).bytes;
+    CachedPlan p = cached_plan(n, q_heads, kv_heads, d, q_len, max_len, weights);
+    const size_t bytes = p.bytes;
+    if (p.groups || p.slots <= kTilesWhole * kTile) return bytes;
+    // enough for a call with fewer sequences too, whose units are cut
+    p.groups = resident(d);
+    place_workspace(p, kCus - 1, d, weights);
+    return bytes > p.bytes ? bytes : p.bytes;
 }
 
 hipError_t launch_attn_cached(const CachedArgs &a, int d, int dtype, hipStream_t st)
