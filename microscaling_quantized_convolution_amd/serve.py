@@ -119,6 +119,8 @@ class CachedAttention:
     def evict(self, keep: int, recent: int):
         """Cut every sequence to `keep` tokens a head: the `recent` last ones and those that
         received the most attention. The new pages have to be free beside the old ones."""
+        if keep < 0 or recent < 0:
+            raise ValueError(f"keep {keep}, recent {recent}: expected 0 or more")
         page = self.cache.page_size
         held = [min(h, keep) for h in self.held]
         width = max(1, -(-keep // page))
@@ -130,10 +132,16 @@ class CachedAttention:
         rows = [p + [-1] * (width - len(p)) for p in pages]
         new_table = torch.tensor(rows, dtype=torch.int32, device=self.table.device)
         new_lens = torch.empty_like(self.lens)
-        self.positions = torch.empty((self.n, self.cache.kv_heads, keep), dtype=torch.int32,
-                                     device=self.table.device)
-        mq_kv_evict(self.cache, self.table, self.lens, self.weights, new_table, new_lens,
-                    self.positions, recent)
+        positions = torch.empty((self.n, self.cache.kv_heads, keep), dtype=torch.int32,
+                                device=self.table.device)
+        try:
+            mq_kv_evict(self.cache, self.table, self.lens, self.weights, new_table, new_lens,
+                        positions, recent)
+        except Exception:
+            for p in pages:  # nothing was launched
+                self.free += p
+            raise
+        self.positions = positions
         for old in self.pages:
             self.free += old
         self.pages, self.held, self.lens = pages, held, new_lens
