@@ -353,6 +353,14 @@ def _dense(t: torch.Tensor, dtype: torch.dtype, shape, what: str, device: int) -
     return t.data_ptr()
 
 
+def _ints(t: torch.Tensor, what: str, device: int) -> Tuple[int, int]:
+    """Address and length of an int32 vector."""
+    shape = t.shape
+    if len(shape) != 1:
+        raise ValueError(f"{what}: expected one dimension, got {tuple(shape)}")
+    return _dense(t, torch.int32, shape, what, device), shape[0]
+
+
 def _table(table: torch.Tensor, n: int, device: int) -> Tuple[int, int]:
     """Address and width of a page table of n rows."""
     shape = table.shape
@@ -423,11 +431,9 @@ def mq_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: torch.
     """Quantize the packed keys and values k, v [tokens][kv_heads][dim] into the cache behind each
     sequence's lens[s] tokens: sequence s receives rows cu[s]:cu[s + 1]. lens is not changed."""
     dev = _current_device()
-    shape = lens.shape
-    n = shape[0]
+    pl, n = _ints(lens, "lens", dev)
     pt, width = _table(table, n, dev)
-    st = _lib.mq_kv_append(cache.ref(dev), _rows(k, "k", dev), _rows(v, "v", dev), pt,
-                           _dense(lens, torch.int32, shape, "lens", dev),
+    st = _lib.mq_kv_append(cache.ref(dev), _rows(k, "k", dev), _rows(v, "v", dev), pt, pl,
                            _dense(cu, torch.int32, (n + 1,), "cu", dev), n, width,
                            _raw_stream(dev) if stream is None else _stream(stream))
     if st:
@@ -456,14 +462,12 @@ def mq_attn_cached(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: t
     its lens[s] cached tokens (these included), into out. weights (fp32, cache.weights_shape)
     gains the attention each cached token received, from every sequence that reads its page."""
     dev = _current_device()
-    shape = lens.shape
-    n = shape[0]
+    pl, n = _ints(lens, "lens", dev)
     pt, width = _table(table, n, dev)
     pw = (None if weights is None
           else _dense(weights, torch.float32, cache.weights_shape, "weights", dev))
     st = _lib.mq_attn_cached(cache.ref(dev), _rows(q, "q", dev), _rows(out, "out", dev), pt,
-                             _dense(lens, torch.int32, shape, "lens", dev), n, width, q_len,
-                             max_len, scale, pw,
+                             pl, n, width, q_len, max_len, scale, pw,
                              None if ws is None else _dense(ws, torch.uint8, ws.shape, "ws", dev),
                              0 if ws is None else ws.numel(),
                              _raw_stream(dev) if stream is None else _stream(stream))
@@ -476,10 +480,9 @@ def mq_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch
     """Causal attention over packed prompts: rows cu[s]:cu[s + 1] of q, out [tokens][q_heads][dim]
     and k, v [tokens][kv_heads][dim] are sequence s, none longer than max_len."""
     dev = _current_device()
-    shape = cu.shape
+    pc, n = _ints(cu, "cu", dev)
     st = _lib.mq_attn_prompt(_rows(q, "q", dev), _rows(k, "k", dev), _rows(v, "v", dev),
-                             _rows(out, "out", dev), _dense(cu, torch.int32, shape, "cu", dev),
-                             shape[0] - 1, max_len, scale,
+                             _rows(out, "out", dev), pc, n - 1, max_len, scale,
                              _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise MQError(st, "mq_attn_prompt")
@@ -492,14 +495,13 @@ def mq_kv_evict(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, weights
     with the largest weights, copied to the pages of new_table; kept [sequences][kv_heads][keep]
     receives their former positions, new_lens the sequences' new lengths."""
     dev = _current_device()
-    i32, shape = torch.int32, lens.shape
-    n, keep = shape[0], kept.shape[-1]
+    i32, keep = torch.int32, kept.shape[-1]
+    pl, n = _ints(lens, "lens", dev)
     pt, width = _table(table, n, dev)
     pn, new_width = _table(new_table, n, dev)
     st = _lib.mq_kv_evict(cache.ref(dev),
-                          _dense(weights, torch.float32, cache.weights_shape, "weights", dev), pt,
-                          _dense(lens, i32, shape, "lens", dev), pn,
-                          _dense(new_lens, i32, shape, "new_lens", dev),
+                          _dense(weights, torch.float32, cache.weights_shape, "weights", dev), pt, pl, pn,
+                          _dense(new_lens, i32, (n,), "new_lens", dev),
                           _dense(kept, i32, (n, cache.kv_heads, keep), "kept", dev), n, width,
                           new_width, keep, recent,
                           _raw_stream(dev) if stream is None else _stream(stream))
