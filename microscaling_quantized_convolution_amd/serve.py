@@ -38,7 +38,7 @@ class CachedAttention:
         self.n, self.q_heads = n_seqs, q_heads
         self.width = -(-max_len // page_size)
         self.max_len = max_len
-        # room for every sequence at its longest, and for one being evicted into fresh pages
+        # room for every sequence at its longest, and for one being cut into fresh pages
         num_pages = (n_seqs + 1) * self.width if num_pages is None else num_pages
         self.cache = KVCache.empty(num_pages, page_size, kv_heads, head_dim, device)
         self.weights = torch.zeros(self.cache.weights_shape, device=device)
@@ -118,34 +118,48 @@ class CachedAttention:
 
     def evict(self, keep: int, recent: int):
         """Cut every sequence to `keep` tokens a head: the `recent` last ones and those that
-        received the most attention. The new pages have to be free beside the old ones."""
+        received the most attention. Shorter sequences stay as they are. The new pages have to be
+        free beside the old ones: as many sequences are cut at a time as there are pages for, and
+        there must be enough for one."""
         if keep < 0 or recent < 0:
             raise ValueError(f"keep {keep}, recent {recent}: expected 0 or more")
-        page = self.cache.page_size
-        held = [min(h, keep) for h in self.held]
-        width = max(1, -(-keep // page))
-        fresh = self._take(sum(-(-h // page) for h in held))
-        pages: List[List[int]] = []
-        for h in held:
-            pages.append(fresh[:-(-h // page)])
-            fresh = fresh[-(-h // page):]
-        rows = [p + [-1] * (width - len(p)) for p in pages]
-        new_table = torch.tensor(rows, dtype=torch.int32, device=self.table.device)
-        new_lens = torch.empty_like(self.lens)
-        positions = torch.empty((self.n, self.cache.kv_heads, keep), dtype=torch.int32,
-                                device=self.table.device)
+        need = -(-keep // self.cache.page_size)
+        cut = [s for s, h in enumerate(self.held) if h > keep]
+        if cut and need > len(self.free):
+            raise RuntimeError(f"{need} pages wanted, {len(self.free)} free")
+        dev = self.table.device
+        at = torch.arange(keep, dtype=torch.int32, device=dev)
+        held = torch.tensor(self.held, dtype=torch.int32, device=dev)[:, None, None]
+        positions = torch.where(at < held, at, -1).repeat(1, self.cache.kv_heads, 1)
         try:
-            mq_kv_evict(self.cache, self.table, self.lens, self.weights, new_table, new_lens,
-                        positions, recent)
+            while cut:
+                count = len(self.free) // need if need else len(cut)
+                self._cut(cut[:count], keep, recent, need, positions)
+                cut = cut[count:]
+            self.positions = positions
+        finally:
+            self._copy_table()
+            self.lens.copy_(torch.tensor(self.held, dtype=torch.int32))
+
+    def _cut(self, seqs: List[int], keep: int, recent: int, need: int, positions: torch.Tensor):
+        """Cut these sequences, all longer than keep, into `need` fresh pages each."""
+        dev = self.table.device
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+        width = max(len(self.pages[s]) for s in seqs)
+        table = ints([self.pages[s] + [-1] * (width - len(self.pages[s])) for s in seqs])
+        lens = ints([self.held[s] for s in seqs])
+        new_lens, kept = torch.empty_like(lens), torch.empty_like(positions[:len(seqs)])
+        fresh = self._take(need * len(seqs))
+        try:
+            mq_kv_evict(self.cache, table, lens, self.weights, ints(fresh).view(len(seqs), need),
+                        new_lens, kept, recent)
         except Exception:
-            for p in pages:  # nothing was launched
-                self.free += p
+            self.free += fresh  # nothing was launched
             raise
-        self.positions = positions
-        for old in self.pages:
-            self.free += old
-        self.pages, self.held, self.lens = pages, held, new_lens
-        self._copy_table()
+        positions[torch.tensor(seqs, device=dev)] = kept
+        for i, s in enumerate(seqs):
+            self.free += self.pages[s]
+            self.pages[s], self.held[s] = fresh[i * need:(i + 1) * need], keep
 
 
 def main():

@@ -59,3 +59,68 @@ def test_a_refused_eviction_changes_nothing(calls):
         assert state(layer) == before
     layer.evict(16, 4)
     assert layer.held == [16, 16] and len(layer.free) == 12 - 2
+
+
+def evicted(calls):
+    """Lengths of the sequences in each eviction that was made."""
+    return [args[2].tolist() for name, args in calls if name == "mq_kv_evict"]
+
+
+@pytest.mark.parametrize("n,keep", [(8, 1024), (3, 2048), (1, 4095), (5, 0)])
+def test_a_full_layer_of_the_default_size_can_evict(calls, n, keep):
+    """Every sequence at max_len: nothing more can be appended, and a cut fits the pool."""
+    full, page = 4096, 64
+    layer = filled(new_layer(n, full, page), [full] * n)
+    with pytest.raises(ValueError):
+        layer.decode(rows(n, 2), rows(n, 1), rows(n, 1))
+    pool = layer.cache.num_pages
+    layer.evict(keep, 0)
+    assert layer.held == [keep] * n == layer.lens.tolist()
+    assert sorted(sum(layer.pages, []) + layer.free) == list(range(pool))
+    assert [len(p) for p in layer.pages] == [-(-keep // page)] * n
+    for p, row in zip(layer.pages, layer.table.tolist()):
+        assert row == p + [-1] * (len(row) - len(p))
+    assert sum(evicted(calls), []) == [full] * n  # each of them once
+    assert layer.positions.shape == (n, 1, keep)
+    layer.decode(rows(n, 2), rows(n, 1), rows(n, 1))
+
+
+def test_an_eviction_with_room_is_one_call(calls):
+    layer = filled(new_layer(4, 64, 16, num_pages=64), [64] * 4)
+    layer.evict(32, 8)
+    assert evicted(calls) == [[64] * 4]
+
+
+def test_short_sequences_stay_where_they_are(calls):
+    layer = filled(new_layer(3, 64, 16), [64, 20, 33])
+    kept = list(layer.pages[1])
+    layer.evict(32, 8)
+    assert evicted(calls) == [[64, 33]] and layer.pages[1] == kept
+    assert layer.held == [32, 20, 32] == layer.lens.tolist()
+    assert layer.positions[1, 0].tolist() == list(range(20)) + [-1] * 12
+
+
+def test_an_eviction_without_room_changes_nothing(calls):
+    layer = filled(new_layer(2, 64, 16, num_pages=8), [64, 64])
+    before = state(layer)
+    with pytest.raises(RuntimeError):
+        layer.evict(32, 8)
+    assert state(layer) == before and not evicted(calls)
+
+
+def test_an_eviction_refused_half_way_keeps_what_was_done(calls, monkeypatch):
+    layer = filled(new_layer(3, 64, 16), [64] * 3)  # 4 free pages: two sequences at a time
+    call = serve.mq_kv_evict
+
+    def second_refused(*args):
+        if evicted(calls):
+            calls.refused = "mq_kv_evict"
+        call(*args)
+    monkeypatch.setattr(serve, "mq_kv_evict", second_refused)
+    with pytest.raises(mq.MQError):
+        layer.evict(32, 0)
+    assert evicted(calls) == [[64, 64]] and layer.held == [32, 32, 64] == layer.lens.tolist()
+    assert sorted(sum(layer.pages, []) + layer.free) == list(range(16))
+    assert [len(p) for p in layer.pages] == [2, 2, 4]
+    for p, row in zip(layer.pages, layer.table.tolist()):
+        assert row == p + [-1] * (len(row) - len(p))
