@@ -86,13 +86,16 @@ class CachedAttention:
         """Prompts of the given lengths (0: none) for sequences that hold nothing, packed one after
         another: q [tokens][q_heads][dim], k and v [tokens][kv_heads][dim]. Returns their
         attention."""
+        tokens = (len(q), len(k), len(v))
+        if len(lengths) != self.n or min(lengths, default=0) < 0 or tokens != (sum(lengths),) * 3:
+            raise ValueError(f"lengths {list(lengths)} for {self.n} sequences and {tokens} rows of q, k and v")
         if any(held and new for held, new in zip(self.held, lengths)):
             raise ValueError("a prompt for a sequence that holds tokens")
         self._reserve(lengths)
         cu = torch.tensor([sum(lengths[:s]) for s in range(self.n + 1)], dtype=torch.int32,
                           device=q.device)
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        mq_attn_prompt(q, k, v, out, cu, max(lengths), self.scale)
+        mq_attn_prompt(q, k, v, out, cu, max(lengths, default=0), self.scale)
         mq_kv_append(k, v, self.cache, self.table, self.lens, cu)
         self._grow(lengths)
         return out

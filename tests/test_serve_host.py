@@ -124,3 +124,16 @@ def test_an_eviction_refused_half_way_keeps_what_was_done(calls, monkeypatch):
     assert [len(p) for p in layer.pages] == [2, 2, 4]
     for p, row in zip(layer.pages, layer.table.tolist()):
         assert row == p + [-1] * (len(row) - len(p))
+
+
+@pytest.mark.parametrize("lengths,tokens", [([40, 20], (59, 60, 60)), ([40, 20], (60, 61, 60)),
+                                            ([40, 20], (60, 60, 59)), ([60], (60, 60, 60)),
+                                            ([20, 20, 20], (60, 60, 60)), ([70, -10], (60, 60, 60))])
+def test_prefill_refuses_lengths_that_do_not_fit(calls, lengths, tokens):
+    """Before anything is launched or changed: a length for each sequence, none negative, and as
+    many rows as they add up to."""
+    layer = new_layer(max_len=128)
+    before = state(layer)
+    with pytest.raises(ValueError):
+        layer.prefill(rows(tokens[0], 2), rows(tokens[1], 1), rows(tokens[2], 1), lengths)
+    assert not calls and state(layer) == before
