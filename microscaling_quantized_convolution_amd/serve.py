@@ -108,15 +108,19 @@ class CachedAttention:
         """One new token of every sequence: q [n_seqs][q_heads][dim], k and v
         [n_seqs][kv_heads][dim]. Returns its attention over the cache, itself included."""
         self._reserve([1] * self.n)
-        mq_kv_append(k, v, self.cache, self.table, self.lens, self.steps)
-        self.held = [h + 1 for h in self.held]
-        self.lens += 1
         if self.ws is None:
             self.ws = attn_cached_workspace(self.n, self.q_heads, self.cache.kv_heads,
                                             self.cache.head_dim, 1, self.max_len, True, q.device)
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        mq_attn_cached(q, self.cache, self.table, self.lens, out, self.ws, self.scale, 1,
-                       self.max_len, self.weights)
+        mq_kv_append(k, v, self.cache, self.table, self.lens, self.steps)
+        self.lens += 1
+        try:
+            mq_attn_cached(q, self.cache, self.table, self.lens, out, self.ws, self.scale, 1,
+                           self.max_len, self.weights)
+        except Exception:
+            self.lens -= 1  # the tokens just written are not held: the step can be made again
+            raise
+        self.held = [h + 1 for h in self.held]
         return out
 
     def evict(self, keep: int, recent: int):

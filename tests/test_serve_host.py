@@ -137,3 +137,17 @@ def test_prefill_refuses_lengths_that_do_not_fit(calls, lengths, tokens):
     with pytest.raises(ValueError):
         layer.prefill(rows(tokens[0], 2), rows(tokens[1], 1), rows(tokens[2], 1), lengths)
     assert not calls and state(layer) == before
+
+
+def test_a_refused_step_can_be_made_again(calls):
+    """A step whose attention is refused has added no token."""
+    layer = filled(new_layer(), [16, 5])
+    calls.refused = "mq_attn_cached"
+    for _ in range(2):
+        with pytest.raises(mq.MQError):
+            layer.decode(rows(2, 2), rows(2, 1), rows(2, 1))
+        assert layer.held == [16, 5] == layer.lens.tolist()
+    calls.refused = None
+    layer.decode(rows(2, 2), rows(2, 1), rows(2, 1))
+    assert layer.held == [17, 6] == layer.lens.tolist() and calls[-1][1][3].tolist() == [17, 6]
+    assert sorted(sum(layer.pages, []) + layer.free) == list(range(layer.cache.num_pages))
