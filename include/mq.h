@@ -447,9 +447,8 @@ size_t mq_attn_cached_workspace_bytes(int32_t n_seqs, int32_t q_heads, int32_t k
  * i in [0, q_len), sees tokens t <= lens[s] - q_len + i; query head h reads key/value head
  * h / (q_heads / kv_heads):
  *   p[t] = softmax_t(scale * sum_d q[d] * K[t][d])     out[d] = sum_t p[t] * V[t][d]
- * with the softmax and both sums in fp32 from exact products of the cache's values; p is rounded
- * to bf16 for the second product (to two bf16 parts where dtype is MQ_F16). A row that sees no
- * token is 0.
+ * with the softmax and both sums in fp32 from exact products of the cache's values; p is held to
+ * 2^-16 of itself for the second product. A row that sees no token is 0.
  * q, out:  n_seqs * q_len rows, sequence by sequence.
  * max_len: no sequence holds more tokens than this (longer ones are read up to it); 0 stands for
  *          max_pages * page_size. It sizes the launch and the workspace.

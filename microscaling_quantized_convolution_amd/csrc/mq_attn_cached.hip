@@ -5,7 +5,7 @@
 // key/value head times the new tokens) and takes 64 cached tokens at a time:
 //   S^T = K Q^T            v_mfma 16x16x32, the codes decoded exactly to dtype
 //   P   = 2^(S - m)        in fp32, on the accumulator registers
-//   O^T += V^T P^T         v_mfma 16x16x32 in bf16
+//   O^T += V^T P^T         v_mfma 16x16x32 in bf16, P in two parts
 // The products are laid out so that no value changes lanes between them. In step t of the first
 // product, row m of the tile is token 4t + m%4 of the tile's block m/4; its result then leaves
 // lane group g = lane/16 with tokens 4t..4t+3 of block g, and after four steps with all 16
@@ -362,8 +362,11 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / kCus) attn_cached_k
             for (int j = 0; j < 4; ++j) {
                 const float a0 = p[8 * u + 2 * j], a1 = p[8 * u + 2 * j + 1];
                 ph[j] = Elem<MQ_BF16>::pack(a0, a1);
-                // bf16 holds p to 2^-9, as the bf16 output will be; for half-precision outputs the
-                // rest of p goes in as a second part, and both hold it to 2^-17
+                // bf16 has the range of p times a block's scale and holds it to 2^-8; what that leaves
+                // goes in as a second part, and both hold it to 2^-16, so that the output's own
+                // rounding is the one that counts. The second product is not what bounds the kernel:
+                // 32 sequences up to 4096 tokens 26.6 us with one part and 27.8 with both, others
+                // within 2%.
                 pr[j] = Elem<MQ_BF16>::pack(a0 - __uint_as_float(ph[j] << 16),
                                             a1 - __uint_as_float(ph[j] & 0xFFFF0000u));
             }
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / kCus) attn_cached_k
             for (int i = 0; i < VT; ++i) {
                 const bf16x8_t vv = decode8<MQ_BF16>(v[i][2 * u], v[i][2 * u + 1]);
                 o[i] = Elem<MQ_BF16>::mfma16(vv, hi, o[i]);
-                if constexpr (DT == MQ_F16) o[i] = Elem<MQ_BF16>::mfma16(vv, lo, o[i]);
+                o[i] = Elem<MQ_BF16>::mfma16(vv, lo, o[i]);
             }
         }
         load_v(vb);

@@ -129,3 +129,26 @@ def test_rows_whose_scores_are_all_minus_infinity(n):
     whole = torch.empty(n, 2, 64, dtype=BF16, device="cuda")
     mq.mq_attn_prompt(q[:1].expand(n, 2, 64).contiguous().cuda(), k.cuda(), k.cuda(), whole, ints([0, n]), n, 1.0)
     assert torch.isnan(whole[:, 0]).all() and (whole[:, 1] == 1.0).all()
+
+
+# ---- probabilities in more than 16 bits --------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lens", [[300, 77], [2500, 1030]])
+def test_cached_results_round_once(dtype, lens):
+    """p goes into the second product to 2^-16 of itself, so that an output is off by its own
+    rounding and little else, however much the values cancel."""
+    dim, heads, group, scale = 64, 2, 3, 0.125
+    cache, table = filled(71, lens, 32, heads, dim, dtype)
+    q = randn(torch.Generator().manual_seed(41), len(lens), heads * group, dim, dtype=dtype)
+    got = run_cached(cache, table, lens, q, 1, scale).double()
+    for s, n in enumerate(lens):
+        for h in range(heads):
+            k, v = (ref.tokens(cache, side, table[s], n, h)[0] for side in ("k", "v"))
+            rows = q[s, h * group:(h + 1) * group].double()
+            p = torch.softmax(rows @ k.t() * scale, 1)
+            size = (rows.abs() @ k.abs().t() * scale).amax(1, keepdim=True)
+            want = p @ v
+            bound = ref.attn_bound(want, p @ v.abs(), 2.0 ** -16, ref.score_error(dim, size), n, ref.U[dtype])
+            err = (got[s, h * group:(h + 1) * group] - want).abs()
+            assert (err <= bound).all(), f"{(err / bound).max()} of the bound"
