@@ -50,6 +50,7 @@ class CachedAttention:
         self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=device)
         self.steps = torch.arange(n_seqs + 1, dtype=torch.int32, device=device)
         self.ws: Optional[torch.Tensor] = None
+        self.ws_len = 0  # tokens of a sequence that it is enough for
         self.positions: Optional[torch.Tensor] = None  # of the last eviction
 
     def _take(self, count: int) -> List[int]:
@@ -108,15 +109,17 @@ class CachedAttention:
         """One new token of every sequence: q [n_seqs][q_heads][dim], k and v
         [n_seqs][kv_heads][dim]. Returns its attention over the cache, itself included."""
         self._reserve([1] * self.n)
-        if self.ws is None:
+        longest = max(self.held) + 1  # not max_len: the call's grid and scratch go by it
+        if longest > self.ws_len:
+            self.ws_len = min(self.max_len, 1 << (longest - 1).bit_length())
             self.ws = attn_cached_workspace(self.n, self.q_heads, self.cache.kv_heads,
-                                            self.cache.head_dim, 1, self.max_len, True, q.device)
+                                            self.cache.head_dim, 1, self.ws_len, True, q.device)
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         mq_kv_append(k, v, self.cache, self.table, self.lens, self.steps)
         self.lens += 1
         try:
             mq_attn_cached(q, self.cache, self.table, self.lens, out, self.ws, self.scale, 1,
-                           self.max_len, self.weights)
+                           longest, self.weights)
         except Exception:
             self.lens -= 1  # the tokens just written are not held: the step can be made again
             raise

@@ -151,3 +151,14 @@ def test_a_refused_step_can_be_made_again(calls):
     layer.decode(rows(2, 2), rows(2, 1), rows(2, 1))
     assert layer.held == [17, 6] == layer.lens.tolist() and calls[-1][1][3].tolist() == [17, 6]
     assert sorted(sum(layer.pages, []) + layer.free) == list(range(layer.cache.num_pages))
+
+
+def test_a_step_is_sized_by_the_longest_sequence(calls):
+    """Not by what the layer could hold: grid and scratch of the attention go by its max_len."""
+    layer = filled(new_layer(max_len=1 << 17, num_pages=64, page=64), [100, 30])
+    need = lambda length: mq.mq_attn_cached_workspace_bytes(2, 2, 1, 64, 1, length, True)
+    for longest in range(101, 140):
+        layer.decode(rows(2, 2), rows(2, 1), rows(2, 1))
+        ws, max_len = calls[-1][1][5], calls[-1][1][8]
+        assert max_len == longest == max(layer.held)
+        assert need(longest) <= ws.numel() <= need(2 * longest)
