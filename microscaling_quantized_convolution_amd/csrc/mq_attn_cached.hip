@@ -15,8 +15,8 @@
 //
 // Bound by the bytes of the cache, read once: 131071 tokens, 32 query heads on 8 of 128, are 269 MB
 // in 51 to 53 us, 5.1 to 5.3 TB/s (reads of 8 KB pieces in any order reach 5.8 on this card; the
-// whole call takes 56 to 58 us). 32 sequences of up to 4096 tokens, 107 MB, take 30 us: their
-// longest unit is 64 tiles of one workgroup, one after another at 0.4 us each.
+// whole call takes 56 to 58 us). 32 sequences of up to 4096 tokens, 107 MB, take 31 us: each unit
+// is one workgroup here, of 64 tiles at most and 26 in the mean, at 0.4 us each.
 #include "mq_attn_device.hpp"
 
 #include <cfloat>
@@ -34,7 +34,7 @@ constexpr float kUnseen = -FLT_MAX; // in the kept scores: a token that the row 
 // shared out to as many workgroups as the chip holds at a time, a unit (the kRows query rows of
 // one sequence and key/value head) has as many equal pieces as tiles / per rounds to, one at
 // least, in whole rounds of the waves (rounded up instead: 32 sequences of 1000 to 2000 tokens,
-// 16 heads on 4 of 256, 35 us in place of 28; others within 10% either way). There are then at
+// 16 heads on 4 of 256, 36 us in place of 28; others within 6% either way). There are then at
 // most units + groups pieces, which the host can launch without the lengths; each workgroup finds
 // its piece by prefix sums over the sequences, and those past the last leave at once. A unit of
 // several pieces is joined by a second launch.
@@ -42,10 +42,12 @@ constexpr float kUnseen = -FLT_MAX; // in the kept scores: a token that the row 
 // Without pieces, a workgroup takes a whole unit and there is no second launch (3 us and more).
 // That is done where no sequence has more than 16 tiles, or at most 64 and there is a unit for
 // every CU: then the units keep the chip busy by themselves unless a few of them hold most of the
-// tokens. Whole against cut, 32 query heads on 8 of 128: 1 x 1000 tokens 10.0 and 10.8 us, 1 x
-// 2000 15.2 and 10.7; 16 sequences (128 units) of 1 to 4000 tokens 25 and 20.7; 32 (256 units) of
-// 1 to 2000 16.6 and 21.5, of 1 to 4000 26.8 and 31.5, one of 4000 among 500s 24.8 and 18.2; 64 of
-// 2000 to 4000 76 and 80.
+// tokens, which the host does not know. Whole against cut, 32 query heads on 8 of 128: 1 x 1000
+// tokens 9.4 and 10.7 us, 1 x 2000 14.9 and 10.8; 16 sequences (128 units) of 1 to 4000 tokens 26.5
+// and 21.2; 32 (256 units) of 1 to 2000 17.1 and 23.1, of 1 to 4000 28.6 and 32.8; 64 of 2000 to
+// 4000 75 and 79; against it, one of 4000 among 500s 26.8 and 16.3. Above 64 tiles either can be
+// right (32 of 8000 each 90 and 96, of 500 to 8000 evenly 57 and 62, but mostly short ones up to 8000
+// 51 and 41, 64 of those 96 and 84), and cutting loses less where it is wrong.
 struct CachedPlan {
     int rows, row_tiles; // query rows of a key/value head, in tiles of kRows
     int groups;          // workgroups that share the tiles; 0: one for each unit
@@ -56,8 +58,8 @@ struct CachedPlan {
 constexpr int kTilesWhole = 16, kTilesOrCut = 64; // tiles of a sequence, in the rule above
 
 // Workgroups that fit the 256 CUs together (by registers: 3, 2 or 1 to a CU). Tiles shared out to
-// half or twice as many, heads of 128: 1 x 131071 tokens 58.3 and 60.6 us against 57.8; 16
-// sequences of 1 to 4000 tokens 24 and 24 against 20.
+// half or twice as many, heads of 128: 1 x 131071 tokens 46.0 and 48.5 us against 46.9 (from the
+// last-level cache); 16 sequences of 1 to 4000 tokens 24 and 24 against 21.
 constexpr int resident(int d) { return kCus * (d <= 64 ? 3 : (d <= 128 ? 2 : 1)); }
 
 void place_workspace(CachedPlan &p, int64_t units, int d, bool weights)
@@ -104,8 +106,8 @@ __device__ __forceinline__ int tiles_of(const CachedArgs &a, int s)
 
 // A workgroup's share of `total` tiles of the sequences' units. Two rounds of the waves (cut()
 // makes 8 tiles of a share of 6) in one workgroup to a CU are faster than one round in two: 1 x
-// 16000 tokens 12.6 against 14.7 us, 8 x 8190 with 4 new tokens and weights 17.3 against 18.7. With
-// fewer tiles than that, one round on as many CUs as it takes: 1 x 4000 tokens 10.9 against 11.6.
+// 16000 tokens 12.8 against 14.8 us, 8 of up to 8190 with weights 15.4 against 15.9. With fewer tiles
+// than that, one round on as many CUs as it takes: 1 x 4000 tokens 11.1 against 12.0.
 template <int D>
 __device__ __forceinline__ int share(int total, const CachedArgs &a, const CachedPlan &pl)
 {
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(64 * kWaves, resident(D) / kCus) attn_cached_k
 // query row along the cache (kJoinThreads / (D/4) parts at a time, four dimensions to a lane),
 // the others add the weights of 256 tokens, summed over the rows in order, to their places. Bound
 // by the latency of the launch and of three loads that wait for each other (lengths, maxima and
-// sums, parts): 5 us at 131071 tokens, 7 us with the weights of 8 x 8190.
+// sums, parts): 5.5 us at 131071 tokens, 8 us with the weights of 8 of up to 8190.
 constexpr int kJoinThreads = 256;
 
 template <int DT, int D>

@@ -68,8 +68,9 @@ __device__ __forceinline__ int capacity(int max_pages, int page)
 //
 // One wave per touched block, head and side (keys, values). Bound by the bytes: 2 B in and 1 B
 // out per element; 65536 tokens of 8 heads of 128 are 403 MB in 81 us, 4.95 TB/s (a large copy
-// reaches 5.16). A step of a few tokens takes 8 us, all of it call and launch. The block's largest magnitude is found on the 16-bit patterns (their
-// magnitudes order like unsigned numbers), two at a time, while the elements stay in registers.
+// reaches 5.16). A step of a few tokens takes 8 us, all of it call and launch. The block's largest
+// magnitude is found on the 16-bit patterns (their magnitudes order like unsigned numbers), two at
+// a time, while the elements stay in registers.
 // Every load is made, with the token clamped into the new ones, and what does not belong is
 // cleared afterwards: loads under a condition were waited for one by one.
 template <int DT, int D>

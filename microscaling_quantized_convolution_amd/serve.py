@@ -8,6 +8,8 @@ the library's calls in their order:
   decode    mq_kv_append of the new tokens, then mq_attn_cached, which adds up the weights
   evict     mq_kv_evict into fresh pages; the old ones become free
 
+A prompt's own attention adds no weights: an eviction ranks its tokens by what the tokens generated
+since gave them, and equal weights (none, right after ``prefill``) by position, the lowest first.
 Projections, rotary embeddings and the rest of the layer are the caller's. Pages are handed out on
 the host, so only ``prefill``, the first token of a page and ``evict`` copy a table to the device;
 after an eviction the heads of a sequence hold different tokens (``positions`` tells which).
