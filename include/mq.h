@@ -511,6 +511,144 @@ mq_status mq_kv_evict(const mq_kv_cache *cache, float *weights_dev, const int32_
                       int32_t max_pages, int32_t new_max_pages, int32_t keep, int32_t recent,
                       hipStream_t stream);
 
+/* ---- microscaled 4-bit linear layers ---------------------------------------------------------
+ *
+ * The linear layers of a transformer block on E2M1 elements with one power-of-two scale per 32 of
+ * them along the contracted dimension, the operands that the scaled matrix instructions take:
+ * quantization along rows and columns from one read (mq_mx4_quantize, read back by
+ * mq_mx4_dequantize), the product of two quantized matrices (mq_mx4_matmul), a linear layer on a
+ * quantized weight (mq_mx4_linear) and its gradients (mq_mx4_linear_backward), and the gated
+ * feed-forward product silu(x Wg^T) * (x Wu^T) (mq_mx4_gated) and its gradients
+ * (mq_mx4_gated_backward). Each tensor is quantized once for each direction that it is contracted
+ * along, and read once for both.
+ *
+ * Every product is exact and summed in fp32 (in an order that the sizes alone fix: results repeat
+ * bit for bit); a sum below 2^-126 in magnitude may become 0.
+ */
+
+/* mq_matrix.dtype: an mq_dtype, or fp32. */
+#define MQ_F32 3
+
+/* Elements that share one scale, and columns that lie together (mq_mx4). */
+#define MQ_MX4_BLOCK 32
+#define MQ_MX4_PIECE 256
+
+/* A dense matrix: element (r, c) is data[r * stride + c]. data must be aligned to the element's
+ * size (16-byte alignment, and a stride that keeps it, is faster). stride in elements, >= cols.
+ * A matrix without elements may be null. */
+typedef struct {
+    void *data;
+    int64_t stride;
+    int32_t rows, cols, dtype;
+} mq_matrix;
+
+/*
+ * A quantized matrix of rows x cols, with blocks of 32 along a row. Rows are cut into
+ * P = ceil(cols / 256) pieces of 256 columns (8 blocks), the last one filled up with zeros:
+ *   codes   [P][rows][128]  E2M1 (s|ee|m, bias 1); element j of a piece in byte j / 2, the even
+ *                           one in the low half
+ *   scales  [P][rows][8]    one byte e for a block of 32: the scale 2^(e-127)
+ * An element's value is decode(code) * 2^(e-127). Scale bytes written by this library lie in
+ * [2, 252]; 255 marks a block that received a NaN or an infinity: its codes are 0, and every sum
+ * that it takes part in is NaN. Elements past cols must have code 0, and no scale byte of 255.
+ * codes must be 16-byte aligned, scales 8-byte aligned (MQ_ERR_ARG otherwise).
+ */
+typedef struct {
+    int32_t rows, cols;
+    uint8_t *codes, *scales;
+} mq_mx4;
+
+/* Bytes of the codes and of the scales of a quantized matrix (0 for invalid arguments, and for a
+ * matrix without elements). */
+size_t mq_mx4_codes_bytes(int32_t rows, int32_t cols);
+size_t mq_mx4_scales_bytes(int32_t rows, int32_t cols);
+
+/*
+ * mq_mx4_quantize: x along its rows, its columns, or both from one read. With amax the largest
+ * magnitude of a block,
+ *   e    = the smallest byte with amax <= 6 * 2^(e-127), but in [2, 252]
+ *   code = CastE2M1(x * 2^(127-e))
+ * CastE2M1 is to nearest, ties to the even code, saturating at 6 (MQ_RNE), or stochastic (MQ_SR): up
+ * from the neighbour below in magnitude iff u < frac * 65536, where frac is the distance to it in
+ * steps and u a 16-bit draw: of element j (of 32) of block t = row * ceil(cols / 32) + block, the
+ * (j%2)-th half of word (j%8)/2 of Philox4x32-10(counter = (4t + j/8 as 64 bits, low word first;
+ * d; 0), key = seed) with d = 0 for rows and 1 for columns. A code keeps its element's sign.
+ * row: null, or rows x cols. col: null, or cols x rows, the transposed matrix along its rows.
+ * Errors: MQ_ERR_ARG (null, misaligned, negative, unknown dtype or rounding, neither row nor col),
+ *         MQ_ERR_SHAPE, MQ_ERR_UNSUPPORTED (a dimension of 2^30 or more, or more work than a grid
+ *         holds).
+ */
+mq_status mq_mx4_quantize(const mq_matrix *x, const mq_mx4 *row, const mq_mx4 *col, int32_t rnd,
+                          uint64_t seed, hipStream_t stream);
+
+/* mq_mx4_dequantize: the values of q, rounded once to out's type. Errors: as mq_mx4_quantize. */
+mq_status mq_mx4_dequantize(const mq_mx4 *q, const mq_matrix *out, hipStream_t stream);
+
+/*
+ * mq_mx4_matmul: y = a b^T, y[m][n] = sum_k a[m][k] * b[n][k], rounded once to y's type.
+ * a: M x K, b: N x K, y: M x N (K = 0 gives zeros).
+ * ws_dev / ws_bytes: device scratch, 16-byte aligned, of at least
+ *          mq_mx4_matmul_workspace_bytes(M, N, K) bytes (may be null where that is 0); so for
+ *          the calls below. What suffices for M rows suffices for fewer.
+ * Errors: MQ_ERR_ARG, MQ_ERR_SHAPE, MQ_ERR_WORKSPACE, MQ_ERR_UNSUPPORTED (as mq_mx4_quantize).
+ */
+size_t mq_mx4_matmul_workspace_bytes(int32_t m, int32_t n, int32_t k);
+mq_status mq_mx4_matmul(const mq_mx4 *a, const mq_mx4 *b, const mq_matrix *y, void *ws_dev,
+                        size_t ws_bytes, hipStream_t stream);
+
+/*
+ * mq_mx4_linear: y = Q(x) w^T, x quantized along its rows (MQ_RNE) on the way.
+ * x: M x K (M may be 0), w: N x K, y: M x N; the types of x and y are independent.
+ * x_col: null, or K x M: receives x quantized along its columns, which the weight's gradient reads.
+ * Errors: as mq_mx4_matmul.
+ */
+size_t mq_mx4_linear_workspace_bytes(int32_t m, int32_t n, int32_t k);
+mq_status mq_mx4_linear(const mq_matrix *x, const mq_mx4 *w, const mq_matrix *y,
+                        const mq_mx4 *x_col, void *ws_dev, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * mq_mx4_linear_backward: the gradients of y = x w^T for dy: M x N,
+ *   dx = Q(dy) w        M x K, from w_col (K x N), the weight quantized along its columns
+ *   dw = Q(dy^T) x      N x K, from x_col (K x M)
+ * with dy quantized along its rows and its columns, rounded as `rnd` says (see mq_mx4_quantize).
+ * dx or dw may be null, and with it w_col or x_col. M = 0 gives dw = 0.
+ * Errors: as mq_mx4_matmul; MQ_ERR_ARG also where dx and dw are both null.
+ */
+size_t mq_mx4_linear_backward_workspace_bytes(int32_t m, int32_t n, int32_t k);
+mq_status mq_mx4_linear_backward(const mq_matrix *dy, const mq_mx4 *x_col, const mq_mx4 *w_col,
+                                 const mq_matrix *dx, const mq_matrix *dw, int32_t rnd,
+                                 uint64_t seed, void *ws_dev, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * mq_mx4_gated: h = silu(G) * U with G = Q(x) wg^T, U = Q(x) wu^T, silu(z) = z / (1 + exp(-z));
+ * the two products and the activation stay in fp32, h is rounded once.
+ * x: M x K, wg and wu: F x K, h: M x F. g, u: both null, or M x F of h's type: receive G and U,
+ * rounded, for the backward pass. x_col: as for mq_mx4_linear.
+ * Errors: as mq_mx4_matmul.
+ */
+size_t mq_mx4_gated_workspace_bytes(int32_t m, int32_t f, int32_t k);
+mq_status mq_mx4_gated(const mq_matrix *x, const mq_mx4 *wg, const mq_mx4 *wu, const mq_matrix *h,
+                       const mq_matrix *g, const mq_matrix *u, const mq_mx4 *x_col, void *ws_dev,
+                       size_t ws_bytes, hipStream_t stream);
+
+/*
+ * mq_mx4_gated_backward: the gradients of mq_mx4_gated for dh: M x F, from the g and u that it kept
+ * (all three of one type). With s = 1 / (1 + exp(-g)),
+ *   dg = dh * u * s * (1 + g * (1 - s))     du = dh * g * s      (fp32, never stored)
+ *   dx = Q(dg) wg + Q(du) wu     M x K, from wg_col and wu_col (K x F)
+ *   dwg = Q(dg^T) x, dwu = Q(du^T) x      F x K, both of one type, from x_col (K x M)
+ * dg and du are quantized along rows and columns, rounded as `rnd` says; a stochastic draw of du is
+ * that of dg's with d + 2 in the counter. dx may be null, and with it wg_col and wu_col; dwg and dwu
+ * may both be null, and with them x_col. M = 0 gives dwg = dwu = 0.
+ * Errors: as mq_mx4_linear_backward.
+ */
+size_t mq_mx4_gated_backward_workspace_bytes(int32_t m, int32_t f, int32_t k);
+mq_status mq_mx4_gated_backward(const mq_matrix *dh, const mq_matrix *g, const mq_matrix *u,
+                                const mq_mx4 *x_col, const mq_mx4 *wg_col, const mq_mx4 *wu_col,
+                                const mq_matrix *dx, const mq_matrix *dwg, const mq_matrix *dwu,
+                                int32_t rnd, uint64_t seed, void *ws_dev, size_t ws_bytes,
+                                hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,7 +26,9 @@ MQ_SRC_DENSE, MQ_SRC_NCHW, MQ_SRC_OIHW = 0, 1, 2  # mq_quant_job.layout
 MQ_QUANTIZE_BATCH_MAX = 4
 MQ_NOALLOC_SCRATCH_BYTES = 32 << 20  # library-owned split-K scratch of mq_conv_backward_noalloc
 MQ_F16, MQ_BF16 = 1, 2  # mq_dtype: element type of the attention calls
+MQ_F32 = 3              # with these, element type of a dense matrix of the linear layers
 MQ_KV_BLOCK = 16        # tokens that share one scale of the key/value cache
+MQ_MX4_BLOCK, MQ_MX4_PIECE = 32, 256  # a 4-bit matrix: elements to a scale, columns together
 
 EXPORTS = (
     "mq_status_str", "mq_codes_bytes", "mq_scales_bytes", "mq_relayout_cbf",
@@ -37,6 +39,11 @@ EXPORTS = (
     "mq_conv_fwd_amax", "mq_conv_backward_amax",
     "mq_kv_append", "mq_attn_cached_workspace_bytes", "mq_attn_cached", "mq_attn_prompt",
     "mq_kv_evict",
+    "mq_mx4_codes_bytes", "mq_mx4_scales_bytes", "mq_mx4_quantize", "mq_mx4_dequantize",
+    "mq_mx4_matmul_workspace_bytes", "mq_mx4_matmul", "mq_mx4_linear_workspace_bytes",
+    "mq_mx4_linear", "mq_mx4_linear_backward_workspace_bytes", "mq_mx4_linear_backward",
+    "mq_mx4_gated_workspace_bytes", "mq_mx4_gated", "mq_mx4_gated_backward_workspace_bytes",
+    "mq_mx4_gated_backward",
 )
 
 
@@ -68,6 +75,16 @@ class mq_rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64), ("tokens", ctypes.c_int32),
                 ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class mq_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class mq_mx4(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
 
 
 class mq_kv_cache(ctypes.Structure):
@@ -122,6 +139,19 @@ def _load() -> ctypes.CDLL:
     L.mq_attn_cached.argtypes = [C, R, R, P, P, i32, i32, i32, i32, f32, P, P, sz, P]
     L.mq_attn_prompt.argtypes = [R, R, R, R, P, i32, i32, f32, P]
     L.mq_kv_evict.argtypes = [C, P, P, P, P, P, P, i32, i32, i32, i32, i32, P]
+    M, Q = ctypes.POINTER(mq_matrix), ctypes.POINTER(mq_mx4)
+    for name, count in (("codes", 2), ("scales", 2), ("matmul_workspace", 3),
+                        ("linear_workspace", 3), ("linear_backward_workspace", 3),
+                        ("gated_workspace", 3), ("gated_backward_workspace", 3)):
+        f = getattr(L, f"mq_mx4_{name}_bytes")
+        f.restype, f.argtypes = sz, [i32] * count
+    L.mq_mx4_quantize.argtypes = [M, Q, Q, i32, u64, P]
+    L.mq_mx4_dequantize.argtypes = [Q, M, P]
+    L.mq_mx4_matmul.argtypes = [Q, Q, M, P, sz, P]
+    L.mq_mx4_linear.argtypes = [M, Q, M, Q, P, sz, P]
+    L.mq_mx4_linear_backward.argtypes = [M, Q, Q, M, M, i32, u64, P, sz, P]
+    L.mq_mx4_gated.argtypes = [M, Q, Q, M, M, M, Q, P, sz, P]
+    L.mq_mx4_gated_backward.argtypes = [M, M, M, Q, Q, Q, M, M, M, i32, u64, P, sz, P]
     for name in EXPORTS:
         getattr(L, name).restype = getattr(L, name).restype or ctypes.c_int
     return L
@@ -507,3 +537,185 @@ def mq_kv_evict(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, weights
                           _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise MQError(st, "mq_kv_evict")
+
+
+# ---- microscaled 4-bit linear layers -----------------------------------------------------------
+
+_MATRIX_DTYPES = {torch.float16: MQ_F16, torch.bfloat16: MQ_BF16, torch.float32: MQ_F32}
+
+
+def _matrix(t: torch.Tensor, what: str, device: int) -> mq_matrix:
+    """[rows][cols] view with contiguous rows -> mq_matrix."""
+    dt, strides = _MATRIX_DTYPES.get(t.dtype), t.stride()
+    if (dt is None or len(strides) != 2 or t.get_device() != device or
+            (strides[1] != 1 and t.shape[1] > 1) or (strides[0] < t.shape[1] and t.shape[0] > 1)):
+        raise ValueError(f"{what}: expected a float16, bfloat16 or float32 matrix with contiguous "
+                         f"rows on cuda:{device} (the current device), got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}, strides {strides}")
+    r, c = t.shape
+    return mq_matrix(t.data_ptr(), max(strides[0], c), r, c, dt)
+
+
+class MX4:
+    """A matrix of rows x cols in 4 bits with one power-of-two scale per 32 elements of a row
+    (mq_mx4; the layout is in include/mq.h). Made from its uint8 tensors, codes
+    [pieces][rows][128] and scales [pieces][rows][8] with pieces = ceil(cols / 256), or by
+    :meth:`empty`."""
+
+    def __init__(self, rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor):
+        self.shape = torch.Size((rows, cols))
+        pieces, dev = -(-cols // MQ_MX4_PIECE), codes.get_device()
+        self.device, self.codes, self.scales = codes.device, codes, scales
+        self.struct = mq_mx4(rows, cols,
+                             _dense(codes, torch.uint8, (pieces, rows, MQ_MX4_PIECE // 2), "codes", dev),
+                             _dense(scales, torch.uint8, (pieces, rows, MQ_MX4_PIECE // MQ_MX4_BLOCK),
+                                    "scales", dev))
+        self._ref, self._dev = ctypes.byref(self.struct), dev
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device: Union[str, torch.device] = "cuda") -> "MX4":
+        """Room for a matrix (its memory is not cleared: mq_mx4_quantize writes all of it)."""
+        pieces = -(-cols // MQ_MX4_PIECE)
+        new = lambda width: torch.empty((pieces, rows, width), dtype=torch.uint8, device=device)
+        return cls(rows, cols, new(MQ_MX4_PIECE // 2), new(MQ_MX4_PIECE // MQ_MX4_BLOCK))
+
+    def ref(self, device: int):
+        """The structure, for a call on that device."""
+        if device != self._dev:
+            raise ValueError(f"MX4 matrix on {self.device}, but the current device is cuda:{device}")
+        return self._ref
+
+
+def _scratch(ws: Optional[torch.Tensor], device: int):
+    """Address and size of a workspace."""
+    if ws is None:
+        return None, 0
+    return _dense(ws, torch.uint8, ws.shape, "ws", device), ws.numel()
+
+
+def _mx4_workspace(name: str, m: int, n: int, k: int, device) -> torch.Tensor:
+    if min(m, n, k) < 0 or max(m, n, k) >= 1 << 30:
+        raise ValueError(f"sizes {m}, {n}, {k}: expected 0 to 2^30 - 1")
+    return torch.empty(getattr(_lib, f"mq_mx4_{name}_workspace_bytes")(m, n, k), dtype=torch.uint8,
+                       device=device)
+
+
+def mx4_matmul_workspace(m: int, n: int, k: int, device: Union[str, torch.device] = "cuda") -> torch.Tensor:
+    """Device scratch for mq_mx4_matmul calls of up to m rows (so for the other calls)."""
+    return _mx4_workspace("matmul", m, n, k, device)
+
+
+def mx4_linear_workspace(m: int, n: int, k: int, device: Union[str, torch.device] = "cuda") -> torch.Tensor:
+    return _mx4_workspace("linear", m, n, k, device)
+
+
+def mx4_linear_backward_workspace(m: int, n: int, k: int,
+                                  device: Union[str, torch.device] = "cuda") -> torch.Tensor:
+    return _mx4_workspace("linear_backward", m, n, k, device)
+
+
+def mx4_gated_workspace(m: int, f: int, k: int, device: Union[str, torch.device] = "cuda") -> torch.Tensor:
+    return _mx4_workspace("gated", m, f, k, device)
+
+
+def mx4_gated_backward_workspace(m: int, f: int, k: int,
+                                 device: Union[str, torch.device] = "cuda") -> torch.Tensor:
+    return _mx4_workspace("gated_backward", m, f, k, device)
+
+
+def mq_mx4_quantize(x: torch.Tensor, row: Optional[MX4] = None, col: Optional[MX4] = None,
+                    rnd: int = MQ_RNE, seed: int = 0, stream=None):
+    """Quantize x [rows][cols] along its rows into row (rows x cols), along its columns into col
+    (cols x rows), or both from one read."""
+    dev = _current_device()
+    st = _lib.mq_mx4_quantize(_matrix(x, "x", dev), None if row is None else row.ref(dev),
+                              None if col is None else col.ref(dev), rnd, seed & (2 ** 64 - 1),
+                              _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_mx4_quantize")
+
+
+def mq_mx4_dequantize(q: MX4, out: torch.Tensor, stream=None) -> torch.Tensor:
+    """The values of q, rounded to out's type, into out (which is returned)."""
+    dev = _current_device()
+    st = _lib.mq_mx4_dequantize(q.ref(dev), _matrix(out, "out", dev),
+                                _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_mx4_dequantize")
+    return out
+
+
+def mq_mx4_matmul(a: MX4, b: MX4, y: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None):
+    """y = a b^T for quantized a (M x K) and b (N x K)."""
+    dev = _current_device()
+    pw, size = _scratch(ws, dev)
+    st = _lib.mq_mx4_matmul(a.ref(dev), b.ref(dev), _matrix(y, "y", dev), pw, size,
+                            _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_mx4_matmul")
+
+
+def mq_mx4_linear(x: torch.Tensor, w: MX4, y: torch.Tensor, ws: Optional[torch.Tensor],
+                  x_col: Optional[MX4] = None, stream=None):
+    """y = Q(x) w^T for dense x [M][K] and a quantized weight (N x K); x_col (K x M), if given,
+    receives x quantized along its columns, for mq_mx4_linear_backward."""
+    dev = _current_device()
+    pw, size = _scratch(ws, dev)
+    st = _lib.mq_mx4_linear(_matrix(x, "x", dev), w.ref(dev), _matrix(y, "y", dev),
+                            None if x_col is None else x_col.ref(dev), pw, size,
+                            _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_mx4_linear")
+
+
+def mq_mx4_linear_backward(dy: torch.Tensor, x_col: Optional[MX4], w_col: Optional[MX4],
+                           dx: Optional[torch.Tensor], dw: Optional[torch.Tensor],
+                           ws: Optional[torch.Tensor], rnd: int = MQ_RNE, seed: int = 0,
+                           stream=None):
+    """Gradients of mq_mx4_linear for dy [M][N]: dx [M][K] from the weight along its columns
+    (w_col, K x N), dw [N][K] from the input along its columns (x_col, K x M); either may be None."""
+    dev = _current_device()
+    pw, size = _scratch(ws, dev)
+    st = _lib.mq_mx4_linear_backward(_matrix(dy, "dy", dev), None if x_col is None else x_col.ref(dev),
+                                     None if w_col is None else w_col.ref(dev),
+                                     None if dx is None else _matrix(dx, "dx", dev),
+                                     None if dw is None else _matrix(dw, "dw", dev), rnd,
+                                     seed & (2 ** 64 - 1), pw, size,
+                                     _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_mx4_linear_backward")
+
+
+def mq_mx4_gated(x: torch.Tensor, wg: MX4, wu: MX4, h: torch.Tensor, ws: Optional[torch.Tensor],
+                 g: Optional[torch.Tensor] = None, u: Optional[torch.Tensor] = None,
+                 x_col: Optional[MX4] = None, stream=None):
+    """h = silu(G) * U with G = Q(x) wg^T, U = Q(x) wu^T, in one kernel; g and u, if given, receive
+    G and U for mq_mx4_gated_backward, x_col (K x M) x quantized along its columns."""
+    dev = _current_device()
+    pw, size = _scratch(ws, dev)
+    st = _lib.mq_mx4_gated(_matrix(x, "x", dev), wg.ref(dev), wu.ref(dev), _matrix(h, "h", dev),
+                           None if g is None else _matrix(g, "g", dev),
+                           None if u is None else _matrix(u, "u", dev),
+                           None if x_col is None else x_col.ref(dev), pw, size,
+                           _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_mx4_gated")
+
+
+def mq_mx4_gated_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, x_col: Optional[MX4],
+                          wg_col: Optional[MX4], wu_col: Optional[MX4], dx: Optional[torch.Tensor],
+                          dwg: Optional[torch.Tensor], dwu: Optional[torch.Tensor],
+                          ws: Optional[torch.Tensor], rnd: int = MQ_RNE, seed: int = 0, stream=None):
+    """Gradients of mq_mx4_gated for dh [M][F] from the g and u that it kept: dx [M][K] (or None)
+    from the weights along their columns (K x F), dwg and dwu [F][K] (or both None) from the input
+    along its columns (x_col, K x M)."""
+    dev = _current_device()
+    pw, size = _scratch(ws, dev)
+    held = [None if q is None else q.ref(dev) for q in (x_col, wg_col, wu_col)]
+    out = [None if t is None else _matrix(t, name, dev)
+           for name, t in (("dx", dx), ("dwg", dwg), ("dwu", dwu))]
+    st = _lib.mq_mx4_gated_backward(_matrix(dh, "dh", dev), _matrix(g, "g", dev), _matrix(u, "u", dev),
+                                    *held, *out, rnd, seed & (2 ** 64 - 1), pw, size,
+                                    _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise MQError(st, "mq_mx4_gated_backward")

@@ -1,0 +1,63 @@
+// mq_mx4.hpp -- what the microscaled 4-bit linear layers share (internal).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/mq.h"
+
+namespace mq {
+
+constexpr int kMxBlock = MQ_MX4_BLOCK; // elements per scale
+constexpr int kMxPiece = MQ_MX4_PIECE; // columns that lie together
+constexpr int kMxScaleMin = 2;         // smallest scale byte written: the step of the smallest
+                                       // codes, 2^-1 * 2^(2-127), is the smallest normal fp32
+constexpr int kMxScaleMax = 252;       // largest: its code 6 is 1.5 * 2^127
+
+// A quantized matrix (mq_mx4): piece p of row r at codes + (p * rows + r) * 128 and
+// scales + (p * rows + r) * 8.
+struct Mx4View {
+    uint8_t *codes, *scales;
+    int rows, cols;
+    __host__ __device__ int pieces() const { return (cols + kMxPiece - 1) / kMxPiece; }
+};
+
+struct MatView {
+    void *p;
+    int64_t stride; // elements
+    int dtype;
+};
+
+// What is quantized: a matrix, or one of the gradients of h = silu(g) u for dh (row- and
+// column-wise; `col` is its transpose along its rows). rows, cols: the matrix's.
+struct Mx4QuantArgs {
+    MatView x;       // or dh
+    MatView g, u;    // gradients only
+    int rows, cols;
+    Mx4View row, col;   // codes null: not wanted
+    Mx4View row2, col2; // gradients: of u (row, col: of g)
+    int sr;
+    uint32_t seed_lo, seed_hi;
+};
+
+// y_j = sum over s of a[j][s] b[j][s]^T for j < jobs (the same M x N each); s = 1 only where
+// pieces[1] > 0. Gated: job 0's b[0] and b[1] are the two weights, of the one operand a[0], and y[0]
+// receives silu(G) U, g and u (null: not wanted) the products themselves.
+struct Mx4MatmulArgs {
+    Mx4View a[2][2], b[2][2];
+    MatView y[2], g, u;
+    int jobs, m, n;
+    int pieces[2];
+    bool gated;
+    void *ws;
+};
+
+hipError_t launch_mx4_quantize(const Mx4QuantArgs &a, hipStream_t st);
+hipError_t launch_mx4_gradients(const Mx4QuantArgs &a, hipStream_t st);
+hipError_t launch_mx4_dequantize(const Mx4View &q, const MatView &out, hipStream_t st);
+hipError_t launch_mx4_matmul(const Mx4MatmulArgs &a, hipStream_t st);
+// bytes of a.ws for m x n outputs from k columns (0: none); no smaller for smaller m
+size_t mx4_matmul_workspace(int jobs, int m, int n, int k);
+
+} // namespace mq
