@@ -11,7 +11,7 @@ LIB = os.path.join(HERE, "libmq.so")
 SOURCES = ["mq_api.cpp", "mq_relayout.hip", "mq_quantize.hip", "mq_conv.hip",
            "mq_conv_spatial.hip", "mq_conv_wgrad.hip", "mq_noalloc.hip", "mq_attn_api.cpp",
            "mq_attn_cached.hip", "mq_attn_prompt.hip", "mq_kv.hip", "mq_mx4_api.cpp",
-           "mq_mx4_quantize.hip", "mq_mx4_matmul.hip"]
+           "mq_mx4_quantize.hip", "mq_mx4_matmul.hip", "mq_mx4_rows.hip"]
 
 # -ffp-contract=off: the quantizer's fp32 scale arithmetic must round every operation as written.
 # fp32 division stays IEEE-correct (hipcc's default) and fp32 denormals are kept (no

@@ -50,6 +50,9 @@ struct Mx4MatmulArgs {
     int jobs, m, n;
     int pieces[2];
     bool gated;
+    bool vec;       // set by the launch: rows of the outputs are 16-byte aligned
+    MatView x;      // null, or a[0][0] still dense (mx4_quantizes_rows): m rows of `cols`
+    int cols;
     void *ws;
 };
 
@@ -57,6 +60,9 @@ hipError_t launch_mx4_quantize(const Mx4QuantArgs &a, hipStream_t st);
 hipError_t launch_mx4_gradients(const Mx4QuantArgs &a, hipStream_t st);
 hipError_t launch_mx4_dequantize(const Mx4View &q, const MatView &out, hipStream_t st);
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs &a, hipStream_t st);
+// whether launch_mx4_matmul takes these m rows dense, and quantizes them itself
+bool mx4_quantizes_rows(int m, int n, int k);
+hipError_t launch_mx4_rows(const Mx4MatmulArgs &a, hipStream_t st); // m <= 16
 // bytes of a.ws for m x n outputs from k columns (0: none); no smaller for smaller m
 size_t mx4_matmul_workspace(int jobs, int m, int n, int k);
 

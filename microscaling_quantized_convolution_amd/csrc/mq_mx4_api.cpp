@@ -89,6 +89,17 @@ mq::Mx4MatmulArgs matmul_args(const mq::Mx4View &a, const mq::Mx4View &b, const 
     return m;
 }
 
+// A layer's input: quantized along its rows into the workspace (unless the product does that) and
+// along its columns into x_col, if given.
+mq_status quantize_input(const mq_matrix *x, const mq_mx4 *x_col, bool inside, uint8_t *&at, mq::Mx4View &row, hipStream_t stream)
+{
+    mq::Mx4QuantArgs q = quantize_args(x, MQ_RNE, 0);
+    row = take(at, x->rows, x->cols);
+    if (!inside) q.row = row;
+    q.col = view(x_col);
+    return inside || x->rows == 0 || x->cols == 0 ? MQ_OK : launched(mq::launch_mx4_quantize(q, stream));
+}
+
 bool sizes_ok(int32_t a, int32_t b, int32_t c) { return a >= 0 && b >= 0 && c >= 0 && fits(a, b, c); }
 
 size_t max2(size_t a, size_t b) { return a > b ? a : b; }
@@ -161,15 +172,14 @@ mq_status mq_mx4_linear(const mq_matrix *x, const mq_mx4 *w, const mq_matrix *y,
     if (!fits(x->rows, x->cols, w->rows)) return MQ_ERR_UNSUPPORTED;
     const size_t need = mq_mx4_linear_workspace_bytes(x->rows, w->rows, x->cols);
     if (need && (!ws || ws_bytes < need)) return MQ_ERR_WORKSPACE;
+    mq::Mx4View row;
     uint8_t *at = static_cast<uint8_t *>(ws);
-    mq::Mx4QuantArgs q = quantize_args(x, MQ_RNE, 0);
-    q.row = take(at, x->rows, x->cols);
-    q.col = view(x_col);
-    if (x->rows && x->cols) {
-        const mq_status st = launched(mq::launch_mx4_quantize(q, stream));
-        if (st != MQ_OK) return st;
-    }
-    return launched(mq::launch_mx4_matmul(matmul_args(q.row, view(w), y, at), stream));
+    const bool inside = !x_col && mq::mx4_quantizes_rows(x->rows, w->rows, x->cols);
+    const mq_status st = quantize_input(x, x_col, inside, at, row, stream);
+    if (st != MQ_OK) return st;
+    mq::Mx4MatmulArgs a = matmul_args(row, view(w), y, at);
+    if (inside) a.x = view(x), a.cols = x->cols;
+    return launched(mq::launch_mx4_matmul(a, stream));
 }
 
 size_t mq_mx4_linear_backward_workspace_bytes(int32_t m, int32_t n, int32_t k)
@@ -221,15 +231,13 @@ mq_status mq_mx4_gated(const mq_matrix *x, const mq_mx4 *wg, const mq_mx4 *wu, c
     if (!fits(m, f, k)) return MQ_ERR_UNSUPPORTED;
     const size_t need = mq_mx4_gated_workspace_bytes(m, f, k);
     if (need && (!ws || ws_bytes < need)) return MQ_ERR_WORKSPACE;
+    mq::Mx4View row;
     uint8_t *at = static_cast<uint8_t *>(ws);
-    mq::Mx4QuantArgs q = quantize_args(x, MQ_RNE, 0);
-    q.row = take(at, m, k);
-    q.col = view(x_col);
-    if (m && k) {
-        const mq_status st = launched(mq::launch_mx4_quantize(q, stream));
-        if (st != MQ_OK) return st;
-    }
-    mq::Mx4MatmulArgs a = matmul_args(q.row, view(wg), h, at);
+    const bool inside = !x_col && mq::mx4_quantizes_rows(m, f, k);
+    const mq_status st = quantize_input(x, x_col, inside, at, row, stream);
+    if (st != MQ_OK) return st;
+    mq::Mx4MatmulArgs a = matmul_args(row, view(wg), h, at);
+    if (inside) a.x = view(x), a.cols = k;
     a.b[0][1] = view(wu);
     a.g = view(g);
     a.u = view(u);

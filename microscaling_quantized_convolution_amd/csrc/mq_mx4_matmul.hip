@@ -1,108 +1,329 @@
 // mq_mx4_matmul.hip -- products of microscaled 4-bit matrices, y = a b^T.
 #include "mq_mx4_device.hpp"
 
+#include <type_traits>
+#include <utility>
+
 namespace mq {
 namespace {
 
-// The 16 bytes of one block as an operand: lane (row n, half h) of the 32x32x64 product takes the
-// 32 elements of one block, whose scale is byte S of `scales`.
-__device__ __forceinline__ i32x8_t operand(u32x4_t c)
+// 64 lanes x 16 bytes from base + off (bytes, per lane) to 1 KB of LDS at byte `lds`. The caller
+// waits (vmcnt) before the data is read. Nothing is returned in registers.
+__device__ __forceinline__ void load_to_lds(const void *base, uint32_t off, uint32_t lds)
 {
-    return i32x8_t{(int)c[0], (int)c[1], (int)c[2], (int)c[3], 0, 0, 0, 0};
+    asm volatile("s_mov_b32 m0, %0\n\t"
+                 "s_nop 0\n\t"
+                 "global_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(base)
+                 : "memory");
 }
 
-template <int S>
-__device__ __forceinline__ f32x16_t product(u32x4_t a, uint32_t sa, u32x4_t b, uint32_t sb, f32x16_t c)
+// The same, 64 lanes x 4 bytes to 256 bytes of LDS.
+__device__ __forceinline__ void load_word_to_lds(const void *base, uint32_t off, uint32_t lds)
 {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a), operand(b), c, 4, 4, S, (int)sa, S, (int)sb);
+    asm volatile("s_mov_b32 m0, %0\n\t"
+                 "s_nop 0\n\t"
+                 "global_load_lds_dword %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(base)
+                 : "memory");
 }
 
-// One row's share of a piece for one lane: blocks 4h .. 4h+3 and their scales.
-struct Share {
-    u32x4_t c[4];
-    uint32_t s;
-};
-__device__ __forceinline__ Share load_share(const Mx4View &q, int piece, int row, int h)
+// All but the wave's last LEFT loads into LDS have arrived, every read of LDS is done, for all waves.
+template <int LEFT>
+__device__ __forceinline__ void lds_barrier()
 {
-    const int64_t at = (int64_t)piece * q.rows + row;
-    Share r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.c[i] = *(const u32x4_t *)(q.codes + at * 128 + (4 * h + i) * 16);
-    r.s = *(const uint32_t *)(q.scales + at * 8 + 4 * h);
-    return r;
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\t"
+                 "s_barrier" ::"n"(LEFT)
+                 : "memory");
 }
-__device__ __forceinline__ f32x16_t product(const Share &a, const Share &b, f32x16_t c)
+
+__device__ __forceinline__ uint32_t lds_address(const void *p)
 {
-    c = product<0>(a.c[0], a.s, b.c[0], b.s, c);
-    c = product<1>(a.c[1], a.s, b.c[1], b.s, c);
-    c = product<2>(a.c[2], a.s, b.c[2], b.s, c);
-    return product<3>(a.c[3], a.s, b.c[3], b.s, c);
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+
+__device__ __forceinline__ u32x4_t read_lds(uint32_t at)
+{
+    typedef const __attribute__((address_space(3))) u32x4_t *lp;
+    return *(lp)(uintptr_t)at;
+}
+
+// The lane's 16 accumulators of a 32 x 32 tile, row r, columns 8 (k / 4) + 4 h + k % 4 from c on:
+// lanes h = 0 and 1 of a row exchange fours, so that each holds two runs of 8 columns.
+__device__ __forceinline__ uint32_t read_lds_word(uint32_t at)
+{
+    typedef const __attribute__((address_space(3))) uint32_t *lp;
+    return *(lp)(uintptr_t)at;
 }
 
 template <int DT>
-__device__ __forceinline__ void put(const MatView &y, int64_t r, int c, float v)
+__device__ __forceinline__ void put_tile(const MatView &y, bool vec, int r, int c, int rows, int cols, int h, f32x16_t v)
 {
-    static_cast<typename Dense<DT>::T *>(y.p)[r * y.stride + c] = Dense<DT>::store(v);
-}
-
-// A wave for each 32 x 32 of the output, operands straight from memory.
-template <int DT, bool GATED>
-__global__ void __launch_bounds__(256) mx4_matmul_kernel(Mx4MatmulArgs a, int tiles_n)
-{
-    const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
-    const int64_t tile = blockIdx.x * (int64_t)4 + (threadIdx.x >> 6);
-    const int tm = (int)(tile / tiles_n) * 32, tn = (int)(tile % tiles_n) * 32;
-    if (tm >= a.m) return;
-    const int job = blockIdx.y;
-    const int rm = min(tm + n, a.m - 1), rn = min(tn + n, a.n - 1);
-    f32x16_t acc[2];
+    typedef typename Dense<DT>::T T;
+    float o[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.0f;
-    for (int p = 0; p < a.pieces[0]; ++p) {
-        const Share x = load_share(a.a[job][0], p, rm, h);
-        acc[0] = product(x, load_share(a.b[job][0], p, rn, h), acc[0]);
-        if constexpr (GATED) acc[1] = product(x, load_share(a.b[job][1], p, rn, h), acc[1]);
-    }
-    if constexpr (!GATED)
-        for (int p = 0; p < a.pieces[1]; ++p)
-            acc[0] = product(load_share(a.a[job][1], p, rm, h), load_share(a.b[job][1], p, rn, h), acc[0]);
-    if (tn + n >= a.n) return;
+    for (int g = 0; g < 4; g += 2)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int r = tm + 8 * (i / 4) + 4 * h + i % 4;
-        if (r >= a.m) continue;
-        if constexpr (GATED) {
-            const float g = acc[0][i], u = acc[1][i];
-            put<DT>(a.y[0], r, tn + n, g * sigmoid(g) * u);
-            if (a.g.p) put<DT>(a.g, r, tn + n, g);
-            if (a.u.p) put<DT>(a.u, r, tn + n, u);
+        for (int k = 0; k < 4; ++k) {
+            const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[4 * g + k]), __float_as_uint(v[4 * g + 4 + k]), false, false);
+            o[4 * g + k] = __uint_as_float(s[0]);
+            o[4 * g + 4 + k] = __uint_as_float(s[1]);
+        }
+    if (r >= rows) return;
+    T *row = static_cast<T *>(y.p) + r * y.stride;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int at = c + 16 * g + 8 * h;
+        T e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k] = Dense<DT>::store(o[8 * g + k]);
+        if (vec && at + 8 <= cols) {
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(T) / 2; ++k) *((u32x4_t *)(row + at) + k) = ((const u32x4_t *)e)[k];
         } else {
-            put<DT>(a.y[job], r, tn + n, acc[0][i]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (at + k < cols) row[at + k] = e[k];
         }
     }
 }
 
-template <int DT>
-hipError_t matmul(const Mx4MatmulArgs &a, hipStream_t st)
+// f(0), ..., f(N - 1), each with its number as a type
+template <int N, class F, int... I>
+__device__ __forceinline__ void unroll_(F &&f, std::integer_sequence<int, I...>) { (f(std::integral_constant<int, I>{}), ...); }
+template <int N, class F>
+__device__ __forceinline__ void unroll(F &&f) { unroll_<N>(f, std::make_integer_sequence<int, N>{}); }
+
+// WM x WN waves, each of TM x TN tiles of 32 x 32; STAGES pieces in LDS.
+template <int DT, bool GATED, int WM, int WN, int TM, int TN, int STAGES>
+__global__ void __launch_bounds__(WM * WN * 64, WM * WN == 4 && (WM * TM + WN * TN) * 32 * 136 * STAGES > 80 * 1024 ? 1 : 2) mx4_matmul_kernel(Mx4MatmulArgs a, int tiles_m, int tiles_n)
 {
-    const int tiles_n = (a.n + 31) / 32;
-    const int64_t grid = ((int64_t)((a.m + 31) / 32) * tiles_n + 3) / 4;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    constexpr int W = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
+    constexpr int LA = BM / 8 / W, LB = BN / 8 / W; // 1 KB pieces of a stage to each wave
+    constexpr int ON = GATED ? BN / 2 : BN;         // output columns of a tile
+    constexpr int LZ = (BM + BN + W * 32 - 1) / (W * 32), ZR = LZ * W * 32; // 32 rows' scales to a load; the
+                                                                            // last wave's may be no one's
+    __shared__ __align__(256) uint8_t as[STAGES][BM * 128], bs[STAGES][BN * 128], zs[STAGES][ZR * 8];
+    static_assert(BM % (W * 8) == 0 && BN % (W * 8) == 0, "the waves' shares are whole");
+    static_assert(LA % 2 == 0 && LB % 2 == 0, "");
+    static_assert(BM / 32 % LZ == 0 && ON / 32 % LZ == 0, "a wave's scales are of one operand");
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 31, h = lane >> 5, wm = wave / WN, wn = wave % WN;
+    const int job = blockIdx.y;
+    // workgroups go to the 8 XCDs in turn: each XCD receives one stretch of the tiles, eight rows of
+    // tiles to a band
+    int tile = blockIdx.x;
+    {
+        const int count = tiles_m * tiles_n, per = count / 8, rest = count % 8, x = tile % 8;
+        tile = x * per + min(x, rest) + tile / 8;
+    }
+    constexpr int BAND = 8;
+    const int band = tile / (BAND * tiles_n), in = tile % (BAND * tiles_n);
+    const int high = min(BAND, tiles_m - band * BAND);
+    const int m0 = (band * BAND + in % high) * BM, n0 = in / high * ON;
+
+    // Where the lane's 16 bytes of each 1 KB come from: block (lane % 8) ^ (row / 2 % 8) of its row,
+    // so that 16 rows' blocks of one number lie in different banks; the last row again past it.
+    const uint32_t block = ((lane & 7) ^ (lane >> 4)) * 16;
+    const int b_part = GATED ? wave / (W / 2) : 0, b_wave = GATED ? wave % (W / 2) : wave;
+    uint32_t from_a = (wave * LA * 8 + (lane >> 3)) * 128 + block, lim_a = (a.m - 1 - m0) * 128 + block;
+    uint32_t from_b = (b_wave * LB * 8 + (lane >> 3)) * 128 + block, lim_b = (a.n - 1 - n0) * 128 + block;
+    const uint32_t lds_a = lds_address(&as[0][0]), lds_b = lds_address(&bs[0][0]), lds_z = lds_address(&zs[0][0]);
+    // rows of the lane's operands, whose scales it takes four blocks to a word
+    const auto b_row = [&](int j) {
+        return GATED ? (j / (TN / 2)) * ON + (wn * (TN / 2) + j % (TN / 2)) * 32 : (wn * TN + j) * 32;
+    };
+    // the wave's share of the scales: 32 rows to a load, 4 blocks to a lane; the first waves take a's
+    const int z_row = wave * LZ * 32, z_part = z_row < BM ? 0 : (GATED && z_row >= BM + ON ? 2 : 1);
+    const int z_first = z_part == 0 ? z_row : z_row - BM - (z_part == 2 ? ON : 0);
+    uint32_t from_z = z_first * 8 + lane * 4, lim_z = ((z_part == 0 ? a.m - m0 : a.n - n0) - 1) * 8 + (lane & 1) * 4;
+
+    // the piece that is loaded next
+    const int total = GATED ? a.pieces[0] : a.pieces[0] + a.pieces[1];
+    const uint8_t *ca, *cb, *cz;
+    int64_t rows_a, rows_b;
+    const auto open = [&](int s) {
+        const Mx4View va = a.a[job][s], vb = a.b[job][GATED ? b_part : s];
+        rows_a = va.rows;
+        rows_b = vb.rows;
+        ca = va.codes + (int64_t)m0 * 128;
+        cb = vb.codes + (int64_t)n0 * 128;
+        cz = z_part == 0 ? va.scales + (int64_t)m0 * 8 : a.b[job][GATED ? z_part - 1 : s].scales + (int64_t)n0 * 8;
+    };
+    int next = 0;
+    const auto advance = [&] {
+        ++next;
+        if (next >= total) return; // the last piece again: nothing reads it
+        if (!GATED && next == a.pieces[0]) return open(1);
+        ca += rows_a * 128;
+        cb += rows_b * 128;
+        cz += (z_part == 0 ? rows_a : rows_b) * 8;
+    };
+    // load i of the wave's LOADS of the next piece
+    constexpr int LOADS = LZ + LA + LB;
+    const auto stage = [&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        const int slot = next % STAGES;
+        if constexpr (i < LZ)
+            load_word_to_lds(cz, min(from_z + i * 256, lim_z), lds_z + slot * ZR * 8 + (wave * LZ + i) * 256);
+        else if constexpr (i < LZ + LA)
+            load_to_lds(ca, min(from_a + (i - LZ) * 1024, lim_a) ^ ((i - LZ) % 2 * 64), lds_a + slot * BM * 128 + (wave * LA + i - LZ) * 1024);
+        else
+            load_to_lds(cb, min(from_b + (i - LZ - LA) * 1024, lim_b) ^ ((i - LZ - LA) % 2 * 64), lds_b + slot * BN * 128 + (wave * LB + i - LZ - LA) * 1024);
+    };
+    f32x16_t acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    if (total > 0) {
+        open(!GATED && a.pieces[0] == 0);
+        unroll<STAGES - 1>([&](auto) {
+            unroll<LOADS>(stage);
+            advance();
+        });
+    }
+    for (int p = 0; p < total; ++p) {
+        lds_barrier<(STAGES - 2) * LOADS>(); // piece p is there, piece p - 1 is no longer read
+        const int at = p % STAGES;
+        const uint32_t at_a = lds_a + at * BM * 128 + (wm * TM * 32 + n) * 128;
+        const uint32_t at_b = lds_b + at * BN * 128 + n * 128;
+        u32x4_t fa[2][TM], fb[2][TN];
+        const auto fetch = [&](auto sc) {
+            constexpr int S = decltype(sc)::value;
+            const uint32_t slot = (uint32_t)((4 * h + S) ^ (n / 2 & 7)) * 16;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb[S & 1][j] = read_lds(at_b + b_row(j) * 128 + slot);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[S & 1][i] = read_lds(at_a + i * 4096 + slot);
+        };
+        fetch(std::integral_constant<int, 0>{});
+        uint32_t sa[TM], sb[TN];
+        const uint32_t at_z = lds_z + at * ZR * 8 + n * 8 + h * 4;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sb[j] = read_lds_word(at_z + (BM + b_row(j)) * 8);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sa[i] = read_lds_word(at_z + (wm * TM + i) * 256);
+        // (the addresses of a piece's loads are made anew: kept, they would not fit)
+        asm volatile("" : "+v"(from_a), "+v"(from_b), "+v"(from_z));
+        unroll<4>([&](auto sc) {
+            constexpr int S = decltype(sc)::value;
+            if constexpr (S < 3) fetch(std::integral_constant<int, S + 1>{});
+            unroll<TM>([&](auto tc) {
+                constexpr int i = decltype(tc)::value;
+                unroll<LOADS>([&](auto lc) {
+                    constexpr int l = decltype(lc)::value;
+                    if constexpr (l * 1 * TM / LOADS == S * TM + i) stage(lc);
+                });
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    acc[i][j] = product<S>(fb[S & 1][j], sb[j], fa[S & 1][i], sa[i], acc[i][j]);
+                    asm volatile("" : "+v"(acc[i][j])); // here, in the order of the loads
+                }
+            });
+        });
+        advance();
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); // no load into LDS outlives the workgroup
+    // accumulator k of lane (n, h): row n of the tile, column 8 (k / 4) + 4 h + k % 4
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int r = m0 + (wm * TM + i) * 32 + n;
+#pragma unroll
+        for (int j = 0; j < (GATED ? TN / 2 : TN); ++j) {
+            const int c = n0 + (GATED ? (wn * (TN / 2) + j) * 32 : b_row(j));
+            if constexpr (GATED) {
+                f32x16_t out;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) out[k] = silu(acc[i][j][k]) * acc[i][j + TN / 2][k];
+                put_tile<DT>(a.y[0], a.vec, r, c, a.m, a.n, h, out);
+                if (a.g.p) {
+                    put_tile<DT>(a.g, a.vec, r, c, a.m, a.n, h, acc[i][j]);
+                    put_tile<DT>(a.u, a.vec, r, c, a.m, a.n, h, acc[i][j + TN / 2]);
+                }
+            } else {
+                put_tile<DT>(a.y[job], a.vec, r, c, a.m, a.n, h, acc[i][j]);
+            }
+        }
+    }
+}
+
+template <int DT, bool GATED, int WM, int WN, int TM, int TN, int STAGES>
+hipError_t matmul_tiles(const Mx4MatmulArgs &a, hipStream_t st)
+{
+    constexpr int BM = WM * TM * 32, BN = WN * TN * 32 / (GATED ? 2 : 1);
+    const int tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + BN - 1) / BN;
+    const int64_t grid = (int64_t)tiles_m * tiles_n;
+    if (grid > INT32_MAX / 8) return hipErrorInvalidValue;
     const dim3 g((uint32_t)grid, a.jobs);
-    if (a.gated) mx4_matmul_kernel<DT, true><<<g, 256, 0, st>>>(a, tiles_n);
-    else mx4_matmul_kernel<DT, false><<<g, 256, 0, st>>>(a, tiles_n);
+    mx4_matmul_kernel<DT, GATED, WM, WN, TM, TN, STAGES><<<g, WM * WN * 64, 0, st>>>(a, tiles_m, tiles_n);
     return hipGetLastError();
+}
+
+enum Kind { kRows, kTile64, kTile128Deep, kTile128, kTile256 };
+
+template <int DT, bool GATED>
+hipError_t matmul(const Mx4MatmulArgs &a, Kind kind, hipStream_t st)
+{
+    if (kind == kTile256) return matmul_tiles<DT, GATED, 4, 2, 2, 4, 2>(a, st);
+    if (kind == kTile128) return matmul_tiles<DT, GATED, 4, 2, 1, 2, 2>(a, st);
+    if (kind == kTile128Deep) return matmul_tiles<DT, GATED, 4, 2, 1, 2, 4>(a, st);
+    if constexpr (GATED) return matmul_tiles<DT, true, 2, 2, 1, 2, 3>(a, st);
+    else return matmul_tiles<DT, false, 2, 2, 1, 1, 4>(a, st);
+}
+
+template <int DT>
+hipError_t matmul(const Mx4MatmulArgs &a, Kind kind, hipStream_t st)
+{
+    return a.gated ? matmul<DT, true>(a, kind, st) : matmul<DT, false>(a, kind, st);
+}
+
+bool rows_aligned(const MatView &m)
+{
+    const int64_t size = m.dtype == MQ_F32 ? 4 : 2;
+    return (reinterpret_cast<uintptr_t>(m.p) & 15) == 0 && m.stride * size % 16 == 0;
+}
+
+int64_t tiles_of(const Mx4MatmulArgs &a, int bm, int bn)
+{
+    return (((int64_t)a.m + bm - 1) / bm) * (((int64_t)a.n + bn - 1) / bn) * a.jobs;
+}
+
+// Up to 16 rows, a workgroup takes 16 columns and its waves share the sum; where that makes as many
+// workgroups of 64 columns as CUs, these read the weight in larger pieces.
+bool rows_kind(int m, int64_t n) { return m <= 16 && n < 12288; }
+
+Kind kind_of(const Mx4MatmulArgs &a)
+{
+    const bool g = a.gated;
+    if (rows_kind(a.m, (int64_t)a.n * a.jobs)) return kRows;
+    if (tiles_of(a, 64, 64) <= (g ? 256 : 512)) return kTile64;
+    if (tiles_of(a, 128, g ? 64 : 128) <= 256) return kTile128Deep;
+    return tiles_of(a, 256, g ? 128 : 256) >= 512 && a.pieces[0] + a.pieces[1] >= 8 ? kTile256 : kTile128;
 }
 
 } // namespace
 
 size_t mx4_matmul_workspace(int, int, int, int) { return 0; }
 
-hipError_t launch_mx4_matmul(const Mx4MatmulArgs &a, hipStream_t st)
+bool mx4_quantizes_rows(int m, int n, int k)
 {
-    if (a.m == 0 || a.n == 0) return hipSuccess;
-    return a.y[0].dtype == MQ_BF16 ? matmul<MQ_BF16>(a, st)
-                                   : (a.y[0].dtype == MQ_F16 ? matmul<MQ_F16>(a, st) : matmul<MQ_F32>(a, st));
+    return rows_kind(m, n) && (int64_t)m * k <= 1 << 14 && (int64_t)m * k * ((n + 15) / 16) <= 1 << 22;
+}
+
+hipError_t launch_mx4_matmul(const Mx4MatmulArgs &given, hipStream_t st)
+{
+    if (given.m == 0 || given.n == 0) return hipSuccess;
+    Mx4MatmulArgs a = given;
+    a.vec = rows_aligned(a.y[0]) && rows_aligned(a.y[1]) && rows_aligned(a.g) && rows_aligned(a.u);
+    const Kind kind = kind_of(a);
+    if (kind == kRows) return launch_mx4_rows(a, st);
+    const int dt = a.y[0].dtype;
+    return dt == MQ_BF16 ? matmul<MQ_BF16>(a, kind, st) : (dt == MQ_F16 ? matmul<MQ_F16>(a, kind, st) : matmul<MQ_F32>(a, kind, st));
 }
 
 } // namespace mq

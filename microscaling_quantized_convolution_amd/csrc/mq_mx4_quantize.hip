@@ -1,117 +1,341 @@
 // mq_mx4_quantize.hip -- microscaled 4-bit quantization along rows and columns, and back.
+//
+// A block of 32 gets the smallest power of two that brings its largest magnitude to 6 or less, as a
+// byte, and 32 codes of 4 bits. Every kernel reads its input once: where rows and columns are wanted,
+// a wave holds a tile of 64 columns in registers and takes the blocks of both directions from them.
 #include "mq_mx4_device.hpp"
 
 namespace mq {
 namespace {
 
-// One of the values that are quantized: an element of x, or of a gradient of h = silu(g) u.
-enum { kPlain, kGradG, kGradU };
-template <int DT, int KIND>
-__device__ __forceinline__ float value_at(const Mx4QuantArgs &a, int r, int c)
+// Where row r of piece p lies, in rows of pieces.
+__device__ __forceinline__ int64_t place(const Mx4View &q, int p, int64_t r) { return (int64_t)p * q.rows + r; }
+
+// ---- rows alone ---------------------------------------------------------------------------------
+//
+// 8 columns and U rows to a thread, 4 threads to a block.
+template <int DT, bool SR, int U, bool TAIL>
+__global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Mx4QuantArgs a, int width, int across)
 {
     typedef typename Dense<DT>::T T;
-    const auto at = [&](const MatView &m) { return Dense<DT>::load(static_cast<const T *>(m.p)[r * m.stride + c]); };
-    const float x = at(a.x);
-    if constexpr (KIND == kPlain) return x;
-    const float g = at(a.g), s = sigmoid(g);
-    if constexpr (KIND == kGradU) return x * (g * s);
-    return x * at(a.u) * (s * (1.0f + g * (1.0f - s)));
-}
-
-// A thread for each block of 32, the blocks that fill up the last piece included.
-template <int DT, int KIND, bool COL, bool SR>
-__global__ void __launch_bounds__(256) mx4_quantize_kernel(Mx4QuantArgs a, Mx4View q)
-{
-    const int pieces = q.pieces();
-    const int64_t id = blockIdx.x * (int64_t)256 + threadIdx.x;
-    if (id >= (int64_t)q.rows * pieces * 8) return;
-    // neighbouring threads read neighbouring elements
-    const int r = COL ? (int)(id % q.rows) : (int)(id / (pieces * 8));
-    const int b = COL ? (int)(id / q.rows) : (int)(id % (pieces * 8));
-    float v[32];
+    const int groups = a.row.pieces() * 32;
+    const int g = (int)(blockIdx.x % across) * width + (int)(threadIdx.x % width);
+    const int r0 = (int)(blockIdx.x / across * (256 / width) + threadIdx.x / width) * U; // below 2^30 + 1024
+    if (g >= groups) return; // whole quads: groups is a multiple of 32
+    if (r0 >= a.rows) return;
+    const Reach reach = reach_of(g * 8, a.cols);
+    Eight<T> raw[U];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const int c = b * 32 + j;
-        v[j] = c < q.cols ? (COL ? value_at<DT, KIND>(a, c, r) : value_at<DT, KIND>(a, r, c)) : 0.0f;
+    for (int u = 0; u < U; ++u) raw[u] = load8<TAIL>(static_cast<const T *>(a.x.p) + (int64_t)min(r0 + u, a.rows - 1) * a.x.stride, reach, a.cols);
+    const int blocks = (a.cols + 31) / 32;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (r0 + u >= a.rows) return;
+        float v[8];
+        values8<DT, TAIL>(raw[u], reach, v);
+        const uint32_t e = mx4_scale(quad_max(amax8(v)));
+        const uint64_t n = 4 * ((uint64_t)(r0 + u) * blocks) + g;
+        const int64_t at = place(a.row, g >> 5, r0 + u);
+        *(uint32_t *)(a.row.codes + at * 128 + (g & 31) * 4) = encode8<SR>(v, e, n, 0, a.seed_lo, a.seed_hi);
+        if ((g & 3) == 0) a.row.scales[at * 8 + (g & 31) / 4] = (uint8_t)e;
     }
-    const uint64_t t = (uint64_t)r * (uint32_t)((q.cols + 31) / 32) + b;
-    u32x4_t codes;
-    const uint32_t e = mx4_block<SR>(v, t, (COL ? 1u : 0u) + (KIND == kGradU ? 2u : 0u), a.seed_lo, a.seed_hi, &codes);
-    const int64_t at = ((int64_t)(b / 8) * q.rows + r) * 8 + b % 8;
-    *(u32x4_t *)(q.codes + at * 16) = codes;
-    q.scales[at] = (uint8_t)e;
 }
 
+// ---- rows and columns -----------------------------------------------------------------------------
+//
+// Lane (q, cg) of a wave holds NR rows of 8 columns: 8 NR rows of 64 columns to a wave, 256 / (8 NR)
+// waves one above another to a piece of columns. A row's block lies in a quad of lanes; a column's in
+// one lane (NR = 32), or in 32 / NR of them, 8 lanes apart.
+
+// Eight values to quantize: of x, or of dg and du of h = silu(g) u.
+template <int DT, bool GRAD, bool TAIL> struct Source {
+    static constexpr int K = GRAD ? 2 : 1;
+    static __device__ __forceinline__ void load(const Mx4QuantArgs &a, int64_t r, Reach at, float (*v)[8])
+    {
+        typedef typename Dense<DT>::T T;
+        const auto get = [&](const MatView &m, float *to) {
+            values8<DT, TAIL>(load8<TAIL>(static_cast<const T *>(m.p) + r * m.stride, at, a.cols), at, to);
+        };
+        get(a.x, v[0]);
+        if constexpr (GRAD) {
+            float g[8], u[8];
+            get(a.g, g);
+            get(a.u, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float dh = v[0][i], s = sigmoid(g[i]);
+                v[0][i] = dh * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
+                v[1][i] = dh * (g[i] * s);
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t max_lane_xor_16(uint32_t v)
+{
+    const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max_u32(s[0], s[1]);
+}
+
+template <int DT, bool GRAD, int NR, bool SR, bool TAIL>
+__global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs a, int across)
+{
+    constexpr int K = Source<DT, GRAD, TAIL>::K, WR = 8 * NR, STACK = 256 / WR; // rows of a wave, waves to a piece
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 3, cg = lane & 7;
+    // a workgroup's waves: STACK of them one above another, the others beside
+    const int down = blockIdx.x / across;
+    const int c0 = (int)((blockIdx.x % across) * (4 / STACK) + wave / STACK) * 64, c = c0 + cg * 8;
+    const int r0 = (down * STACK + wave % STACK) * WR + q * NR;
+    if (c0 >= (a.row.codes ? a.row.pieces() * 256 : a.cols)) return;
+    const Reach reach = reach_of(c, a.cols);
+    float v[K][NR][8];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        float t[K][8];
+        Source<DT, GRAD, TAIL>::load(a, min(r0 + r, a.rows - 1), reach, t);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[k][r][i] = r0 + r < a.rows ? t[k][i] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const Mx4View &row = k ? a.row2 : a.row, &col = k ? a.col2 : a.col;
+        if (row.codes) {
+            const int g = c / 8, blocks = (a.cols + 31) / 32;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const uint32_t e = mx4_scale(quad_max(amax8(v[k][r])));
+                if (r0 + r >= a.rows) continue;
+                const uint64_t n = 4 * ((uint64_t)(r0 + r) * blocks) + g;
+                const int64_t at = place(row, g >> 5, r0 + r);
+                *(uint32_t *)(row.codes + at * 128 + (g & 31) * 4) = encode8<SR>(v[k][r], e, n, 2 * k, a.seed_lo, a.seed_hi);
+                if ((g & 3) == 0) row.scales[at * 8 + (g & 31) / 4] = (uint8_t)e;
+            }
+        }
+        if (col.codes) {
+            const int blocks = (a.rows + 31) / 32, part = (r0 & 255); // first row within the piece
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t amax = 0;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) amax = max_u32(amax, __float_as_uint(v[k][r][i]) & 0x7FFFFFFFu);
+                if constexpr (NR < 32) amax = max_u32(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x128, 0xF, 0xF, true)); // lane ^ 8
+                if constexpr (NR < 16) amax = max_lane_xor_16(amax);
+                const uint32_t e = mx4_scale(amax);
+                if (c + i >= a.cols) continue;
+                const int64_t at = place(col, r0 >> 8, c + i);
+                uint32_t codes[NR / 8];
+#pragma unroll
+                for (int w = 0; w < NR / 8; ++w) {
+                    float t[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) t[j] = v[k][8 * w + j][i];
+                    const uint64_t n = 4 * ((uint64_t)(c + i) * blocks) + (uint64_t)(r0 / 8 + w);
+                    codes[w] = encode8<SR>(t, e, n, 2 * k + 1, a.seed_lo, a.seed_hi);
+                }
+                uint32_t *to = (uint32_t *)(col.codes + at * 128 + part / 2);
+                if constexpr (NR == 32) *(u32x4_t *)to = *(const u32x4_t *)codes;
+                else if constexpr (NR == 16) *(uint64_t *)to = *(const uint64_t *)codes;
+                else *to = codes[0];
+                if (NR == 32 || part % 32 == 0) col.scales[at * 8 + part / 32] = (uint8_t)e;
+            }
+        }
+    }
+}
+
+// The same for 16-bit elements rounded to nearest, two to a register all the way: NR = 32.
+template <int DT, bool TAIL>
+__global__ void __launch_bounds__(256, 2) mx4_quantize_packed_kernel(Mx4QuantArgs a, int across)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 3, cg = lane & 7;
+    const int down = blockIdx.x / across;
+    const int c0 = ((int)(blockIdx.x % across) * 4 + wave) * 64, c = c0 + cg * 8;
+    const int r0 = down * 256 + q * 32;
+    if (c0 >= (a.row.codes ? a.row.pieces() * 256 : a.cols)) return;
+    const uint16_t *x = static_cast<const uint16_t *>(a.x.p) + (int64_t)r0 * a.x.stride;
+    const Reach reach = reach_of(c, a.cols);
+    Eight<uint16_t> raw[32];
+#pragma unroll
+    for (int r = 0; r < 32; ++r) raw[r] = load8<TAIL>(x + (int64_t)min(r, a.rows - 1 - r0) * a.x.stride, reach, a.cols);
+    u32x4_t d[32];
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+        d[r] = __builtin_bit_cast(u32x4_t, shifted<TAIL>(raw[r], reach));
+        if (r0 + r >= a.rows) d[r] = u32x4_t{0, 0, 0, 0};
+    }
+    typedef __attribute__((ext_vector_type(2))) uint16_t u16x2_t;
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+    typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
+    const auto max2 = [](uint32_t m, uint32_t v) {
+        const u16x2_t x = __builtin_bit_cast(u16x2_t, m), y = __builtin_bit_cast(u16x2_t, v & 0x7FFF7FFFu);
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(x, y));
+    };
+    const auto scale_of = [](uint32_t half) { return mx4_scale(__float_as_uint(Dense<DT>::load((uint16_t)half))); };
+    const auto code2 = [](uint32_t c, uint32_t two, float by, auto at) {
+        if constexpr (DT == MQ_BF16) return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, two), by, decltype(at)::value);
+        else return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2_t, two), by, decltype(at)::value);
+    };
+    const auto codes8 = [&](uint32_t e, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+        const float by = __uint_as_float((e == 255 ? 127u : e) << 23);
+        uint32_t k = code2(0, x0, by, Int<0>{});
+        k = code2(k, x1, by, Int<1>{});
+        k = code2(k, x2, by, Int<2>{});
+        k = code2(k, x3, by, Int<3>{});
+        return e == 255 ? 0u : k;
+    };
+    if (a.row.codes) {
+        const int g = c / 8;
+        const int64_t at0 = place(a.row, g >> 5, r0);
+        uint32_t *to = (uint32_t *)(a.row.codes + at0 * 128 + (g & 31) * 4);
+        uint8_t *zs = a.row.scales + at0 * 8 + (g & 31) / 4;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+            uint32_t m = max2(max2(max2(max2(0u, d[r][0]), d[r][1]), d[r][2]), d[r][3]);
+            m = quad_max(max_u32(m & 0xFFFFu, m >> 16));
+            const uint32_t e = scale_of(m), k = codes8(e, d[r][0], d[r][1], d[r][2], d[r][3]);
+            if (r0 + r < a.rows) {
+                to[r * 32] = k;
+                if ((g & 3) == 0) zs[r * 8] = (uint8_t)e;
+            }
+        }
+    }
+    if (a.col.codes) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int r = 0; r < 32; ++r) m = max2(m, d[r][k]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint32_t e = scale_of(half ? m >> 16 : m & 0xFFFFu);
+                u32x4_t codes;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t two[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        two[j] = __builtin_amdgcn_perm(d[8 * w + 2 * j + 1][k], d[8 * w + 2 * j][k], half ? 0x07060302u : 0x05040100u);
+                    codes[w] = codes8(e, two[0], two[1], two[2], two[3]);
+                }
+                const int i = c + 2 * k + half;
+                if (i >= a.cols) continue;
+                const int64_t at = place(a.col, down, i);
+                *(u32x4_t *)(a.col.codes + at * 128 + q * 16) = codes;
+                a.col.scales[at * 8 + q] = (uint8_t)e;
+            }
+        }
+    }
+}
+
+// ---- back -----------------------------------------------------------------------------------------
+
+// 8 columns to a thread.
 template <int DT>
-__global__ void __launch_bounds__(256) mx4_dequantize_kernel(Mx4View q, MatView out)
+__global__ void __launch_bounds__(256) mx4_dequantize_kernel(Mx4View q, MatView out, bool vec, int width, int across)
 {
-    const int blocks = (q.cols + 31) / 32;
-    const int64_t id = blockIdx.x * (int64_t)256 + threadIdx.x;
-    if (id >= (int64_t)q.rows * blocks) return;
-    const int r = (int)(id / blocks), b = (int)(id % blocks);
-    const int64_t at = ((int64_t)(b / 8) * q.rows + r) * 8 + b % 8;
-    const u32x4_t codes = *(const u32x4_t *)(q.codes + at * 16);
-    const uint32_t e = q.scales[at];
     typedef typename Dense<DT>::T T;
-    T *to = static_cast<T *>(out.p) + r * out.stride + b * 32;
-    for (int j = 0; j < 32 && b * 32 + j < q.cols; ++j) {
-        const uint32_t c = codes[j / 8] >> (4 * (j % 8));
+    const int g = (int)(blockIdx.x % across) * width + (int)(threadIdx.x % width);
+    const int64_t r = blockIdx.x / across * (int64_t)(256 / width) + threadIdx.x / width;
+    if (g * 8 >= q.cols || r >= q.rows) return;
+    const int64_t at = place(q, g >> 5, r);
+    const uint32_t codes = *(const uint32_t *)(q.codes + at * 128 + (g & 31) * 4);
+    const uint32_t e = q.scales[at * 8 + (g & 31) / 4];
+    T v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t c = codes >> (4 * j);
         const float m = elem_mag_to_float<kFP4>(c & 7u);
-        const float v = __builtin_amdgcn_ldexpf(c & 8u ? -m : m, (int)e - 127);
-        to[j] = Dense<DT>::store(e == 255 ? __uint_as_float(0x7FC00000u) : v);
+        const float x = __builtin_amdgcn_ldexpf(c & 8u ? -m : m, (int)e - 127);
+        v[j] = Dense<DT>::store(e == 255 ? __uint_as_float(0x7FC00000u) : x);
+    }
+    T *to = static_cast<T *>(out.p) + r * out.stride + g * 8;
+    if (vec && g * 8 + 8 <= q.cols) {
+#pragma unroll
+        for (int j = 0; j < (int)sizeof(T) / 2; ++j) ((u32x4_t *)to)[j] = ((const u32x4_t *)v)[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (g * 8 + j < q.cols) to[j] = v[j];
     }
 }
 
-template <int DT, int KIND, bool COL>
-hipError_t quantize(const Mx4QuantArgs &a, const Mx4View &q, hipStream_t st)
+// Threads to a row of `groups`, of a workgroup's 256.
+int width_of(int groups)
 {
-    if (!q.codes) return hipSuccess;
-    const int64_t threads = (int64_t)q.rows * q.pieces() * 8, grid = (threads + 255) / 256;
-    if (grid == 0) return hipSuccess;
+    int w = 32;
+    while (w < 256 && w < groups) w *= 2;
+    return w;
+}
+
+template <int DT, bool SR>
+hipError_t rows_alone(const Mx4QuantArgs &a, hipStream_t st)
+{
+    const int groups = a.row.pieces() * 32, width = width_of(groups), across = (groups + width - 1) / width;
+    // four rows to a thread hide the loads' latency, where that leaves a workgroup for every CU
+    const bool four = (int64_t)across * a.rows * width >= 4 * 256 * 512;
+    const int per = 256 / width * (four ? 4 : 1);
+    const int64_t grid = ((int64_t)a.rows + per - 1) / per * across;
     if (grid > INT32_MAX) return hipErrorInvalidValue;
-    if (a.sr) mx4_quantize_kernel<DT, KIND, COL, true><<<(uint32_t)grid, 256, 0, st>>>(a, q);
-    else mx4_quantize_kernel<DT, KIND, COL, false><<<(uint32_t)grid, 256, 0, st>>>(a, q);
+    const auto run = [&](auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        if (four) mx4_quantize_rows_kernel<DT, SR, 4, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, width, across);
+        else mx4_quantize_rows_kernel<DT, SR, 1, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, width, across);
+    };
+    if (a.cols % 8) run(Int<1>{});
+    else run(Int<0>{});
     return hipGetLastError();
 }
 
-template <int DT>
-hipError_t gradients(const Mx4QuantArgs &a, hipStream_t st)
+template <int DT, bool GRAD, int NR, bool SR>
+hipError_t both(const Mx4QuantArgs &a, hipStream_t st)
 {
-    hipError_t e = quantize<DT, kGradG, false>(a, a.row, st);
-    if (e == hipSuccess) e = quantize<DT, kGradU, false>(a, a.row2, st);
-    if (e == hipSuccess) e = quantize<DT, kGradG, true>(a, a.col, st);
-    if (e == hipSuccess) e = quantize<DT, kGradU, true>(a, a.col2, st);
-    return e;
+    const int beside = 4 / (256 / (8 * NR)) * 64; // columns of a workgroup
+    const int cols = a.row.codes ? a.row.pieces() * 256 : a.cols, across = (cols + beside - 1) / beside;
+    const int64_t grid = ((int64_t)a.rows + 255) / 256 * across;
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    const auto run = [&](auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
+        if constexpr (!GRAD && !SR && DT != MQ_F32) mx4_quantize_packed_kernel<DT, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, across);
+        else mx4_quantize_both_kernel<DT, GRAD, NR, SR, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, across);
+    };
+    if (a.cols % 8) run(Int<1>{});
+    else run(Int<0>{});
+    return hipGetLastError();
 }
 
-template <int DT>
-hipError_t plain(const Mx4QuantArgs &a, hipStream_t st)
+template <int DT, bool SR>
+hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
 {
-    const hipError_t e = quantize<DT, kPlain, false>(a, a.row, st);
-    return e == hipSuccess ? quantize<DT, kPlain, true>(a, a.col, st) : e;
+    if (grad) return both<DT, true, 8, SR>(a, st);
+    if (!a.col.codes) return rows_alone<DT, SR>(a, st);
+    return both<DT, false, DT != MQ_F32 && !SR ? 32 : 16, SR>(a, st);
+}
+
+hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
+{
+    if (a.x.dtype == MQ_BF16) return a.sr ? quantize<MQ_BF16, true>(a, grad, st) : quantize<MQ_BF16, false>(a, grad, st);
+    if (a.x.dtype == MQ_F16) return a.sr ? quantize<MQ_F16, true>(a, grad, st) : quantize<MQ_F16, false>(a, grad, st);
+    return a.sr ? quantize<MQ_F32, true>(a, grad, st) : quantize<MQ_F32, false>(a, grad, st);
 }
 
 } // namespace
 
-hipError_t launch_mx4_quantize(const Mx4QuantArgs &a, hipStream_t st)
-{
-    return a.x.dtype == MQ_BF16 ? plain<MQ_BF16>(a, st) : (a.x.dtype == MQ_F16 ? plain<MQ_F16>(a, st) : plain<MQ_F32>(a, st));
-}
+hipError_t launch_mx4_quantize(const Mx4QuantArgs &a, hipStream_t st) { return quantize(a, false, st); }
 
-hipError_t launch_mx4_gradients(const Mx4QuantArgs &a, hipStream_t st)
-{
-    return a.x.dtype == MQ_BF16 ? gradients<MQ_BF16>(a, st)
-                                : (a.x.dtype == MQ_F16 ? gradients<MQ_F16>(a, st) : gradients<MQ_F32>(a, st));
-}
+hipError_t launch_mx4_gradients(const Mx4QuantArgs &a, hipStream_t st) { return quantize(a, true, st); }
 
 hipError_t launch_mx4_dequantize(const Mx4View &q, const MatView &out, hipStream_t st)
 {
-    const int64_t threads = (int64_t)q.rows * ((q.cols + 31) / 32), grid = (threads + 255) / 256;
-    if (grid == 0) return hipSuccess;
+    if (q.rows == 0 || q.cols == 0) return hipSuccess;
+    const int groups = (q.cols + 7) / 8, width = width_of(groups), across = (groups + width - 1) / width;
+    const int64_t grid = ((int64_t)q.rows + 256 / width - 1) / (256 / width) * across;
     if (grid > INT32_MAX) return hipErrorInvalidValue;
-    if (out.dtype == MQ_BF16) mx4_dequantize_kernel<MQ_BF16><<<(uint32_t)grid, 256, 0, st>>>(q, out);
-    else if (out.dtype == MQ_F16) mx4_dequantize_kernel<MQ_F16><<<(uint32_t)grid, 256, 0, st>>>(q, out);
-    else mx4_dequantize_kernel<MQ_F32><<<(uint32_t)grid, 256, 0, st>>>(q, out);
+    const int64_t size = out.dtype == MQ_F32 ? 4 : 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(out.p) & 15) == 0 && out.stride * size % 16 == 0;
+    if (out.dtype == MQ_BF16) mx4_dequantize_kernel<MQ_BF16><<<(uint32_t)grid, 256, 0, st>>>(q, out, vec, width, across);
+    else if (out.dtype == MQ_F16) mx4_dequantize_kernel<MQ_F16><<<(uint32_t)grid, 256, 0, st>>>(q, out, vec, width, across);
+    else mx4_dequantize_kernel<MQ_F32><<<(uint32_t)grid, 256, 0, st>>>(q, out, vec, width, across);
     return hipGetLastError();
 }
 
