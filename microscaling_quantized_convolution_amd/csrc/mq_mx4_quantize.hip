@@ -43,9 +43,11 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Mx4QuantArgs a, 
 
 // ---- rows and columns -----------------------------------------------------------------------------
 //
-// Lane (q, cg) of a wave holds NR rows of 8 columns: 8 NR rows of 64 columns to a wave, 256 / (8 NR)
-// waves one above another to a piece of columns. A row's block lies in a quad of lanes; a column's in
-// one lane (NR = 32), or in 32 / NR of them, 8 lanes apart.
+// Lane (q, cg) of a wave holds NR rows of 8 columns: 8 NR rows of 64 columns to a wave, and up to four
+// waves one above another. A row's block lies in a quad of lanes; a column's in one lane (NR = 32), or
+// in 32 / NR of them, 8 lanes apart.
+
+constexpr int stack_of(int nr) { return nr >= 8 ? 32 / nr : 4; } // waves one above another
 
 // Eight values to quantize: of x, or of dg and du of h = silu(g) u.
 template <int DT, bool GRAD, bool TAIL> struct Source {
@@ -71,16 +73,22 @@ template <int DT, bool GRAD, bool TAIL> struct Source {
     }
 };
 
+// Largest value of this lane and the one 16 (32) lanes away.
 __device__ __forceinline__ uint32_t max_lane_xor_16(uint32_t v)
 {
     const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max_u32(s[0], s[1]);
+}
+__device__ __forceinline__ uint32_t max_lane_xor_32(uint32_t v)
+{
+    const auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
     return max_u32(s[0], s[1]);
 }
 
 template <int DT, bool GRAD, int NR, bool SR, bool TAIL>
 __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs a, int across)
 {
-    constexpr int K = Source<DT, GRAD, TAIL>::K, WR = 8 * NR, STACK = 256 / WR; // rows of a wave, waves to a piece
+    constexpr int K = Source<DT, GRAD, TAIL>::K, WR = 8 * NR, STACK = stack_of(NR); // rows of a wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 3, cg = lane & 7;
     // a workgroup's waves: STACK of them one above another, the others beside
     const int down = blockIdx.x / across;
@@ -122,22 +130,25 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
                 for (int r = 0; r < NR; ++r) amax = max_u32(amax, __float_as_uint(v[k][r][i]) & 0x7FFFFFFFu);
                 if constexpr (NR < 32) amax = max_u32(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x128, 0xF, 0xF, true)); // lane ^ 8
                 if constexpr (NR < 16) amax = max_lane_xor_16(amax);
+                if constexpr (NR < 8) amax = max_lane_xor_32(amax);
                 const uint32_t e = mx4_scale(amax);
                 if (c + i >= a.cols) continue;
                 const int64_t at = place(col, r0 >> 8, c + i);
-                uint32_t codes[NR / 8];
+                constexpr int E = (NR + 7) / 8;
+                uint32_t codes[E];
 #pragma unroll
-                for (int w = 0; w < NR / 8; ++w) {
+                for (int w = 0; w < E; ++w) {
+                    const uint64_t n = 4 * ((uint64_t)(c + i) * blocks) + (uint64_t)(r0 / 8 + w);
                     float t[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) t[j] = v[k][8 * w + j][i];
-                    const uint64_t n = 4 * ((uint64_t)(c + i) * blocks) + (uint64_t)(r0 / 8 + w);
+                    for (int j = 0; j < 8; ++j) t[j] = v[k][(8 * w + j) % NR][i]; // (NR = 4: twice, in either half's place)
                     codes[w] = encode8<SR>(t, e, n, 2 * k + 1, a.seed_lo, a.seed_hi);
                 }
-                uint32_t *to = (uint32_t *)(col.codes + at * 128 + part / 2);
+                uint32_t *to = (uint32_t *)(col.codes + at * 128 + (part & ~7) / 2);
                 if constexpr (NR == 32) *(u32x4_t *)to = *(const u32x4_t *)codes;
                 else if constexpr (NR == 16) *(uint64_t *)to = *(const uint64_t *)codes;
-                else *to = codes[0];
+                else if constexpr (NR == 8) *to = codes[0];
+                else ((uint16_t *)to)[part / 4 % 2] = (uint16_t)(part & 4 ? codes[0] >> 16 : codes[0]);
                 if (NR == 32 || part % 32 == 0) col.scales[at * 8 + part / 32] = (uint8_t)e;
             }
         }
@@ -290,13 +301,13 @@ hipError_t rows_alone(const Mx4QuantArgs &a, hipStream_t st)
 template <int DT, bool GRAD, int NR, bool SR>
 hipError_t both(const Mx4QuantArgs &a, hipStream_t st)
 {
-    const int beside = 4 / (256 / (8 * NR)) * 64; // columns of a workgroup
+    constexpr int down = 8 * NR * stack_of(NR), beside = 4 / stack_of(NR) * 64; // rows and columns of a workgroup
     const int cols = a.row.codes ? a.row.pieces() * 256 : a.cols, across = (cols + beside - 1) / beside;
-    const int64_t grid = ((int64_t)a.rows + 255) / 256 * across;
+    const int64_t grid = ((int64_t)a.rows + 255) / 256 * (256 / down) * across; // whole pieces of columns
     if (grid > INT32_MAX) return hipErrorInvalidValue;
     const auto run = [&](auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
-        if constexpr (!GRAD && !SR && DT != MQ_F32) mx4_quantize_packed_kernel<DT, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, across);
+        if constexpr (NR == 32) mx4_quantize_packed_kernel<DT, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, across);
         else mx4_quantize_both_kernel<DT, GRAD, NR, SR, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, across);
     };
     if (a.cols % 8) run(Int<1>{});
@@ -307,9 +318,13 @@ hipError_t both(const Mx4QuantArgs &a, hipStream_t st)
 template <int DT, bool SR>
 hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
 {
-    if (grad) return both<DT, true, 8, SR>(a, st);
-    if (!a.col.codes) return rows_alone<DT, SR>(a, st);
-    return both<DT, false, DT != MQ_F32 && !SR ? 32 : 16, SR>(a, st);
+    if (!grad && !a.col.codes) return rows_alone<DT, SR>(a, st);
+    // the tallest tiles that give each SIMD a wave: taller ones write longer runs of a column's codes
+    const auto waves = [&](int nr) { return ((int64_t)a.rows + 8 * nr - 1) / (8 * nr) * ((a.cols + 63) / 64); };
+    constexpr int TALL = DT != MQ_F32 && !SR ? 32 : 16;
+    if (grad) return waves(8) >= 1024 ? both<DT, true, 8, SR>(a, st) : both<DT, true, 4, SR>(a, st);
+    if (waves(TALL) >= 1024) return both<DT, false, TALL, SR>(a, st);
+    return waves(8) >= 1024 ? both<DT, false, 8, SR>(a, st) : both<DT, false, 4, SR>(a, st);
 }
 
 hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
