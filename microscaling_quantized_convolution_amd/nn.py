@@ -24,6 +24,14 @@ reproducible and no two layers or steps share a stream of random bits.
 In eval mode with ``cache_weight=True`` the weight is quantized once and reused until the
 parameter changes (its version counter moves): the inference path then quantizes only
 activations.
+
+``MXLinear`` and ``MXGatedMLP`` are the linear layer and the gated feed-forward block of a
+transformer on microscaled 4-bit operands (E2M1, a power-of-two scale per 32 elements along the
+contracted dimension). A training step reads each weight once for both of its directions, and the
+forward pass keeps the input in 4 bits along its columns instead of itself:
+
+  forward   W -> rows and columns (one call); Y = mq_mx4_linear(X, W rows), which also leaves X's columns
+  backward  G_Y -> rows and columns (one call, SR); G_X from W's columns, G_W from X's
 """
 from __future__ import annotations
 
@@ -32,11 +40,13 @@ from typing import List, Optional, Tuple
 import torch
 from torch import nn
 
-from . import (MQ_NVFP4, MQ_QUANTIZE_WS_BYTES, MQ_ROLE_ACT, MQ_ROLE_GRAD, MQ_ROLE_WEIGHT,
+from . import (MQ_NVFP4, MX4, MQ_QUANTIZE_WS_BYTES, MQ_ROLE_ACT, MQ_ROLE_GRAD, MQ_ROLE_WEIGHT,
                MQ_RNE, MQ_SR, MQ_SRC_NCHW, MQ_SRC_OIHW, QTensor, mq_conv_backward,
                mq_conv_dgrad, mq_conv_fwd, mq_conv_wgrad, mq_quantize_batch, mq_quantize_nchw, mq_quantize_weight,
-               mq_relayout_cbf, mq_relayout_weight, mq_wgrad_workspace_bytes, out_hw,
-               quant_job)
+               mq_mx4_gated, mq_mx4_gated_backward, mq_mx4_linear, mq_mx4_linear_backward,
+               mq_mx4_quantize, mq_relayout_cbf, mq_relayout_weight, mq_wgrad_workspace_bytes,
+               mx4_gated_backward_workspace, mx4_gated_workspace, mx4_linear_backward_workspace,
+               mx4_linear_workspace, out_hw, quant_job)
 
 
 def _check_input(t: torch.Tensor, what: str, ndim: int = 4):
@@ -175,6 +185,187 @@ class MQConv2d(nn.Module):
     def extra_repr(self) -> str:
         return (f"{self.in_channels}, {self.out_channels}, kernel_size={self.kernel_size}, "
                 f"stride={self.stride}, padding={self.padding}, fmt=NVFP{self.fmt}")
+
+
+# ---- linear layers and the gated feed-forward block on microscaled 4-bit operands --------------
+
+def _rows_of(x: torch.Tensor, cols: int, what: str) -> torch.Tensor:
+    """x [...][cols] as a matrix with contiguous rows."""
+    if not x.is_cuda or x.dtype not in (torch.float16, torch.bfloat16, torch.float32) or x.dim() < 1:
+        raise ValueError(f"{what}: expected a float16, bfloat16 or float32 CUDA tensor, got "
+                         f"{tuple(x.shape)} {x.dtype} on {x.device}")
+    if x.shape[-1] != cols:
+        raise ValueError(f"{what} has {x.shape[-1]} features, the weight expects {cols}")
+    return x.reshape(-1, cols).contiguous()
+
+
+def quantize_linear_weight(weight: torch.Tensor, columns: bool) -> Tuple[MX4, Optional[MX4]]:
+    """A weight [out][in] along its rows and, if asked, its columns, from one read (RNE)."""
+    n, k = weight.shape
+    row = MX4.empty(n, k, weight.device)
+    col = MX4.empty(k, n, weight.device) if columns else None
+    mq_mx4_quantize(weight, row, col)
+    return row, col
+
+
+class MXLinearFunction(torch.autograd.Function):
+    """Autograd function: y = x weight^T and its gradients through the library."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, weight: torch.Tensor, sr_seed: int, held: Optional[MX4]):
+        n, k = weight.shape
+        rows = _rows_of(x, k, "input")
+        m, dev = rows.shape[0], x.device
+        need_x, need_w = ctx.needs_input_grad[:2]
+        with torch.cuda.device(dev):
+            w_row, w_col = (held, None) if held is not None else quantize_linear_weight(
+                weight.detach().contiguous(), need_x)
+            if need_x and w_col is None:
+                w_col = MX4.empty(k, n, dev)
+                mq_mx4_quantize(weight.detach().contiguous(), None, w_col)
+            x_col = MX4.empty(k, m, dev) if need_w else None
+            y = torch.empty((m, n), dtype=x.dtype, device=dev)
+            mq_mx4_linear(rows, w_row, y, mx4_linear_workspace(m, n, k, dev), x_col)
+        ctx.x_col, ctx.w_col, ctx.sr_seed = x_col, w_col, sr_seed
+        ctx.sizes, ctx.shape, ctx.w_dtype = (m, n, k), x.shape, weight.dtype
+        return y.view(*x.shape[:-1], n)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gy: torch.Tensor):
+        m, n, k = ctx.sizes
+        rows, dev = _rows_of(gy, n, "gradient"), gy.device
+        dx = dw = None
+        with torch.cuda.device(dev):
+            if ctx.w_col is not None:
+                dx = torch.empty((m, k), dtype=gy.dtype, device=dev)
+            if ctx.x_col is not None:
+                dw = torch.empty((n, k), dtype=ctx.w_dtype, device=dev)
+            if dx is not None or dw is not None:
+                mq_mx4_linear_backward(rows, ctx.x_col, ctx.w_col, dx, dw,
+                                       mx4_linear_backward_workspace(m, n, k, dev), MQ_SR, ctx.sr_seed)
+        return None if dx is None else dx.view(ctx.shape), dw, None, None
+
+
+class MXGatedFunction(torch.autograd.Function):
+    """Autograd function: silu(x gate^T) * (x up^T) and its gradients through the library."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, sr_seed: int,
+                held: Optional[Tuple[MX4, MX4]]):
+        f, k = gate.shape
+        rows = _rows_of(x, k, "input")
+        m, dev = rows.shape[0], x.device
+        need_x, need_w = ctx.needs_input_grad[0], any(ctx.needs_input_grad[1:3])
+        with torch.cuda.device(dev):
+            new = lambda: torch.empty((m, f), dtype=x.dtype, device=dev)
+            if held is not None:
+                row = held
+                col = [None, None]
+                if need_x:
+                    col = [MX4.empty(k, f, dev) for _ in row]
+                    for w, q in zip((gate, up), col):
+                        mq_mx4_quantize(w.detach().contiguous(), None, q)
+            else:
+                row, col = zip(*(quantize_linear_weight(w.detach().contiguous(), need_x)
+                                 for w in (gate, up)))
+            x_col = MX4.empty(k, m, dev) if need_w else None
+            g, u = (new(), new()) if need_x or need_w else (None, None)
+            h = new()
+            mq_mx4_gated(rows, row[0], row[1], h, mx4_gated_workspace(m, f, k, dev), g, u, x_col)
+        ctx.g, ctx.u, ctx.x_col, ctx.w_col, ctx.sr_seed = g, u, x_col, col, sr_seed
+        ctx.sizes, ctx.shape, ctx.w_dtype = (m, f, k), x.shape, gate.dtype
+        return h.view(*x.shape[:-1], f)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh: torch.Tensor):
+        m, f, k = ctx.sizes
+        rows, dev = _rows_of(dh, f, "gradient"), dh.device
+        need_x, need_w = ctx.needs_input_grad[0], any(ctx.needs_input_grad[1:3])
+        dx = dwg = dwu = None
+        with torch.cuda.device(dev):
+            if need_x:
+                dx = torch.empty((m, k), dtype=dh.dtype, device=dev)
+            if need_w:
+                dwg, dwu = (torch.empty((f, k), dtype=ctx.w_dtype, device=dev) for _ in range(2))
+            if need_x or need_w:
+                mq_mx4_gated_backward(rows, ctx.g, ctx.u, ctx.x_col, ctx.w_col[0], ctx.w_col[1], dx, dwg,
+                                      dwu, mx4_gated_backward_workspace(m, f, k, dev), MQ_SR,
+                                      ctx.sr_seed)
+        return None if dx is None else dx.view(ctx.shape), dwg, dwu, None, None
+
+
+class _MXModule(nn.Module):
+    """What the 4-bit modules share: seeds of the stochastic rounding, and weights held in 4 bits
+    from one evaluation to the next (``cache_weight``) until a parameter changes."""
+
+    def __init__(self, layer_index: int, layers: int, seed_base: int, cache_weight: bool):
+        super().__init__()
+        self.layer_index, self.layers, self.seed_base = layer_index, layers, seed_base
+        self.cache_weight = cache_weight
+        self.step = 0
+        self._held: Optional[List[MX4]] = None
+        self._held_key: Optional[tuple] = None
+
+    def _next_seed(self) -> int:
+        seed = self.seed_base + self.layer_index + self.layers * self.step
+        if self.training:
+            self.step += 1
+        return seed
+
+    def _cached(self, *weights: torch.Tensor) -> Optional[List[MX4]]:
+        if self.training or not self.cache_weight:
+            return None
+        key = tuple((w.data_ptr(), w._version) for w in weights)
+        if self._held is None or self._held_key != key:
+            with torch.cuda.device(weights[0].device):
+                self._held = [quantize_linear_weight(w.detach().contiguous(), False)[0] for w in weights]
+            self._held_key = key
+        return self._held
+
+
+class MXLinear(_MXModule):
+    """Linear layer (no bias) whose forward and backward products run on 4-bit operands; fp32 master
+    weight. Inputs [...][in_features] in float16, bfloat16 or float32; outputs of their type."""
+
+    def __init__(self, in_features: int, out_features: int, layer_index: int = 0, layers: int = 1,
+                 seed_base: int = 1, cache_weight: bool = False):
+        super().__init__(layer_index, layers, seed_base, cache_weight)
+        self.in_features, self.out_features = in_features, out_features
+        self.weight = nn.Parameter(torch.empty(out_features, in_features))
+        nn.init.normal_(self.weight, std=in_features ** -0.5)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        held = self._cached(self.weight)
+        return MXLinearFunction.apply(x, self.weight, self._next_seed(), None if held is None else held[0])
+
+    def extra_repr(self) -> str:
+        return f"{self.in_features}, {self.out_features}"
+
+
+class MXGatedMLP(_MXModule):
+    """Gated feed-forward block: down(silu(x gate^T) * (x up^T)), all three products on 4-bit
+    operands; fp32 master weights."""
+
+    def __init__(self, features: int, hidden: int, layer_index: int = 0, layers: int = 1,
+                 seed_base: int = 1, cache_weight: bool = False):
+        super().__init__(2 * layer_index, 2 * layers, seed_base, cache_weight)
+        self.features, self.hidden = features, hidden
+        self.gate = nn.Parameter(torch.empty(hidden, features))
+        self.up = nn.Parameter(torch.empty(hidden, features))
+        for w in (self.gate, self.up):
+            nn.init.normal_(w, std=features ** -0.5)
+        self.down = MXLinear(hidden, features, 2 * layer_index + 1, 2 * layers, seed_base, cache_weight)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        held = self._cached(self.gate, self.up)
+        h = MXGatedFunction.apply(x, self.gate, self.up, self._next_seed(),
+                                  None if held is None else tuple(held))
+        return self.down(h)
+
+    def extra_repr(self) -> str:
+        return f"{self.features}, {self.hidden}"
 
 
 # ---- ResNet-18 with the 19 body convolutions quantized ---------------------------------------

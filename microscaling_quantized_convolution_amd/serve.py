@@ -15,7 +15,11 @@ the host, so only ``prefill``, the first token of a page and ``evict`` copy a ta
 after an eviction the heads of a sequence hold different tokens (``positions`` tells which).
 Everything runs on the current stream.
 
-``python -m microscaling_quantized_convolution_amd.serve`` runs a small batch through all three.
+``FeedForward`` is the gated feed-forward block that follows, its weights held in 4 bits:
+
+  call      mq_mx4_gated (both projections, the activation and the product), mq_mx4_linear
+
+``python -m microscaling_quantized_convolution_amd.serve`` runs a small batch through all of them.
 """
 from __future__ import annotations
 
@@ -24,8 +28,9 @@ from typing import List, Optional, Sequence
 
 import torch
 
-from . import (KVCache, attn_cached_workspace, mq_attn_cached, mq_attn_prompt, mq_kv_append,
-               mq_kv_evict)
+from . import (MX4, KVCache, attn_cached_workspace, mq_attn_cached, mq_attn_prompt, mq_kv_append,
+               mq_kv_evict, mq_mx4_gated, mq_mx4_linear, mq_mx4_quantize, mx4_gated_workspace,
+               mx4_linear_workspace)
 
 
 class CachedAttention:
@@ -174,6 +179,36 @@ class CachedAttention:
             self.pages[s], self.held[s] = fresh[i * need:(i + 1) * need], keep
 
 
+class FeedForward:
+    """The block down(silu(gate x) * (up x)) for up to max_tokens rows at a time. gate and up are
+    [hidden][width], down [width][hidden]; they are quantized once and not kept."""
+
+    def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, max_tokens: int):
+        self.hidden, self.width = gate.shape
+        if up.shape != gate.shape or down.shape != (self.width, self.hidden):
+            raise ValueError(f"gate {tuple(gate.shape)}, up {tuple(up.shape)}, down {tuple(down.shape)}: expected "
+                             f"[hidden][width] twice and [width][hidden]")
+        if max_tokens < 1:
+            raise ValueError(f"max_tokens {max_tokens}: expected 1 or more")
+        self.max_tokens = max_tokens
+        self.gate, self.up, self.down = (MX4.empty(*w.shape, w.device) for w in (gate, up, down))
+        for w, q in ((gate, self.gate), (up, self.up), (down, self.down)):
+            mq_mx4_quantize(w, q)
+        gated = mx4_gated_workspace(max_tokens, self.hidden, self.width, gate.device)
+        linear = mx4_linear_workspace(max_tokens, self.width, self.hidden, gate.device)
+        self.ws = gated if gated.numel() >= linear.numel() else linear  # one call after the other
+
+    def __call__(self, x: torch.Tensor) -> torch.Tensor:
+        """x [tokens][width] (rows of any stride) -> [tokens][width] of its type."""
+        if x.dim() != 2 or x.shape[1] != self.width or x.shape[0] > self.max_tokens:
+            raise ValueError(f"x {tuple(x.shape)}: expected up to {self.max_tokens} rows of {self.width}")
+        h = torch.empty((x.shape[0], self.hidden), dtype=x.dtype, device=x.device)
+        y = torch.empty((x.shape[0], self.width), dtype=x.dtype, device=x.device)
+        mq_mx4_gated(x, self.gate, self.up, h, self.ws)
+        mq_mx4_linear(h, self.down, y, self.ws)
+        return y
+
+
 def main():
     n, q_heads, kv_heads, dim, lengths = 3, 8, 2, 64, [200, 37, 90]
     layer = CachedAttention(n, 512, q_heads, kv_heads, dim, page_size=32)
@@ -187,6 +222,10 @@ def main():
     layer.evict(64, 16)
     out = layer.decode(new(n, q_heads), new(n, kv_heads), new(n, kv_heads))
     print("evict  ", tuple(out.shape), "tokens held", layer.held, "pages free", len(layer.free))
+    width, hidden = q_heads * dim, 4 * q_heads * dim
+    new_weight = lambda rows, cols: torch.randn(rows, cols, device="cuda") * cols ** -0.5
+    feed = FeedForward(new_weight(hidden, width), new_weight(hidden, width), new_weight(width, hidden), total)
+    print("feed   ", tuple(feed(out.view(n, width)).shape), "4-bit weights", 3 * width * hidden * 17 // 32, "bytes")
 
 
 if __name__ == "__main__":
