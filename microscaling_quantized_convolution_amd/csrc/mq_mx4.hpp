@@ -50,7 +50,6 @@ struct Mx4MatmulArgs {
     int jobs, m, n;
     int pieces[2];
     bool gated;
-    bool vec;       // set by the launch: rows of the outputs are 16-byte aligned
     MatView x;      // null, or a[0][0] still dense (mx4_quantizes_rows): m rows of `cols`
     int cols;
     void *ws;

@@ -174,23 +174,4 @@ __device__ __forceinline__ void put(const MatView &y, int64_t r, int c, float v)
     static_cast<typename Dense<DT>::T *>(y.p)[r * y.stride + c] = Dense<DT>::store(v);
 }
 
-// Columns c .. c + 3 (c a multiple of 4) of row r. vec: rows are 16-byte aligned.
-template <int DT>
-__device__ __forceinline__ void put4(const MatView &y, bool vec, int64_t r, int c, int cols, f32x4_t v)
-{
-    typedef typename Dense<DT>::T T;
-    T *to = static_cast<T *>(y.p) + r * y.stride + c;
-    T e[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) e[k] = Dense<DT>::store(v[k]);
-    if (vec && c + 4 <= cols) {
-        if constexpr (sizeof(T) == 4) *(u32x4_t *)to = *(const u32x4_t *)e;
-        else *(uint64_t *)to = *(const uint64_t *)e;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (c + k < cols) to[k] = e[k];
-    }
-}
-
 } // namespace mq

@@ -34,6 +34,7 @@ __device__ __forceinline__ void load_word_to_lds(const void *base, uint32_t off,
 template <int LEFT>
 __device__ __forceinline__ void lds_barrier()
 {
+    static_assert(LEFT < 64, "the counter's range");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\t"
                  "s_barrier" ::"n"(LEFT)
                  : "memory");
@@ -50,45 +51,55 @@ __device__ __forceinline__ u32x4_t read_lds(uint32_t at)
     return *(lp)(uintptr_t)at;
 }
 
-// The lane's 16 accumulators of a 32 x 32 tile, row r, columns 8 (k / 4) + 4 h + k % 4 from c on:
-// lanes h = 0 and 1 of a row exchange fours, so that each holds two runs of 8 columns.
 __device__ __forceinline__ uint32_t read_lds_word(uint32_t at)
 {
     typedef const __attribute__((address_space(3))) uint32_t *lp;
     return *(lp)(uintptr_t)at;
 }
 
-template <int DT>
-__device__ __forceinline__ void put_tile(const MatView &y, bool vec, int r, int c, int rows, int cols, int h, f32x16_t v)
-{
+// A wave's 32 rows of NT 32 x 32 tiles beside each other, through its own part of LDS: accumulator k of
+// lane (n, h) is row n, column 8 (k / 4) + 4 h + k % 4 of its tile, and memory is written in whole rows
+// of the strip, 16 bytes to a lane (at any alignment). 16 bytes between the rows keep them in
+// different banks.
+template <int DT, int NT> struct Strip {
     typedef typename Dense<DT>::T T;
-    float o[16];
+    static constexpr int E = 16 / (int)sizeof(T), ACROSS = NT * 32 / E, stride = ACROSS * 16 + 16, bytes = 32 * stride;
+    static __device__ __forceinline__ void put(const MatView &y, uint32_t region, int lane, int r0, int c0, int rows, int cols, const f32x16_t *v)
+    {
+        const uint32_t to = region + (lane & 31) * stride + (lane >> 5) * 4 * sizeof(T);
 #pragma unroll
-    for (int g = 0; g < 4; g += 2)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[4 * g + k]), __float_as_uint(v[4 * g + 4 + k]), false, false);
-            o[4 * g + k] = __uint_as_float(s[0]);
-            o[4 * g + 4 + k] = __uint_as_float(s[1]);
+            for (int g = 0; g < 4; ++g) {
+                T e[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) e[k] = Dense<DT>::store(v[j][4 * g + k]);
+                const uint32_t at = to + (j * 32 + 8 * g) * sizeof(T);
+                if constexpr (sizeof(T) == 4) *(__attribute__((address_space(3))) u32x4_t *)(uintptr_t)at = *(const u32x4_t *)e;
+                else *(__attribute__((address_space(3))) uint64_t *)(uintptr_t)at = *(const uint64_t *)e;
+            }
+        __builtin_amdgcn_wave_barrier(); // (a wave's accesses to LDS are made in their order)
+        const int chunk = lane % ACROSS, c = c0 + chunk * E;
+#pragma unroll
+        for (int i = 0; i < ACROSS / 2; ++i) { // 64 / ACROSS rows at a time
+            const int row = i * (64 / ACROSS) + lane / ACROSS, r = r0 + row;
+            const u32x4_t x = read_lds(region + row * stride + chunk * 16);
+            if (r >= rows) continue;
+            T *out = static_cast<T *>(y.p) + r * y.stride + c;
+            if (c + E <= cols) {
+                *(Sixteen *)out = __builtin_bit_cast(Sixteen, x);
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (c + k < cols) out[k] = ((const T *)&x)[k];
+            }
         }
-    if (r >= rows) return;
-    T *row = static_cast<T *>(y.p) + r * y.stride;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        const int at = c + 16 * g + 8 * h;
-        T e[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = Dense<DT>::store(o[8 * g + k]);
-        if (vec && at + 8 <= cols) {
-#pragma unroll
-            for (int k = 0; k < (int)sizeof(T) / 2; ++k) *((u32x4_t *)(row + at) + k) = ((const u32x4_t *)e)[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (at + k < cols) row[at + k] = e[k];
-        }
+        __builtin_amdgcn_wave_barrier();
     }
-}
+    struct Sixteen {
+        uint16_t w[8];
+    } __attribute__((packed, aligned(sizeof(T))));
+};
 
 // f(0), ..., f(N - 1), each with its number as a type
 template <int N, class F, int... I>
@@ -103,9 +114,11 @@ __global__ void __launch_bounds__(WM * WN * 64, WM * WN == 4 && (WM * TM + WN * 
     constexpr int W = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
     constexpr int LA = BM / 8 / W, LB = BN / 8 / W; // 1 KB pieces of a stage to each wave
     constexpr int ON = GATED ? BN / 2 : BN;         // output columns of a tile
+    constexpr int HALF = TN > 1 ? TN / 2 : 1;       // gated: a wave's gates, whose other factors follow
     constexpr int LZ = (BM + BN + W * 32 - 1) / (W * 32), ZR = LZ * W * 32; // 32 rows' scales to a load; the
                                                                             // last wave's may be no one's
-    __shared__ __align__(256) uint8_t as[STAGES][BM * 128], bs[STAGES][BN * 128], zs[STAGES][ZR * 8];
+    constexpr int A = 0, B = STAGES * BM * 128, Z = B + STAGES * BN * 128, LDS = Z + STAGES * ZR * 8;
+    __shared__ __align__(256) uint8_t lds[LDS];
     static_assert(BM % (W * 8) == 0 && BN % (W * 8) == 0, "the waves' shares are whole");
     static_assert(LA % 2 == 0 && LB % 2 == 0, "");
     static_assert(BM / 32 % LZ == 0 && ON / 32 % LZ == 0, "a wave's scales are of one operand");
@@ -128,17 +141,17 @@ __global__ void __launch_bounds__(WM * WN * 64, WM * WN == 4 && (WM * TM + WN * 
     // so that 16 rows' blocks of one number lie in different banks; the last row again past it.
     const uint32_t block = ((lane & 7) ^ (lane >> 4)) * 16;
     const int b_part = GATED ? wave / (W / 2) : 0, b_wave = GATED ? wave % (W / 2) : wave;
-    uint32_t from_a = (wave * LA * 8 + (lane >> 3)) * 128 + block, lim_a = (a.m - 1 - m0) * 128 + block;
-    uint32_t from_b = (b_wave * LB * 8 + (lane >> 3)) * 128 + block, lim_b = (a.n - 1 - n0) * 128 + block;
-    const uint32_t lds_a = lds_address(&as[0][0]), lds_b = lds_address(&bs[0][0]), lds_z = lds_address(&zs[0][0]);
+    uint32_t from_a = (wave * LA * 8 + (lane >> 3)) * 128 + block, lim_a = (min(a.m - m0, BM) - 1) * 128 + block;
+    uint32_t from_b = (b_wave * LB * 8 + (lane >> 3)) * 128 + block, lim_b = (min(a.n - n0, ON) - 1) * 128 + block;
+    const uint32_t lds_a = lds_address(lds) + A, lds_b = lds_address(lds) + B, lds_z = lds_address(lds) + Z;
     // rows of the lane's operands, whose scales it takes four blocks to a word
     const auto b_row = [&](int j) {
-        return GATED ? (j / (TN / 2)) * ON + (wn * (TN / 2) + j % (TN / 2)) * 32 : (wn * TN + j) * 32;
+        return GATED ? (j / HALF) * ON + (wn * HALF + j % HALF) * 32 : (wn * TN + j) * 32;
     };
     // the wave's share of the scales: 32 rows to a load, 4 blocks to a lane; the first waves take a's
     const int z_row = wave * LZ * 32, z_part = z_row < BM ? 0 : (GATED && z_row >= BM + ON ? 2 : 1);
     const int z_first = z_part == 0 ? z_row : z_row - BM - (z_part == 2 ? ON : 0);
-    uint32_t from_z = z_first * 8 + lane * 4, lim_z = ((z_part == 0 ? a.m - m0 : a.n - n0) - 1) * 8 + (lane & 1) * 4;
+    uint32_t from_z = z_first * 8 + lane * 4, lim_z = (min(z_part == 0 ? a.m - m0 : a.n - n0, z_part == 0 ? BM : ON) - 1) * 8 + (lane & 1) * 4;
 
     // the piece that is loaded next
     const int total = GATED ? a.pieces[0] : a.pieces[0] + a.pieces[1];
@@ -182,13 +195,12 @@ __global__ void __launch_bounds__(WM * WN * 64, WM * WN == 4 && (WM * TM + WN * 
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
     if (total > 0) {
         open(!GATED && a.pieces[0] == 0);
-        unroll<STAGES - 1>([&](auto) {
+        unroll<STAGES>([&](auto) {
             unroll<LOADS>(stage);
             advance();
         });
     }
-    for (int p = 0; p < total; ++p) {
-        lds_barrier<(STAGES - 2) * LOADS>(); // piece p is there, piece p - 1 is no longer read
+    const auto multiply = [&](int p, auto more) {
         const int at = p % STAGES;
         const uint32_t at_a = lds_a + at * BM * 128 + (wm * TM * 32 + n) * 128;
         const uint32_t at_b = lds_b + at * BN * 128 + n * 128;
@@ -217,7 +229,9 @@ __global__ void __launch_bounds__(WM * WN * 64, WM * WN == 4 && (WM * TM + WN * 
                 constexpr int i = decltype(tc)::value;
                 unroll<LOADS>([&](auto lc) {
                     constexpr int l = decltype(lc)::value;
-                    if constexpr (l * 1 * TM / LOADS == S * TM + i) stage(lc);
+                    // early, all in the first step: a barrier soon waits for them (spread over two steps 535 us
+                    // in place of 524 at 8192 x 8192 x 16384, over four 559)
+                    if constexpr (decltype(more)::value && l * TM / LOADS == S * TM + i) stage(lc);
                 });
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
@@ -226,28 +240,38 @@ __global__ void __launch_bounds__(WM * WN * 64, WM * WN == 4 && (WM * TM + WN * 
                 }
             });
         });
-        advance();
+        if constexpr (decltype(more)::value) advance();
+    };
+    // before each piece: it is there for all waves, and the piece before it is no longer read
+    if (total > 0) {
+        lds_barrier<(STAGES - 1) * LOADS>();
+        multiply(0, std::false_type{});
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); // no load into LDS outlives the workgroup
-    // accumulator k of lane (n, h): row n of the tile, column 8 (k / 4) + 4 h + k % 4
+    for (int p = 1; p < total; ++p) {
+        lds_barrier<(STAGES - 2) * LOADS>();
+        multiply(p, std::true_type{});
+    }
+    lds_barrier<0>(); // no load into LDS is left, and all of it is free
+    constexpr int NT = GATED ? HALF : TN;
+    static_assert(W * Strip<DT, NT>::bytes <= LDS, "a strip of 32 rows to each wave");
+    const uint32_t region = lds_address(lds) + wave * Strip<DT, NT>::bytes;
+    const int c = n0 + (GATED ? wn * HALF : wn * TN) * 32;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const int r = m0 + (wm * TM + i) * 32 + n;
+        const int r = m0 + (wm * TM + i) * 32;
+        if constexpr (GATED) {
+            f32x16_t out[NT];
 #pragma unroll
-        for (int j = 0; j < (GATED ? TN / 2 : TN); ++j) {
-            const int c = n0 + (GATED ? (wn * (TN / 2) + j) * 32 : b_row(j));
-            if constexpr (GATED) {
-                f32x16_t out;
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int k = 0; k < 16; ++k) out[k] = silu(acc[i][j][k]) * acc[i][j + TN / 2][k];
-                put_tile<DT>(a.y[0], a.vec, r, c, a.m, a.n, h, out);
-                if (a.g.p) {
-                    put_tile<DT>(a.g, a.vec, r, c, a.m, a.n, h, acc[i][j]);
-                    put_tile<DT>(a.u, a.vec, r, c, a.m, a.n, h, acc[i][j + TN / 2]);
-                }
-            } else {
-                put_tile<DT>(a.y[job], a.vec, r, c, a.m, a.n, h, acc[i][j]);
+                for (int k = 0; k < 16; ++k) out[j][k] = silu(acc[i][j][k]) * acc[i][j + HALF][k];
+            Strip<DT, NT>::put(a.y[0], region, lane, r, c, a.m, a.n, out);
+            if (a.g.p) {
+                Strip<DT, NT>::put(a.g, region, lane, r, c, a.m, a.n, acc[i]);
+                Strip<DT, NT>::put(a.u, region, lane, r, c, a.m, a.n, acc[i] + HALF);
             }
+        } else {
+            Strip<DT, NT>::put(a.y[job], region, lane, r, c, a.m, a.n, acc[i]);
         }
     }
 }
@@ -258,7 +282,7 @@ hipError_t matmul_tiles(const Mx4MatmulArgs &a, hipStream_t st)
     constexpr int BM = WM * TM * 32, BN = WN * TN * 32 / (GATED ? 2 : 1);
     const int tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + BN - 1) / BN;
     const int64_t grid = (int64_t)tiles_m * tiles_n;
-    if (grid > INT32_MAX / 8) return hipErrorInvalidValue;
+    if (grid > UINT32_MAX / (WM * WN * 64)) return hipErrorInvalidValue; // a grid's threads are counted in 32 bits
     const dim3 g((uint32_t)grid, a.jobs);
     mx4_matmul_kernel<DT, GATED, WM, WN, TM, TN, STAGES><<<g, WM * WN * 64, 0, st>>>(a, tiles_m, tiles_n);
     return hipGetLastError();
@@ -280,12 +304,6 @@ template <int DT>
 hipError_t matmul(const Mx4MatmulArgs &a, Kind kind, hipStream_t st)
 {
     return a.gated ? matmul<DT, true>(a, kind, st) : matmul<DT, false>(a, kind, st);
-}
-
-bool rows_aligned(const MatView &m)
-{
-    const int64_t size = m.dtype == MQ_F32 ? 4 : 2;
-    return (reinterpret_cast<uintptr_t>(m.p) & 15) == 0 && m.stride * size % 16 == 0;
 }
 
 int64_t tiles_of(const Mx4MatmulArgs &a, int bm, int bn)
@@ -315,11 +333,9 @@ bool mx4_quantizes_rows(int m, int n, int k)
     return rows_kind(m, n) && (int64_t)m * k <= 1 << 14 && (int64_t)m * k * ((n + 15) / 16) <= 1 << 22;
 }
 
-hipError_t launch_mx4_matmul(const Mx4MatmulArgs &given, hipStream_t st)
+hipError_t launch_mx4_matmul(const Mx4MatmulArgs &a, hipStream_t st)
 {
-    if (given.m == 0 || given.n == 0) return hipSuccess;
-    Mx4MatmulArgs a = given;
-    a.vec = rows_aligned(a.y[0]) && rows_aligned(a.y[1]) && rows_aligned(a.g) && rows_aligned(a.u);
+    if (a.m == 0 || a.n == 0) return hipSuccess;
     const Kind kind = kind_of(a);
     if (kind == kRows) return launch_mx4_rows(a, st);
     const int dt = a.y[0].dtype;

@@ -8,6 +8,8 @@
 namespace mq {
 namespace {
 
+constexpr int64_t kMaxGroups = UINT32_MAX / 256; // a grid's threads are counted in 32 bits
+
 // Where row r of piece p lies, in rows of pieces.
 __device__ __forceinline__ int64_t place(const Mx4View &q, int p, int64_t r) { return (int64_t)p * q.rows + r; }
 
@@ -287,7 +289,7 @@ hipError_t rows_alone(const Mx4QuantArgs &a, hipStream_t st)
     const bool four = (int64_t)across * a.rows * width >= 4 * 256 * 512;
     const int per = 256 / width * (four ? 4 : 1);
     const int64_t grid = ((int64_t)a.rows + per - 1) / per * across;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    if (grid > kMaxGroups) return hipErrorInvalidValue;
     const auto run = [&](auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
         if (four) mx4_quantize_rows_kernel<DT, SR, 4, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, width, across);
@@ -304,7 +306,7 @@ hipError_t both(const Mx4QuantArgs &a, hipStream_t st)
     constexpr int down = 8 * NR * stack_of(NR), beside = 4 / stack_of(NR) * 64; // rows and columns of a workgroup
     const int cols = a.row.codes ? a.row.pieces() * 256 : a.cols, across = (cols + beside - 1) / beside;
     const int64_t grid = ((int64_t)a.rows + 255) / 256 * (256 / down) * across; // whole pieces of columns
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    if (grid > kMaxGroups) return hipErrorInvalidValue;
     const auto run = [&](auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
         if constexpr (NR == 32) mx4_quantize_packed_kernel<DT, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, across);
@@ -345,7 +347,7 @@ hipError_t launch_mx4_dequantize(const Mx4View &q, const MatView &out, hipStream
     if (q.rows == 0 || q.cols == 0) return hipSuccess;
     const int groups = (q.cols + 7) / 8, width = width_of(groups), across = (groups + width - 1) / width;
     const int64_t grid = ((int64_t)q.rows + 256 / width - 1) / (256 / width) * across;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    if (grid > kMaxGroups) return hipErrorInvalidValue;
     const int64_t size = out.dtype == MQ_F32 ? 4 : 2;
     const bool vec = (reinterpret_cast<uintptr_t>(out.p) & 15) == 0 && out.stride * size % 16 == 0;
     if (out.dtype == MQ_BF16) mx4_dequantize_kernel<MQ_BF16><<<(uint32_t)grid, 256, 0, st>>>(q, out, vec, width, across);
