@@ -523,7 +523,9 @@ mq_status mq_kv_evict(const mq_kv_cache *cache, float *weights_dev, const int32_
  * along, and read once for both.
  *
  * Every product is exact and summed in fp32 (in an order that the sizes alone fix: results repeat
- * bit for bit); a sum below 2^-126 in magnitude may become 0.
+ * bit for bit); a sum below 2^-126 in magnitude may become 0. Outputs and workspaces must not
+ * overlap inputs or each other, and calls that can run at the same time must not share a workspace;
+ * a workspace holds nothing from one call to the next.
  */
 
 /* mq_matrix.dtype: an mq_dtype, or fp32. */

@@ -50,6 +50,7 @@ struct Mx4MatmulArgs {
     int jobs, m, n;
     int pieces[2];
     bool gated;
+    bool through;   // set by the launch: outputs are written past the caches
     MatView x;      // null, or a[0][0] still dense (mx4_quantizes_rows): m rows of `cols`
     int cols;
     void *ws;

@@ -78,11 +78,23 @@ __device__ __forceinline__ Reach reach_of(int c, int cols)
     const int start = max(min(c, cols - 8), 0);
     return {start, c - start};
 }
-template <bool TAIL, class T>
+// PASS: past the caches, for what is read once and would fill them.
+template <bool TAIL, bool PASS = false, class T>
 __device__ __forceinline__ Eight<T> load8(const T *row, Reach at, int cols)
 {
-    if (!TAIL || cols >= 8) return *(const Eight<T> *)(row + at.start);
     Eight<T> x;
+    if (!TAIL || cols >= 8) {
+        if constexpr (PASS) {
+            typedef u32x4_t Any __attribute__((aligned(2)));
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                const u32x4_t w = __builtin_nontemporal_load((const Any *)(row + at.start) + i);
+                __builtin_memcpy((char *)&x + 16 * i, &w, 16);
+            }
+            return x;
+        }
+        return *(const Eight<T> *)(row + at.start);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) x.e[i] = i < cols ? row[i] : (T)0;
     return x;
@@ -166,6 +178,15 @@ __device__ __forceinline__ uint32_t encode8(const float *v, uint32_t e, uint64_t
         }
     }
     return e == 255 ? 0u : c;
+}
+
+// 16 bytes to any address, past the caches. (Written out: beside a plain store of the same, the compiler
+// makes one plain store of the two. The wait keeps the data's registers until they are read.)
+__device__ __forceinline__ void store_past(void *to, u32x4_t x)
+{
+    asm volatile("global_store_dwordx4 %0, %1, off nt\n\t"
+                 "s_nop 1" ::"v"(to), "v"(x)
+                 : "memory");
 }
 
 template <int DT>

@@ -64,7 +64,7 @@ __device__ __forceinline__ uint32_t read_lds_word(uint32_t at)
 template <int DT, int NT> struct Strip {
     typedef typename Dense<DT>::T T;
     static constexpr int E = 16 / (int)sizeof(T), ACROSS = NT * 32 / E, stride = ACROSS * 16 + 16, bytes = 32 * stride;
-    static __device__ __forceinline__ void put(const MatView &y, uint32_t region, int lane, int r0, int c0, int rows, int cols, const f32x16_t *v)
+    static __device__ __forceinline__ void put(const MatView &y, uint32_t region, int lane, int r0, int c0, int rows, int cols, bool through, const f32x16_t *v)
     {
         const uint32_t to = region + (lane & 31) * stride + (lane >> 5) * 4 * sizeof(T);
 #pragma unroll
@@ -87,7 +87,8 @@ template <int DT, int NT> struct Strip {
             if (r >= rows) continue;
             T *out = static_cast<T *>(y.p) + r * y.stride + c;
             if (c + E <= cols) {
-                *(Sixteen *)out = __builtin_bit_cast(Sixteen, x);
+                if (through) store_past(out, x);
+                else *(Sixteen *)out = x;
             } else {
 #pragma unroll
                 for (int k = 0; k < E; ++k)
@@ -96,9 +97,7 @@ template <int DT, int NT> struct Strip {
         }
         __builtin_amdgcn_wave_barrier();
     }
-    struct Sixteen {
-        uint16_t w[8];
-    } __attribute__((packed, aligned(sizeof(T))));
+    typedef u32x4_t Sixteen __attribute__((aligned(2)));
 };
 
 // f(0), ..., f(N - 1), each with its number as a type
@@ -265,13 +264,13 @@ __global__ void __launch_bounds__(WM * WN * 64, WM * WN == 4 && (WM * TM + WN * 
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int k = 0; k < 16; ++k) out[j][k] = silu(acc[i][j][k]) * acc[i][j + HALF][k];
-            Strip<DT, NT>::put(a.y[0], region, lane, r, c, a.m, a.n, out);
+            Strip<DT, NT>::put(a.y[0], region, lane, r, c, a.m, a.n, a.through, out);
             if (a.g.p) {
-                Strip<DT, NT>::put(a.g, region, lane, r, c, a.m, a.n, acc[i]);
-                Strip<DT, NT>::put(a.u, region, lane, r, c, a.m, a.n, acc[i] + HALF);
+                Strip<DT, NT>::put(a.g, region, lane, r, c, a.m, a.n, a.through, acc[i]);
+                Strip<DT, NT>::put(a.u, region, lane, r, c, a.m, a.n, a.through, acc[i] + HALF);
             }
         } else {
-            Strip<DT, NT>::put(a.y[job], region, lane, r, c, a.m, a.n, acc[i]);
+            Strip<DT, NT>::put(a.y[job], region, lane, r, c, a.m, a.n, a.through, acc[i]);
         }
     }
 }
@@ -333,11 +332,17 @@ bool mx4_quantizes_rows(int m, int n, int k)
     return rows_kind(m, n) && (int64_t)m * k <= 1 << 14 && (int64_t)m * k * ((n + 15) / 16) <= 1 << 22;
 }
 
-hipError_t launch_mx4_matmul(const Mx4MatmulArgs &a, hipStream_t st)
+hipError_t launch_mx4_matmul(const Mx4MatmulArgs &given, hipStream_t st)
 {
-    if (a.m == 0 || a.n == 0) return hipSuccess;
+    if (given.m == 0 || given.n == 0) return hipSuccess;
+    Mx4MatmulArgs a = given;
     const Kind kind = kind_of(a);
     if (kind == kRows) return launch_mx4_rows(a, st);
+    // Outputs that would fill the caches, and those of many rounds of tiles, are written past them: other
+    // tiles' loads then pass the stores (8192 x 8192 x 4096 to bf16 155 -> 136 us, gated 4096 x 8192 x 4096
+    // 151 -> 132, with G and U 174 -> 154; but 8192 x 4096 x 4096, two rounds of 67 MB, 69 -> 72.5).
+    const int64_t bytes = (int64_t)a.m * a.n * (a.y[0].dtype == MQ_F32 ? 4 : 2) * (a.jobs + (a.g.p ? 2 : 0));
+    a.through = bytes >= 80 << 20 || (kind == kTile256 && tiles_of(a, 256, a.gated ? 128 : 256) >= 768);
     const int dt = a.y[0].dtype;
     return dt == MQ_BF16 ? matmul<MQ_BF16>(a, kind, st) : (dt == MQ_F16 ? matmul<MQ_F16>(a, kind, st) : matmul<MQ_F32>(a, kind, st));
 }

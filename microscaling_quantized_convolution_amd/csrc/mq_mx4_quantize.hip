@@ -52,13 +52,13 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Mx4QuantArgs a, 
 constexpr int stack_of(int nr) { return nr >= 8 ? 32 / nr : 4; } // waves one above another
 
 // Eight values to quantize: of x, or of dg and du of h = silu(g) u.
-template <int DT, bool GRAD, bool TAIL> struct Source {
+template <int DT, bool GRAD, bool TAIL, bool PASS> struct Source {
     static constexpr int K = GRAD ? 2 : 1;
     static __device__ __forceinline__ void load(const Mx4QuantArgs &a, int64_t r, Reach at, float (*v)[8])
     {
         typedef typename Dense<DT>::T T;
         const auto get = [&](const MatView &m, float *to) {
-            values8<DT, TAIL>(load8<TAIL>(static_cast<const T *>(m.p) + r * m.stride, at, a.cols), at, to);
+            values8<DT, TAIL>(load8<TAIL, PASS>(static_cast<const T *>(m.p) + r * m.stride, at, a.cols), at, to);
         };
         get(a.x, v[0]);
         if constexpr (GRAD) {
@@ -90,7 +90,7 @@ __device__ __forceinline__ uint32_t max_lane_xor_32(uint32_t v)
 template <int DT, bool GRAD, int NR, bool SR, bool TAIL>
 __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs a, int across)
 {
-    constexpr int K = Source<DT, GRAD, TAIL>::K, WR = 8 * NR, STACK = stack_of(NR); // rows of a wave
+    constexpr int K = Source<DT, GRAD, TAIL, NR >= 16>::K, WR = 8 * NR, STACK = stack_of(NR); // rows of a wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 3, cg = lane & 7;
     // a workgroup's waves: STACK of them one above another, the others beside
     const int down = blockIdx.x / across;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         float t[K][8];
-        Source<DT, GRAD, TAIL>::load(a, min(r0 + r, a.rows - 1), reach, t);
+        Source<DT, GRAD, TAIL, NR >= 16>::load(a, min(r0 + r, a.rows - 1), reach, t);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_packed_kernel(Mx4QuantArg
     const Reach reach = reach_of(c, a.cols);
     Eight<uint16_t> raw[32];
 #pragma unroll
-    for (int r = 0; r < 32; ++r) raw[r] = load8<TAIL>(x + (int64_t)min(r, a.rows - 1 - r0) * a.x.stride, reach, a.cols);
+    for (int r = 0; r < 32; ++r) raw[r] = load8<TAIL, true>(x + (int64_t)min(r, a.rows - 1 - r0) * a.x.stride, reach, a.cols);
     u32x4_t d[32];
 #pragma unroll
     for (int r = 0; r < 32; ++r) {
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_packed_kernel(Mx4QuantArg
 
 // 8 columns to a thread.
 template <int DT>
-__global__ void __launch_bounds__(256) mx4_dequantize_kernel(Mx4View q, MatView out, bool vec, int width, int across)
+__global__ void __launch_bounds__(256) mx4_dequantize_kernel(Mx4View q, MatView out, bool through, int width, int across)
 {
     typedef typename Dense<DT>::T T;
     const int g = (int)(blockIdx.x % across) * width + (int)(threadIdx.x % width);
@@ -263,9 +263,14 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(Mx4View q, MatView 
         v[j] = Dense<DT>::store(e == 255 ? __uint_as_float(0x7FC00000u) : x);
     }
     T *to = static_cast<T *>(out.p) + r * out.stride + g * 8;
-    if (vec && g * 8 + 8 <= q.cols) {
+    if (g * 8 + 8 <= q.cols) {
 #pragma unroll
-        for (int j = 0; j < (int)sizeof(T) / 2; ++j) ((u32x4_t *)to)[j] = ((const u32x4_t *)v)[j];
+        for (int j = 0; j < (int)sizeof(T) / 2; ++j) {
+            typedef u32x4_t Any __attribute__((aligned(2)));
+            const u32x4_t w = ((const u32x4_t *)v)[j];
+            if (through) store_past((u32x4_t *)to + j, w);
+            else *(Any *)((u32x4_t *)to + j) = w;
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -348,11 +353,11 @@ hipError_t launch_mx4_dequantize(const Mx4View &q, const MatView &out, hipStream
     const int groups = (q.cols + 7) / 8, width = width_of(groups), across = (groups + width - 1) / width;
     const int64_t grid = ((int64_t)q.rows + 256 / width - 1) / (256 / width) * across;
     if (grid > kMaxGroups) return hipErrorInvalidValue;
-    const int64_t size = out.dtype == MQ_F32 ? 4 : 2;
-    const bool vec = (reinterpret_cast<uintptr_t>(out.p) & 15) == 0 && out.stride * size % 16 == 0;
-    if (out.dtype == MQ_BF16) mx4_dequantize_kernel<MQ_BF16><<<(uint32_t)grid, 256, 0, st>>>(q, out, vec, width, across);
-    else if (out.dtype == MQ_F16) mx4_dequantize_kernel<MQ_F16><<<(uint32_t)grid, 256, 0, st>>>(q, out, vec, width, across);
-    else mx4_dequantize_kernel<MQ_F32><<<(uint32_t)grid, 256, 0, st>>>(q, out, vec, width, across);
+    // what would fill the caches is written past them (8192 x 4096 to bf16 18.0 -> 16.4 us)
+    const bool through = (int64_t)q.rows * q.cols * (out.dtype == MQ_F32 ? 4 : 2) >= 64 << 20;
+    if (out.dtype == MQ_BF16) mx4_dequantize_kernel<MQ_BF16><<<(uint32_t)grid, 256, 0, st>>>(q, out, through, width, across);
+    else if (out.dtype == MQ_F16) mx4_dequantize_kernel<MQ_F16><<<(uint32_t)grid, 256, 0, st>>>(q, out, through, width, across);
+    else mx4_dequantize_kernel<MQ_F32><<<(uint32_t)grid, 256, 0, st>>>(q, out, through, width, across);
     return hipGetLastError();
 }
 

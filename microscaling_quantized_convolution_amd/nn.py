@@ -306,7 +306,7 @@ class _MXModule(nn.Module):
         self.cache_weight = cache_weight
         self.step = 0
         self._held: Optional[List[MX4]] = None
-        self._held_key: Optional[tuple] = None
+        self._held_of: list = []
 
     def _next_seed(self) -> int:
         seed = self.seed_base + self.layer_index + self.layers * self.step
@@ -317,11 +317,13 @@ class _MXModule(nn.Module):
     def _cached(self, *weights: torch.Tensor) -> Optional[List[MX4]]:
         if self.training or not self.cache_weight:
             return None
-        key = tuple((w.data_ptr(), w._version) for w in weights)
-        if self._held is None or self._held_key != key:
+        # the parameters themselves, not their addresses: another tensor may come to lie at one
+        now = [(w, w._version, w.data_ptr(), w.dtype) for w in weights]
+        if len(now) != len(self._held_of) or any(a[0] is not b[0] or a[1:] != b[1:]
+                                                 for a, b in zip(now, self._held_of)):
             with torch.cuda.device(weights[0].device):
                 self._held = [quantize_linear_weight(w.detach().contiguous(), False)[0] for w in weights]
-            self._held_key = key
+            self._held_of = now
         return self._held
 
 

@@ -181,7 +181,8 @@ class CachedAttention:
 
 class FeedForward:
     """The block down(silu(gate x) * (up x)) for up to max_tokens rows at a time. gate and up are
-    [hidden][width], down [width][hidden]; they are quantized once and not kept."""
+    [hidden][width], down [width][hidden]; they are quantized once and not kept. Calls share a
+    workspace: one at a time."""
 
     def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, max_tokens: int):
         self.hidden, self.width = gate.shape

@@ -108,6 +108,15 @@ def test_cached_weights():
         block.gate.mul_(2.0)
         z = block(x)
     assert block._held is not held and not torch.equal(z, y)
+    held = block._held
+    with torch.no_grad():  # another parameter in the place of one, and the same one in other types
+        block.up = torch.nn.Parameter(block.up.detach() * 3.0)
+        assert not torch.equal(block(x), z) and block._held is not held
+        held = block._held
+        block.half()
+        block(x)
+        assert block._held is not held
+        block.float()
     # a gradient with respect to the input still goes through held weights
     xr = x.clone().requires_grad_()
     block.requires_grad_(False)

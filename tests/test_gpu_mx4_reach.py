@@ -57,6 +57,16 @@ def test_quantize_many_tiles(rows, cols, dtype, sr):
         same(row, *ref.quantize(f64(x), sr, 0))
 
 
+@pytest.mark.parametrize("rows,cols,dtype", [(3000, 6001, F32), (5000, 6912, BF16), (16, 40, F16)])
+def test_dequantize_large(rows, cols, dtype):
+    q = random_held(rows, rows, cols)
+    out = torch.full((rows + 1, cols + 3), 7.0, dtype=dtype, device="cuda")
+    mq.mq_mx4_dequantize(q, out[:rows, 1:cols + 1])
+    at = some(rows)
+    assert torch.equal(out[at, 1:cols + 1].cpu(), torch.from_numpy(values_of(q, at)).to(dtype))
+    assert (out[rows] == 7.0).all() and (out[:, 0] == 7.0).all() and (out[:, cols + 1:] == 7.0).all()
+
+
 def random_held(seed, rows, cols):
     """A quantized matrix on the GPU of random codes, scales of [126, 128], and some of its rows' values."""
     g = torch.Generator(device="cuda").manual_seed(seed)
