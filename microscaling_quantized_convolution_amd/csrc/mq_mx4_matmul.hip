@@ -320,7 +320,12 @@ Kind kind_of(const Mx4MatmulArgs &a)
     if (rows_kind(a.m, (int64_t)a.n * a.jobs)) return kRows;
     if (tiles_of(a, 64, 64) <= (g ? 256 : 512)) return kTile64;
     if (tiles_of(a, 128, g ? 64 : 128) <= 256) return kTile128Deep;
-    return tiles_of(a, 256, g ? 128 : 256) >= 512 && a.pieces[0] + a.pieces[1] >= 8 ? kTile256 : kTile128;
+    // 256 x 256 one to a CU, or 128 x 128 two to a CU: rounds of the chip, each of so much for a piece
+    // and for a tile's beginning and end (in ns, measured at 2 to 64 pieces)
+    const int64_t pieces = a.pieces[0] + a.pieces[1];
+    const int64_t t256 = (tiles_of(a, 256, g ? 128 : 256) + 255) / 256 * (1810 * pieces + 8000);
+    const int64_t t128 = (tiles_of(a, 128, g ? 64 : 128) + 511) / 512 * (1250 * pieces + 3000);
+    return t256 < t128 ? kTile256 : kTile128;
 }
 
 } // namespace

@@ -90,7 +90,7 @@ __device__ __forceinline__ uint32_t max_lane_xor_32(uint32_t v)
 template <int DT, bool GRAD, int NR, bool SR, bool TAIL>
 __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs a, int across)
 {
-    constexpr int K = Source<DT, GRAD, TAIL, NR >= 16>::K, WR = 8 * NR, STACK = stack_of(NR); // rows of a wave
+    constexpr int K = Source<DT, GRAD, TAIL, (NR >= 16)>::K, WR = 8 * NR, STACK = stack_of(NR); // rows of a wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 3, cg = lane & 7;
     // a workgroup's waves: STACK of them one above another, the others beside
     const int down = blockIdx.x / across;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         float t[K][8];
-        Source<DT, GRAD, TAIL, NR >= 16>::load(a, min(r0 + r, a.rows - 1), reach, t);
+        Source<DT, GRAD, TAIL, (NR >= 16)>::load(a, min(r0 + r, a.rows - 1), reach, t);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
