@@ -19,9 +19,8 @@
 //   128 x 128, 2 slots, two workgroups a CU   one's stores under the other's products: 4096 x 4096 x 512 12.7
 //   256 x 256, 2 slots                        8192 x 8192 x 4096 136 (4.0 PFLOP/s), x 16384 505 (4.35; before
 //                                             outputs passed the caches)
-// Bound at 256 x 256, for each piece of 1.81 us: the matrix instructions 0.98 (1.0 PFLOP/s short of
-// the peak's rate), but on random data the clock falls and products with their LDS reads alone take
-// 1.47 (1.12 on zeros); the 68 KB of a piece 0.98 where two pieces are on their way, 1.36 where one is
+// Bound at 256 x 256, for each piece of 1.81 us: the matrix instructions 0.98, but on random
+// data the clock falls, and products with their LDS reads alone take 1.47 (1.12 on zeros); the 68 KB of a piece 0.98 where two pieces are on their way, 1.36 where one is
 // and 0.6 from L2. A third slot has no room beside 64 KB, smaller tiles load more (256 x 128 with three
 // slots: 45 us at 4096 x 4096 x 4096 against 37). Scales by loads of their own to registers cost 0.29;
 // a piece's loads spread over its products arrive too late (524 to 559 us). Persistent workgroups that

@@ -4,9 +4,8 @@
 // byte, and 32 codes of 4 bits. Every kernel reads its input once: where rows and columns are wanted,
 // a wave holds a tile of 64 columns in registers and takes the blocks of both directions from them.
 //
-// Bound by memory: 8192 x 4096 along both directions 22 us from bf16 (103 MB, 4.7 TB/s) and 42 from fp32
-// (170 MB, 4.0), rows alone 14.5 (85 MB, 5.9); gradients of 4096 x 8192 80 us (272 MB, 3.4 TB/s: 40 vector
-// operations to an element, two of them in four cycles' time). Small ones by a wave's own length: 500 x
+// Bound by memory: 8192 x 4096 along both directions 22 us from bf16 (103 MB, 4.7 TB/s) and 40 from fp32
+// (170 MB, 4.2), rows alone 14.5 (85 MB, 5.9); gradients of 4096 x 8192 61 us (272 MB, 4.5 TB/s). Small ones by a wave's own length: 500 x
 // 1000 4.5 us with 4 rows to a lane, 9 with 32. Stochastic rounding (a Philox call to 8 elements and
 // direction) takes 8192 x 4096 bf16 to 51 us.
 #include "mq_mx4_device.hpp"
@@ -51,11 +50,10 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Mx4QuantArgs a, 
 
 // ---- rows and columns -----------------------------------------------------------------------------
 //
-// Lane (q, cg) of a wave holds NR rows of 8 columns: 8 NR rows of 64 columns to a wave, and up to four
-// waves one above another. A row's block lies in a quad of lanes; a column's in one lane (NR = 32), or
-// in 32 / NR of them, 8 lanes apart.
-
-constexpr int stack_of(int nr) { return nr >= 8 ? 32 / nr : 4; } // waves one above another
+// Lane (q, cg) of a wave holds NR rows of 8 columns: 8 NR rows of 64 columns to a wave, and four waves
+// beside each other, so that rows are read in long runs (one above another: gradients of 4096 x 8192
+// 80 us in place of 61, fp32 42.5 in place of 40). A row's block lies in a quad of lanes; a column's in one
+// lane (NR = 32), or in 32 / NR of them, 8 lanes apart.
 
 // Eight values to quantize: of x, or of dg and du of h = silu(g) u.
 template <int DT, bool GRAD, bool TAIL, bool PASS> struct Source {
@@ -73,9 +71,9 @@ template <int DT, bool GRAD, bool TAIL, bool PASS> struct Source {
             get(a.u, u);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float dh = v[0][i], s = sigmoid(g[i]);
-                v[0][i] = dh * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
-                v[1][i] = dh * (g[i] * s);
+                const float dh = v[0][i], s = sigmoid(g[i]), gs = g[i] * s;
+                v[0][i] = dh * u[i] * __builtin_fmaf(gs, 1.0f - s, s); // s (1 + g (1 - s))
+                v[1][i] = dh * gs;
             }
         }
     }
@@ -96,12 +94,10 @@ __device__ __forceinline__ uint32_t max_lane_xor_32(uint32_t v)
 template <int DT, bool GRAD, int NR, bool SR, bool TAIL>
 __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs a, int across)
 {
-    constexpr int K = Source<DT, GRAD, TAIL, (NR >= 16)>::K, WR = 8 * NR, STACK = stack_of(NR); // rows of a wave
+    constexpr int K = Source<DT, GRAD, TAIL, (NR >= 16)>::K, WR = 8 * NR; // rows of a wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 3, cg = lane & 7;
-    // a workgroup's waves: STACK of them one above another, the others beside
-    const int down = blockIdx.x / across;
-    const int c0 = (int)((blockIdx.x % across) * (4 / STACK) + wave / STACK) * 64, c = c0 + cg * 8;
-    const int r0 = (down * STACK + wave % STACK) * WR + q * NR;
+    const int c0 = ((int)(blockIdx.x % across) * 4 + wave) * 64, c = c0 + cg * 8;
+    const int r0 = (int)(blockIdx.x / across) * WR + q * NR;
     if (c0 >= (a.row.codes ? a.row.pieces() * 256 : a.cols)) return;
     const Reach reach = reach_of(c, a.cols);
     float v[K][NR][8];
@@ -119,18 +115,23 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
         const Mx4View &row = k ? a.row2 : a.row, &col = k ? a.col2 : a.col;
         if (row.codes) {
             const int g = c / 8, blocks = (a.cols + 31) / 32;
+            const int64_t at = place(row, g >> 5, r0);
+            uint32_t *to = (uint32_t *)(row.codes + at * 128 + (g & 31) * 4);
+            uint8_t *zs = row.scales + at * 8 + (g & 31) / 4;
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 const uint32_t e = mx4_scale(quad_max(amax8(v[k][r])));
-                if (r0 + r >= a.rows) continue;
                 const uint64_t n = 4 * ((uint64_t)(r0 + r) * blocks) + g;
-                const int64_t at = place(row, g >> 5, r0 + r);
-                *(uint32_t *)(row.codes + at * 128 + (g & 31) * 4) = encode8<SR>(v[k][r], e, n, 2 * k, a.seed_lo, a.seed_hi);
-                if ((g & 3) == 0) row.scales[at * 8 + (g & 31) / 4] = (uint8_t)e;
+                const uint32_t codes = encode8<SR>(v[k][r], e, n, 2 * k, a.seed_lo, a.seed_hi);
+                if (r0 + r >= a.rows) continue;
+                to[r * 32] = codes;
+                if ((g & 3) == 0) zs[r * 8] = (uint8_t)e;
             }
         }
         if (col.codes) {
-            const int blocks = (a.rows + 31) / 32, part = (r0 & 255); // first row within the piece
+            const int blocks = (a.rows + 31) / 32, part = r0 & 255; // first row within the piece
+            const int64_t at = place(col, r0 >> 8, c);
+            uint8_t *const first = col.codes + at * 128 + (part & ~7) / 2, *const zs = col.scales + at * 8 + part / 32;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint32_t amax = 0;
@@ -141,7 +142,6 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
                 if constexpr (NR < 8) amax = max_lane_xor_32(amax);
                 const uint32_t e = mx4_scale(amax);
                 if (c + i >= a.cols) continue;
-                const int64_t at = place(col, r0 >> 8, c + i);
                 constexpr int E = (NR + 7) / 8;
                 uint32_t codes[E];
 #pragma unroll
@@ -152,12 +152,12 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
                     for (int j = 0; j < 8; ++j) t[j] = v[k][(8 * w + j) % NR][i]; // (NR = 4: twice, in either half's place)
                     codes[w] = encode8<SR>(t, e, n, 2 * k + 1, a.seed_lo, a.seed_hi);
                 }
-                uint32_t *to = (uint32_t *)(col.codes + at * 128 + (part & ~7) / 2);
+                uint32_t *to = (uint32_t *)(first + i * 128);
                 if constexpr (NR == 32) *(u32x4_t *)to = *(const u32x4_t *)codes;
                 else if constexpr (NR == 16) *(uint64_t *)to = *(const uint64_t *)codes;
                 else if constexpr (NR == 8) *to = codes[0];
                 else ((uint16_t *)to)[part / 4 % 2] = (uint16_t)(part & 4 ? codes[0] >> 16 : codes[0]);
-                if (NR == 32 || part % 32 == 0) col.scales[at * 8 + part / 32] = (uint8_t)e;
+                if (NR == 32 || part % 32 == 0) zs[i * 8] = (uint8_t)e;
             }
         }
     }
@@ -314,9 +314,8 @@ hipError_t rows_alone(const Mx4QuantArgs &a, hipStream_t st)
 template <int DT, bool GRAD, int NR, bool SR>
 hipError_t both(const Mx4QuantArgs &a, hipStream_t st)
 {
-    constexpr int down = 8 * NR * stack_of(NR), beside = 4 / stack_of(NR) * 64; // rows and columns of a workgroup
-    const int cols = a.row.codes ? a.row.pieces() * 256 : a.cols, across = (cols + beside - 1) / beside;
-    const int64_t grid = ((int64_t)a.rows + 255) / 256 * (256 / down) * across; // whole pieces of columns
+    const int cols = a.row.codes ? a.row.pieces() * 256 : a.cols, across = (cols + 255) / 256;
+    const int64_t grid = ((int64_t)a.rows + 255) / 256 * (32 / NR) * across; // whole pieces of columns
     if (grid > kMaxGroups) return hipErrorInvalidValue;
     const auto run = [&](auto tail) {
         constexpr bool TAIL = decltype(tail)::value;
