@@ -270,3 +270,53 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="sizes"):
         mq.mx4_gated_workspace(-1, 3, 4)
     assert mq.mq_mx4_matmul(w, mq.MX4.empty(5, 64), z(32, 5)) is None
+
+
+@pytest.mark.parametrize("m,f,k", [(7, 100, 300), (70, 333, 257), (700, 1300, 520)])
+def test_gated_views(m, f, k):
+    """Inputs and outputs inside larger matrices, rows of any alignment, one weight in both places: the
+    same bits as from matrices of their own, and nothing written around the outputs."""
+    def inside(t, fill=3.0):
+        big = torch.full((t.shape[0] + 3, t.shape[1] + 13), fill, dtype=t.dtype, device="cuda")
+        view = big[2:2 + t.shape[0], 5:5 + t.shape[1]]
+        view.copy_(t)
+        return big, view
+    x, dh = spread(1, m, k, BF16), spread(2, m, f, BF16)
+    w, w_col, x_col = random_held(3, f, k), random_held(4, k, f), mq.MX4.empty(k, m)
+    w.scales -= 4
+    ws = torch.empty(max(mq.mx4_gated_workspace(m, f, k).numel(), mq.mx4_gated_backward_workspace(m, f, k).numel()),
+                     dtype=torch.uint8, device="cuda")
+    new = lambda *s, dtype=BF16: torch.zeros(*s, dtype=dtype, device="cuda")
+    out = {"h": new(m, f), "g": new(m, f), "u": new(m, f), "dx": new(m, k), "dwg": new(f, k, dtype=F32),
+           "dwu": new(f, k, dtype=F32)}
+
+    def run(x, dh, o):
+        mq.mq_mx4_gated(x, w, w, o["h"], ws, o["g"], o["u"], x_col)
+        mq.mq_mx4_gated_backward(dh, o["g"], o["u"], x_col, w_col, w_col, o["dx"], o["dwg"], o["dwu"], ws)
+    run(x, dh, out)
+    assert torch.equal(out["g"], out["u"])
+    views = {name: inside(torch.zeros_like(t)) for name, t in out.items()}
+    run(inside(x, float("nan"))[1], inside(dh, float("nan"))[1], {name: v[1] for name, v in views.items()})
+    for name, (big, view) in views.items():
+        assert torch.equal(view, out[name]), name
+        view.fill_(3.0)
+        assert (big == 3.0).all(), name
+
+
+def test_two_streams_at_once():
+    """Calls side by side on two streams, each with its own workspace: the bits of each alone."""
+    m, f, k = 900, 1500, 700
+    wg, wu = random_held(1, f, k), random_held(2, f, k)
+    xs = [spread(s, m, k, BF16) for s in range(2)]
+    want = []
+    for x in xs:
+        want.append(torch.empty(m, f, dtype=BF16, device="cuda"))
+        mq.mq_mx4_gated(x, wg, wu, want[-1], mq.mx4_gated_workspace(m, f, k))
+    streams, got = [torch.cuda.Stream() for _ in xs], [torch.zeros_like(w) for w in want]
+    spaces = [mq.mx4_gated_workspace(m, f, k) for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, y, ws, st in zip(xs, got, spaces, streams):
+            mq.mq_mx4_gated(x, wg, wu, y, ws, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
