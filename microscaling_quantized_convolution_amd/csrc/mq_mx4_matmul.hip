@@ -337,15 +337,21 @@ int64_t tiles_of(const Mx4MatmulArgs &a, int bm, int bn)
     return (((int64_t)a.m + bm - 1) / bm) * (((int64_t)a.n + bn - 1) / bn) * a.jobs;
 }
 
-// Up to 16 rows, a workgroup takes 16 columns and its waves share the sum; where that makes as many
-// workgroups of 64 columns as CUs, these read the weight in larger pieces.
+// Up to 16 rows, a workgroup takes 16 columns and its waves share the sum; where tiles of 64 columns come
+// near to one a CU, they read the weight in larger pieces (16 x 4096 on 16384: 8.1 us in place of 11.2; on
+// 8192 7.1, where strips of 16 take 6.4).
 bool rows_kind(int m, int64_t n) { return m <= 16 && n < 12288; }
 
 Kind kind_of(const Mx4MatmulArgs &a)
 {
     const bool g = a.gated;
     if (rows_kind(a.m, (int64_t)a.n * a.jobs)) return kRows;
+    // 64 x 64 while the chip holds them all at once: 512 x 4096 x 4096 (512 tiles) 9.8 us, 128 x 128 12.4;
+    // 1024 x 4096 x 4096 17.4 and 13.9. Gated (twice the weight's rows to a tile): 300 x 1024 on 2700 (215)
+    // 9.6 and 11.1, 256 x 4096 on 8192 (512) 17.2 and 15.2.
     if (tiles_of(a, 64, 64) <= (g ? 256 : 512)) return kTile64;
+    // four slots while no CU has two of 128 x 128: 2048 x 2048 x 8192 (256) 23.8 us, with two slots 26.6;
+    // 2048 x 4096 x 4096 (512) 25.8 and 22.8
     if (tiles_of(a, 128, g ? 64 : 128) <= 256) return kTile128Deep;
     // 256 x 256 one to a CU, or 128 x 128 two to a CU: rounds of the chip, each of so much for a piece
     // and for a tile's beginning and end (in ns, measured at 2 to 64 pieces)
