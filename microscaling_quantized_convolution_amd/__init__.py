@@ -580,6 +580,10 @@ class MX4:
         new = lambda width: torch.empty((pieces, rows, width), dtype=torch.uint8, device=device)
         return cls(rows, cols, new(MQ_MX4_PIECE // 2), new(MQ_MX4_PIECE // MQ_MX4_BLOCK))
 
+    def __reduce__(self):
+        # a copy or a pickle is its tensors; the structure's addresses are made anew
+        return MX4, (*self.shape, self.codes, self.scales)
+
     def ref(self, device: int):
         """The structure, for a call on that device."""
         if device != self._dev:

@@ -305,8 +305,16 @@ class _MXModule(nn.Module):
         self.layer_index, self.layers, self.seed_base = layer_index, layers, seed_base
         self.cache_weight = cache_weight
         self.step = 0
+        self._release()
+
+    def _release(self):
+        """Let go of the weights held in 4 bits."""
         self._held: Optional[List[MX4]] = None
         self._held_of: list = []
+
+    def __getstate__(self) -> dict:
+        # copies and pickles quantize their own weights
+        return {**self.__dict__, "_held": None, "_held_of": []}
 
     def _next_seed(self) -> int:
         seed = self.seed_base + self.layer_index + self.layers * self.step
