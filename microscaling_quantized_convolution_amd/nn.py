@@ -208,7 +208,19 @@ def quantize_linear_weight(weight: torch.Tensor, columns: bool) -> Tuple[MX4, Op
     return row, col
 
 
-class MXLinearFunction(torch.autograd.Function):
+class _MXFunction(torch.autograd.Function):
+    """What the 4-bit functions share."""
+
+    @classmethod
+    def apply(cls, *args):
+        # ctx.needs_input_grad asks the inputs alone, so that a parameter needs a gradient also where no
+        # graph is recorded: there, nothing is to be made for a backward pass
+        if not torch.is_grad_enabled():
+            args = [a.detach() if isinstance(a, torch.Tensor) else a for a in args]
+        return super().apply(*args)
+
+
+class MXLinearFunction(_MXFunction):
     """Autograd function: y = x weight^T and its gradients through the library."""
 
     @staticmethod
@@ -247,7 +259,7 @@ class MXLinearFunction(torch.autograd.Function):
         return None if dx is None else dx.view(ctx.shape), dw, None, None
 
 
-class MXGatedFunction(torch.autograd.Function):
+class MXGatedFunction(_MXFunction):
     """Autograd function: silu(x gate^T) * (x up^T) and its gradients through the library."""
 
     @staticmethod
