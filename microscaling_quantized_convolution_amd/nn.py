@@ -35,7 +35,7 @@ forward pass keeps the input in 4 bits along its columns instead of itself:
 """
 from __future__ import annotations
 
-from typing import List, Optional, Tuple
+from typing import List, Optional, Sequence, Tuple
 
 import torch
 from torch import nn
@@ -219,6 +219,18 @@ class _MXFunction(torch.autograd.Function):
             args = [a.detach() if isinstance(a, torch.Tensor) else a for a in args]
         return super().apply(*args)
 
+    @staticmethod
+    def save(ctx, matrices: Sequence[Optional[MX4]], *tensors: Optional[torch.Tensor]):
+        """Keep 4-bit matrices and tensors as saved tensors: the backward pass frees them, hooks see them."""
+        ctx.held = [None if q is None else q.shape for q in matrices]
+        ctx.save_for_backward(*tensors, *(t for q in matrices if q is not None for t in (q.codes, q.scales)))
+
+    @staticmethod
+    def saved(ctx, tensors: int) -> Tuple[Sequence[torch.Tensor], List[Optional[MX4]]]:
+        saved = ctx.saved_tensors
+        parts = iter(saved[tensors:])
+        return saved[:tensors], [None if shape is None else MX4(*shape, next(parts), next(parts)) for shape in ctx.held]
+
 
 class MXLinearFunction(_MXFunction):
     """Autograd function: y = x weight^T and its gradients through the library."""
@@ -238,7 +250,8 @@ class MXLinearFunction(_MXFunction):
             x_col = MX4.empty(k, m, dev) if need_w else None
             y = torch.empty((m, n), dtype=x.dtype, device=dev)
             mq_mx4_linear(rows, w_row, y, mx4_linear_workspace(m, n, k, dev), x_col)
-        ctx.x_col, ctx.w_col, ctx.sr_seed = x_col, w_col, sr_seed
+        _MXFunction.save(ctx, (x_col, w_col))
+        ctx.sr_seed = sr_seed
         ctx.sizes, ctx.shape, ctx.w_dtype = (m, n, k), x.shape, weight.dtype
         return y.view(*x.shape[:-1], n)
 
@@ -247,14 +260,15 @@ class MXLinearFunction(_MXFunction):
     def backward(ctx, gy: torch.Tensor):
         m, n, k = ctx.sizes
         rows, dev = _rows_of(gy, n, "gradient"), gy.device
+        _, (x_col, w_col) = _MXFunction.saved(ctx, 0)
         dx = dw = None
         with torch.cuda.device(dev):
-            if ctx.w_col is not None:
+            if w_col is not None:
                 dx = torch.empty((m, k), dtype=gy.dtype, device=dev)
-            if ctx.x_col is not None:
+            if x_col is not None:
                 dw = torch.empty((n, k), dtype=ctx.w_dtype, device=dev)
             if dx is not None or dw is not None:
-                mq_mx4_linear_backward(rows, ctx.x_col, ctx.w_col, dx, dw,
+                mq_mx4_linear_backward(rows, x_col, w_col, dx, dw,
                                        mx4_linear_backward_workspace(m, n, k, dev), MQ_SR, ctx.sr_seed)
         return None if dx is None else dx.view(ctx.shape), dw, None, None
 
@@ -285,7 +299,8 @@ class MXGatedFunction(_MXFunction):
             g, u = (new(), new()) if need_x or need_w else (None, None)
             h = new()
             mq_mx4_gated(rows, row[0], row[1], h, mx4_gated_workspace(m, f, k, dev), g, u, x_col)
-        ctx.g, ctx.u, ctx.x_col, ctx.w_col, ctx.sr_seed = g, u, x_col, col, sr_seed
+        _MXFunction.save(ctx, (x_col, *col), g, u)
+        ctx.sr_seed = sr_seed
         ctx.sizes, ctx.shape, ctx.w_dtype = (m, f, k), x.shape, gate.dtype
         return h.view(*x.shape[:-1], f)
 
@@ -295,6 +310,7 @@ class MXGatedFunction(_MXFunction):
         m, f, k = ctx.sizes
         rows, dev = _rows_of(dh, f, "gradient"), dh.device
         need_x, need_w = ctx.needs_input_grad[0], any(ctx.needs_input_grad[1:3])
+        (g, u), (x_col, wg_col, wu_col) = _MXFunction.saved(ctx, 2)
         dx = dwg = dwu = None
         with torch.cuda.device(dev):
             if need_x:
@@ -302,9 +318,8 @@ class MXGatedFunction(_MXFunction):
             if need_w:
                 dwg, dwu = (torch.empty((f, k), dtype=ctx.w_dtype, device=dev) for _ in range(2))
             if need_x or need_w:
-                mq_mx4_gated_backward(rows, ctx.g, ctx.u, ctx.x_col, ctx.w_col[0], ctx.w_col[1], dx, dwg,
-                                      dwu, mx4_gated_backward_workspace(m, f, k, dev), MQ_SR,
-                                      ctx.sr_seed)
+                mq_mx4_gated_backward(rows, g, u, x_col, wg_col, wu_col, dx, dwg, dwu,
+                                      mx4_gated_backward_workspace(m, f, k, dev), MQ_SR, ctx.sr_seed)
         return None if dx is None else dx.view(ctx.shape), dwg, dwu, None, None
 
 

@@ -88,3 +88,45 @@ def test_no_training_work_without_a_graph(monkeypatch, mode, tokens):
     calls.made.clear()
     m(x)  # and with a graph, for the weights
     assert ("mq_mx4_gated", True) in calls.made and ("mq_mx4_linear", True) in calls.made
+
+
+def test_backward_frees_what_it_kept():
+    """A step's activations are freed by its backward pass, also while the outputs are still held."""
+    m, x = mqnn.MXGatedMLP(256, 4096).cuda(), dense(1, 2048, 256, BF16).cuda().requires_grad_()
+    m(x).sum().backward()  # gradients are there from now on
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    y = m(x)
+    kept = torch.cuda.memory_allocated() - before
+    y.sum().backward()
+    left = torch.cuda.memory_allocated() - before
+    activations = 2 * 2048 * 4096 * 2  # G and U
+    assert kept >= activations
+    assert left <= y.numel() * y.element_size() + (1 << 20)
+    with pytest.raises(RuntimeError, match="second time"):
+        y.sum().backward()
+
+
+def test_saved_tensor_hooks():
+    """What the forward pass keeps is saved as tensors: hooks see all of it, and what they give back is used."""
+    x = dense(1, 70, 96, BF16).cuda()
+    dy = dense(2, 70, 96, BF16).cuda()
+    grads = []
+    for hooks in (False, True):
+        torch.manual_seed(1)
+        m, seen = mqnn.MXGatedMLP(96, 160).cuda(), []
+        xr = x.clone().requires_grad_()
+
+        def pack(t):
+            seen.append(t.numel() * t.element_size())
+            return t.cpu()
+        if hooks:
+            with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t.cuda()):
+                y = m(xr)
+            rows = lambda r, c: -(-c // 256) * r * 136  # codes and scales
+            assert sum(seen) == 2 * 70 * 160 * 2 + rows(96, 70) + 2 * rows(96, 160) + rows(160, 70) + rows(160, 96)
+        else:
+            y = m(xr)
+        y.backward(dy)
+        grads.append([xr.grad, m.gate.grad, m.up.grad, m.down.weight.grad])
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
