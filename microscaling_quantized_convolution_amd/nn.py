@@ -196,7 +196,7 @@ def _rows_of(x: torch.Tensor, cols: int, what: str) -> torch.Tensor:
                          f"{tuple(x.shape)} {x.dtype} on {x.device}")
     if x.shape[-1] != cols:
         raise ValueError(f"{what} has {x.shape[-1]} features, the weight expects {cols}")
-    return x.reshape(-1, cols).contiguous()
+    return x.reshape(x.shape[:-1].numel(), cols).contiguous()  # (-1 cannot be told where cols is 0)
 
 
 def quantize_linear_weight(weight: torch.Tensor, columns: bool) -> Tuple[MX4, Optional[MX4]]:

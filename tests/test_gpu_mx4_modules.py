@@ -130,3 +130,23 @@ def test_saved_tensor_hooks():
         y.backward(dy)
         grads.append([xr.grad, m.gate.grad, m.up.grad, m.down.weight.grad])
     assert all(torch.equal(a, b) for a, b in zip(*grads))
+
+
+@pytest.mark.parametrize("shape", [(3, 64), (0, 64), (2, 0, 64), (64,)])
+def test_linear_without_outputs(shape):
+    layer = mqnn.MXLinear(64, 0).cuda()
+    x = torch.randn(*shape, device="cuda").requires_grad_()
+    y = layer(x)
+    assert y.shape == (*shape[:-1], 0)
+    y.sum().backward()
+    assert x.grad.shape == x.shape and (x.grad == 0).all() and layer.weight.grad.shape == (0, 64)
+
+
+def test_linear_without_inputs():
+    """A weight of no columns: sums of nothing."""
+    w = torch.empty(20, 0, device="cuda", requires_grad=True)
+    x = torch.empty(3, 0, device="cuda", requires_grad=True)
+    y = mqnn.MXLinearFunction.apply(x, w, 0, None)
+    assert y.shape == (3, 20) and (y == 0).all()
+    y.sum().backward()
+    assert x.grad.shape == (3, 0) and w.grad.shape == (20, 0)
