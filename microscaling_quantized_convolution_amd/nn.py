@@ -338,10 +338,11 @@ class _MXModule(nn.Module):
         """Let go of the weights held in 4 bits."""
         self._held: Optional[List[MX4]] = None
         self._held_of: list = []
+        self._held_at: Optional[Tuple[torch.cuda.Stream, torch.cuda.Event]] = None
 
     def __getstate__(self) -> dict:
         # copies and pickles quantize their own weights
-        return {**self.__dict__, "_held": None, "_held_of": []}
+        return {**self.__dict__, "_held": None, "_held_of": [], "_held_at": None}
 
     def _next_seed(self) -> int:
         seed = self.seed_base + self.layer_index + self.layers * self.step
@@ -354,11 +355,18 @@ class _MXModule(nn.Module):
             return None
         # the parameters themselves, not their addresses: another tensor may come to lie at one
         now = [(w, w._version, w.data_ptr(), w.dtype) for w in weights]
-        if len(now) != len(self._held_of) or any(a[0] is not b[0] or a[1:] != b[1:]
-                                                 for a, b in zip(now, self._held_of)):
-            with torch.cuda.device(weights[0].device):
+        with torch.cuda.device(weights[0].device):
+            stream = torch.cuda.current_stream()
+            if len(now) != len(self._held_of) or any(a[0] is not b[0] or a[1:] != b[1:]
+                                                     for a, b in zip(now, self._held_of)):
                 self._held = [quantize_linear_weight(w.detach().contiguous(), False)[0] for w in weights]
-            self._held_of = now
+                self._held_of, self._held_at = now, (stream, stream.record_event())
+            elif stream != self._held_at[0]:
+                # another stream than the one that quantized them: it waits for that, and their memory is
+                # not used again before it has read them
+                stream.wait_event(self._held_at[1])
+                for t in (t for q in self._held for t in (q.codes, q.scales)):
+                    t.record_stream(stream)
         return self._held
 
 

@@ -150,3 +150,32 @@ def test_linear_without_inputs():
     assert y.shape == (3, 20) and (y == 0).all()
     y.sum().backward()
     assert x.grad.shape == (3, 0) and w.grad.shape == (20, 0)
+
+
+def test_held_weights_on_another_stream():
+    """A first evaluation on one stream, behind other work, and the second at once on another one: the
+    second waits for the first one's weights, and their memory is not given away before it has read it."""
+    m, x = block(512, 2048), dense(1, 64, 512, BF16).cuda()
+    with torch.no_grad():
+        want = fresh(m, x)
+    first, second = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.no_grad():
+        with torch.cuda.stream(first):
+            torch.cuda._sleep(20_000_000)
+            a = m(x)
+        with torch.cuda.stream(second):
+            b = m(x)
+    torch.cuda.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want)
+    with torch.no_grad():
+        with torch.cuda.stream(second):  # the old weights are let go of while this still runs
+            torch.cuda._sleep(20_000_000)
+            b = m(x)
+        with torch.cuda.stream(first):
+            m.gate.mul_(1.0)
+            m.down.weight.mul_(1.0)
+            filler = [torch.full((m.hidden * m.features // 2,), 0x77, dtype=torch.uint8, device="cuda") for _ in range(8)]
+            a = m(x)
+    torch.cuda.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want) and len(filler) == 8
