@@ -356,6 +356,10 @@ class _MXModule(nn.Module):
         # the parameters themselves, not their addresses: another tensor may come to lie at one
         now = [(w, w._version, w.data_ptr(), w.dtype) for w in weights]
         with torch.cuda.device(weights[0].device):
+            if torch.cuda.is_current_stream_capturing():
+                # quantized inside the graph: a replay reads the weights as they are then, no memory that is
+                # let go of when they change, and an eager call holds nothing that only a replay fills
+                return None
             stream = torch.cuda.current_stream()
             if len(now) != len(self._held_of) or any(a[0] is not b[0] or a[1:] != b[1:]
                                                      for a, b in zip(now, self._held_of)):

@@ -179,3 +179,33 @@ def test_held_weights_on_another_stream():
             a = m(x)
     torch.cuda.synchronize()
     assert torch.equal(a, want) and torch.equal(b, want) and len(filler) == 8
+
+
+@pytest.mark.parametrize("warm", [False, True])
+def test_held_weights_and_graphs(warm):
+    """A captured evaluation quantizes the weights inside the graph: each replay takes them as they are, and
+    what an eager call holds is neither the graph's nor needed by it."""
+    m, x = block(), dense(1, 5, 64, BF16).cuda()
+    with torch.no_grad():
+        want = fresh(m, x)
+        if warm:
+            assert torch.equal(m(x), want)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = m(x)
+        assert torch.equal(m(x), want)  # eager, before any replay
+        for factor in (1.0, 2.0, -0.5):
+            m.gate.mul_(factor)
+            m.down.weight.mul_(factor)
+            want = fresh(m, x)
+            y.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+            assert torch.equal(m(x), want)
+            junk = [torch.full((1 << 16,), 0x77, dtype=torch.uint8, device="cuda") for _ in range(8)]
+            y.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want) and len(junk) == 8
