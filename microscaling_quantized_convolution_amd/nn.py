@@ -351,7 +351,8 @@ class _MXModule(nn.Module):
         return seed
 
     def _cached(self, *weights: torch.Tensor) -> Optional[List[MX4]]:
-        if self.training or not self.cache_weight:
+        # (changes of tensors made in inference mode are not counted)
+        if self.training or not self.cache_weight or any(w.is_inference() for w in weights):
             return None
         # the parameters themselves, not their addresses: another tensor may come to lie at one
         now = [(w, w._version, w.data_ptr(), w.dtype) for w in weights]

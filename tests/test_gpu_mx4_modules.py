@@ -209,3 +209,13 @@ def test_held_weights_and_graphs(warm):
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, want) and len(junk) == 8
+
+
+def test_weights_made_in_inference_mode():
+    """Their changes are not counted, so that they are not held."""
+    x = dense(1, 5, 64, BF16).cuda()
+    with torch.inference_mode():
+        m = block()
+        y = m(x)
+        m.gate.mul_(2.0)
+        assert torch.equal(m(x), fresh(m, x)) and not torch.equal(m(x), y)
