@@ -325,7 +325,9 @@ class MXGatedFunction(_MXFunction):
 
 class _MXModule(nn.Module):
     """What the 4-bit modules share: seeds of the stochastic rounding, and weights held in 4 bits
-    from one evaluation to the next (``cache_weight``) until a parameter changes."""
+    from one evaluation to the next (``cache_weight``) until a parameter changes: its version counter moves,
+    another takes its place, or the module is moved, cast, or told ``train()`` or ``eval()`` (changes through
+    ``.data`` are not counted: they need one of these)."""
 
     def __init__(self, layer_index: int, layers: int, seed_base: int, cache_weight: bool):
         super().__init__()
@@ -343,6 +345,14 @@ class _MXModule(nn.Module):
     def __getstate__(self) -> dict:
         # copies and pickles quantize their own weights
         return {**self.__dict__, "_held": None, "_held_of": [], "_held_at": None}
+
+    def train(self, mode: bool = True):
+        self._release()
+        return super().train(mode)
+
+    def _apply(self, *args, **kwargs):
+        self._release()
+        return super()._apply(*args, **kwargs)
 
     def _next_seed(self) -> int:
         seed = self.seed_base + self.layer_index + self.layers * self.step

@@ -219,3 +219,18 @@ def test_weights_made_in_inference_mode():
         y = m(x)
         m.gate.mul_(2.0)
         assert torch.equal(m(x), fresh(m, x)) and not torch.equal(m(x), y)
+
+
+def test_weights_changed_past_their_versions():
+    """`.data` changes are not counted: eval() and moves let go of held weights."""
+    m, x = block(), dense(1, 5, 64, BF16).cuda()
+    with torch.no_grad():
+        y = m(x)
+        m.gate.data.mul_(-2.0)
+        m.down.weight.data.mul_(0.5)
+        m.eval()
+        assert torch.equal(m(x), fresh(m, x)) and not torch.equal(m(x), y)
+        m.cpu()
+        m.up.data.mul_(3.0)
+        m.cuda()
+        assert torch.equal(m(x), fresh(m, x))
