@@ -19,7 +19,9 @@ experiments use for the layers it does not quantize.
 
 Stochastic rounding draws its bits from a seed per call: ``seed_base + layer_index +
 layers * step`` with ``step`` counted by the module (one per training forward), so a run is
-reproducible and no two layers or steps share a stream of random bits.
+reproducible, and no two layers or steps share a stream of random bits where every layer of a model
+has a number of its own in 0 .. ``layers`` - 1. An ``MXGatedMLP`` takes two: block i of ``layers``
+blocks is numbers 2i and 2i + 1 of 2 ``layers``. ``number_layers`` numbers a model of several kinds.
 
 In eval mode with ``cache_weight=True`` the weight is quantized once and reused until the
 parameter changes (its version counter moves): the inference path then quantizes only
@@ -426,6 +428,16 @@ class MXGatedMLP(_MXModule):
 
     def extra_repr(self) -> str:
         return f"{self.features}, {self.hidden}"
+
+
+def number_layers(model: nn.Module, seed_base: int = 1) -> int:
+    """Number a model's quantized layers through (``MQConv2d``, ``MXLinear``, and the two products of each
+    ``MXGatedMLP``), in the order of ``model.modules()``, so that no two of them round their gradients by
+    the same bits in any step. Returns how many there are."""
+    layers = [m for m in model.modules() if isinstance(m, (MQConv2d, _MXModule))]
+    for i, m in enumerate(layers):
+        m.layer_index, m.layers, m.seed_base = i, len(layers), seed_base
+    return len(layers)
 
 
 # ---- ResNet-18 with the 19 body convolutions quantized ---------------------------------------

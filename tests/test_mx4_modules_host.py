@@ -45,3 +45,44 @@ def test_matrix_shared_copy():
     assert copy.copy(q).codes is q.codes
     a, b = copy.deepcopy([q, q])
     assert a is b and a is not q
+
+
+def model():
+    """Projections, gated blocks and a convolution in one model, each number given as if all were of one kind."""
+    parts = [mqnn.MXLinear(32, 32, i, 6, 9) for i in (0, 1, 3, 4)]
+    parts[2:2] = [mqnn.MXGatedMLP(32, 64, 2, 6, 9)]
+    return torch.nn.Sequential(*parts, mqnn.MXGatedMLP(32, 64, 5, 6, 9), mqnn.MQConv2d(4, 4, 3, layer_index=2, layers=6))
+
+
+def seeds(m, steps):
+    """The seeds of every gradient that the model's layers round, over some steps."""
+    found = [p for p in m.modules() if hasattr(p, "layer_index")]
+    drawn = []
+    for _ in range(steps):
+        for p in found:
+            if isinstance(p, mqnn.MQConv2d):
+                drawn.append(p.sr_seed())
+                p.step += 1
+            else:
+                drawn.append(p._next_seed())
+    return drawn
+
+
+def test_seeds_of_a_mixed_model():
+    """Numbered through, no two layers or steps share a seed, whatever their kinds; a model without gated
+    blocks keeps the numbers that it would be given by hand."""
+    m = model()
+    assert mqnn.number_layers(m, 9) == 9
+    drawn = seeds(m, 5)
+    assert len(drawn) == 45 and sorted(drawn) == list(range(9, 54))
+    net = mqnn.ResNet18MQ(fmt=mq.MQ_NVFP4, seed_base=4)
+    before = [c.sr_seed() for c in net.mq_convs]
+    assert mqnn.number_layers(net, 4) == len(before) and [c.sr_seed() for c in net.mq_convs] == before
+
+
+def test_seeds_of_one_kind():
+    """By hand: projections by their numbers, gated blocks by pairs of numbers."""
+    for make, each in ((lambda i: mqnn.MXLinear(32, 32, i, 4, 3), 1), (lambda i: mqnn.MXGatedMLP(32, 32, i, 4, 3), 2)):
+        m = torch.nn.Sequential(*(make(i) for i in range(4)))
+        drawn = seeds(m, 3)
+        assert sorted(drawn) == list(range(3, 3 + 12 * each))
