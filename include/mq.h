@@ -589,10 +589,12 @@ mq_status mq_mx4_dequantize(const mq_mx4 *q, const mq_matrix *out, hipStream_t s
 /*
  * mq_mx4_matmul: y = a b^T, y[m][n] = sum_k a[m][k] * b[n][k], rounded once to y's type.
  * a: M x K, b: N x K, y: M x N (K = 0 gives zeros).
- * ws_dev / ws_bytes: device scratch, 16-byte aligned, of at least
- *          mq_mx4_matmul_workspace_bytes(M, N, K) bytes (may be null where that is 0); so for
- *          the calls below. What suffices for M rows suffices for fewer.
- * Errors: MQ_ERR_ARG, MQ_ERR_SHAPE, MQ_ERR_WORKSPACE, MQ_ERR_UNSUPPORTED (as mq_mx4_quantize).
+ * ws_dev / ws_bytes: not used: mq_mx4_matmul_workspace_bytes is 0 for all sizes, and ws_dev may be
+ *          null. Of the calls below: device scratch, 16-byte aligned, of at least
+ *          mq_mx4_..._workspace_bytes(M, N, K) bytes (may be null where that is 0). What suffices
+ *          for M rows suffices for fewer.
+ * Errors: MQ_ERR_ARG (ws_dev not 16-byte aligned among them), MQ_ERR_SHAPE, MQ_ERR_UNSUPPORTED
+ *         (as mq_mx4_quantize); of the calls below also MQ_ERR_WORKSPACE.
  */
 size_t mq_mx4_matmul_workspace_bytes(int32_t m, int32_t n, int32_t k);
 mq_status mq_mx4_matmul(const mq_mx4 *a, const mq_mx4 *b, const mq_matrix *y, void *ws_dev,

@@ -609,11 +609,12 @@ def _mx4_workspace(name: str, m: int, n: int, k: int, device) -> torch.Tensor:
 
 
 def mx4_matmul_workspace(m: int, n: int, k: int, device: Union[str, torch.device] = "cuda") -> torch.Tensor:
-    """Device scratch for mq_mx4_matmul calls of up to m rows (so for the other calls)."""
+    """Device scratch for mq_mx4_matmul calls of up to m rows: nothing, for all sizes."""
     return _mx4_workspace("matmul", m, n, k, device)
 
 
 def mx4_linear_workspace(m: int, n: int, k: int, device: Union[str, torch.device] = "cuda") -> torch.Tensor:
+    """Device scratch for mq_mx4_linear calls of up to m rows (so for the calls below)."""
     return _mx4_workspace("linear", m, n, k, device)
 
 

@@ -53,7 +53,6 @@ struct Mx4MatmulArgs {
     bool through;   // set by the launch: outputs are written past the caches
     MatView x;      // null, or a[0][0] still dense (mx4_quantizes_rows): m rows of `cols`
     int cols;
-    void *ws;
 };
 
 hipError_t launch_mx4_quantize(const Mx4QuantArgs &a, hipStream_t st);
@@ -63,7 +62,5 @@ hipError_t launch_mx4_matmul(const Mx4MatmulArgs &a, hipStream_t st);
 // whether launch_mx4_matmul takes these m rows dense, and quantizes them itself
 bool mx4_quantizes_rows(int m, int n, int k);
 hipError_t launch_mx4_rows(const Mx4MatmulArgs &a, hipStream_t st); // m <= 16
-// bytes of a.ws for m x n outputs from k columns (0: none); no smaller for smaller m
-size_t mx4_matmul_workspace(int jobs, int m, int n, int k);
 
 } // namespace mq

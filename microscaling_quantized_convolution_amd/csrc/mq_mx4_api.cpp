@@ -75,7 +75,7 @@ mq::Mx4QuantArgs quantize_args(const mq_matrix *x, int32_t rnd, uint64_t seed)
     return a;
 }
 
-mq::Mx4MatmulArgs matmul_args(const mq::Mx4View &a, const mq::Mx4View &b, const mq_matrix *y, void *ws)
+mq::Mx4MatmulArgs matmul_args(const mq::Mx4View &a, const mq::Mx4View &b, const mq_matrix *y)
 {
     mq::Mx4MatmulArgs m = {};
     m.a[0][0] = a;
@@ -85,7 +85,6 @@ mq::Mx4MatmulArgs matmul_args(const mq::Mx4View &a, const mq::Mx4View &b, const 
     m.m = y->rows;
     m.n = y->cols;
     m.pieces[0] = a.pieces();
-    m.ws = ws;
     return m;
 }
 
@@ -101,8 +100,6 @@ mq_status quantize_input(const mq_matrix *x, const mq_mx4 *x_col, bool inside, u
 }
 
 bool sizes_ok(int32_t a, int32_t b, int32_t c) { return a >= 0 && b >= 0 && c >= 0 && fits(a, b, c); }
-
-size_t max2(size_t a, size_t b) { return a > b ? a : b; }
 
 } // namespace
 
@@ -140,26 +137,20 @@ mq_status mq_mx4_dequantize(const mq_mx4 *q, const mq_matrix *out, hipStream_t s
     return launched(mq::launch_mx4_dequantize(view(q), view(out), stream));
 }
 
-size_t mq_mx4_matmul_workspace_bytes(int32_t m, int32_t n, int32_t k)
-{
-    return sizes_ok(m, n, k) ? mq::mx4_matmul_workspace(1, m, n, k) : 0;
-}
+size_t mq_mx4_matmul_workspace_bytes(int32_t, int32_t, int32_t) { return 0; }
 
 mq_status mq_mx4_matmul(const mq_mx4 *a, const mq_mx4 *b, const mq_matrix *y, void *ws,
-                        size_t ws_bytes, hipStream_t stream)
+                        size_t, hipStream_t stream)
 {
-    if (!held_ok(a) || !held_ok(b) || !matrix_ok(y)) return MQ_ERR_ARG;
+    if (!held_ok(a) || !held_ok(b) || !matrix_ok(y) || !aligned(ws, 16)) return MQ_ERR_ARG;
     if (a->cols != b->cols || !is(y, a->rows, b->rows)) return MQ_ERR_SHAPE;
     if (!fits(a->rows, b->rows, a->cols)) return MQ_ERR_UNSUPPORTED;
-    const size_t need = mq::mx4_matmul_workspace(1, a->rows, b->rows, a->cols);
-    if (!aligned(ws, 16)) return MQ_ERR_ARG;
-    if (need && (!ws || ws_bytes < need)) return MQ_ERR_WORKSPACE;
-    return launched(mq::launch_mx4_matmul(matmul_args(view(a), view(b), y, ws), stream));
+    return launched(mq::launch_mx4_matmul(matmul_args(view(a), view(b), y), stream));
 }
 
 size_t mq_mx4_linear_workspace_bytes(int32_t m, int32_t n, int32_t k)
 {
-    return sizes_ok(m, n, k) ? held_bytes(m, k) + mq::mx4_matmul_workspace(1, m, n, k) : 0;
+    return sizes_ok(m, n, k) ? held_bytes(m, k) : 0;
 }
 
 mq_status mq_mx4_linear(const mq_matrix *x, const mq_mx4 *w, const mq_matrix *y,
@@ -177,16 +168,14 @@ mq_status mq_mx4_linear(const mq_matrix *x, const mq_mx4 *w, const mq_matrix *y,
     const bool inside = !x_col && mq::mx4_quantizes_rows(x->rows, w->rows, x->cols);
     const mq_status st = quantize_input(x, x_col, inside, at, row, stream);
     if (st != MQ_OK) return st;
-    mq::Mx4MatmulArgs a = matmul_args(row, view(w), y, at);
+    mq::Mx4MatmulArgs a = matmul_args(row, view(w), y);
     if (inside) a.x = view(x), a.cols = x->cols;
     return launched(mq::launch_mx4_matmul(a, stream));
 }
 
 size_t mq_mx4_linear_backward_workspace_bytes(int32_t m, int32_t n, int32_t k)
 {
-    if (!sizes_ok(m, n, k)) return 0;
-    return held_bytes(m, n) + held_bytes(n, m) +
-           max2(mq::mx4_matmul_workspace(1, m, k, n), mq::mx4_matmul_workspace(1, n, k, m));
+    return sizes_ok(m, n, k) ? held_bytes(m, n) + held_bytes(n, m) : 0;
 }
 
 mq_status mq_mx4_linear_backward(const mq_matrix *dy, const mq_mx4 *x_col, const mq_mx4 *w_col,
@@ -208,14 +197,14 @@ mq_status mq_mx4_linear_backward(const mq_matrix *dy, const mq_mx4 *x_col, const
     if (dw) q.col = col;
     mq_status st = MQ_OK;
     if (m && n) st = launched(mq::launch_mx4_quantize(q, stream));
-    if (st == MQ_OK && dx) st = launched(mq::launch_mx4_matmul(matmul_args(row, view(w_col), dx, at), stream));
-    if (st == MQ_OK && dw) st = launched(mq::launch_mx4_matmul(matmul_args(col, view(x_col), dw, at), stream));
+    if (st == MQ_OK && dx) st = launched(mq::launch_mx4_matmul(matmul_args(row, view(w_col), dx), stream));
+    if (st == MQ_OK && dw) st = launched(mq::launch_mx4_matmul(matmul_args(col, view(x_col), dw), stream));
     return st;
 }
 
 size_t mq_mx4_gated_workspace_bytes(int32_t m, int32_t f, int32_t k)
 {
-    return sizes_ok(m, f, k) ? held_bytes(m, k) + mq::mx4_matmul_workspace(2, m, f, k) : 0;
+    return sizes_ok(m, f, k) ? held_bytes(m, k) : 0;
 }
 
 mq_status mq_mx4_gated(const mq_matrix *x, const mq_mx4 *wg, const mq_mx4 *wu, const mq_matrix *h,
@@ -236,7 +225,7 @@ mq_status mq_mx4_gated(const mq_matrix *x, const mq_mx4 *wg, const mq_mx4 *wu, c
     const bool inside = !x_col && mq::mx4_quantizes_rows(m, f, k);
     const mq_status st = quantize_input(x, x_col, inside, at, row, stream);
     if (st != MQ_OK) return st;
-    mq::Mx4MatmulArgs a = matmul_args(row, view(wg), h, at);
+    mq::Mx4MatmulArgs a = matmul_args(row, view(wg), h);
     if (inside) a.x = view(x), a.cols = k;
     a.b[0][1] = view(wu);
     a.g = view(g);
@@ -247,9 +236,7 @@ mq_status mq_mx4_gated(const mq_matrix *x, const mq_mx4 *wg, const mq_mx4 *wu, c
 
 size_t mq_mx4_gated_backward_workspace_bytes(int32_t m, int32_t f, int32_t k)
 {
-    if (!sizes_ok(m, f, k)) return 0;
-    return 2 * (held_bytes(m, f) + held_bytes(f, m)) +
-           max2(mq::mx4_matmul_workspace(1, m, k, 2 * (f < (1 << 29) ? f : (1 << 29))), mq::mx4_matmul_workspace(2, f, k, m));
+    return sizes_ok(m, f, k) ? 2 * (held_bytes(m, f) + held_bytes(f, m)) : 0;
 }
 
 mq_status mq_mx4_gated_backward(const mq_matrix *dh, const mq_matrix *g, const mq_matrix *u,
@@ -280,14 +267,14 @@ mq_status mq_mx4_gated_backward(const mq_matrix *dh, const mq_matrix *g, const m
     mq_status st = MQ_OK;
     if (m && f) st = launched(mq::launch_mx4_gradients(q, stream));
     if (st == MQ_OK && dx) {
-        mq::Mx4MatmulArgs a = matmul_args(row, view(wg_col), dx, at);
+        mq::Mx4MatmulArgs a = matmul_args(row, view(wg_col), dx);
         a.a[0][1] = row2;
         a.b[0][1] = view(wu_col);
         a.pieces[1] = a.pieces[0];
         st = launched(mq::launch_mx4_matmul(a, stream));
     }
     if (st == MQ_OK && dwg) {
-        mq::Mx4MatmulArgs a = matmul_args(col, view(x_col), dwg, at);
+        mq::Mx4MatmulArgs a = matmul_args(col, view(x_col), dwg);
         a.a[1][0] = col2;
         a.b[1][0] = a.b[0][0];
         a.y[1] = view(dwu);

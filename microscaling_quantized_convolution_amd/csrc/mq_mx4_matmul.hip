@@ -363,8 +363,6 @@ Kind kind_of(const Mx4MatmulArgs &a)
 
 } // namespace
 
-size_t mx4_matmul_workspace(int, int, int, int) { return 0; }
-
 bool mx4_quantizes_rows(int m, int n, int k)
 {
     return rows_kind(m, n) && (int64_t)m * k <= 1 << 14 && (int64_t)m * k * ((n + 15) / 16) <= 1 << 22;
