@@ -52,8 +52,8 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Mx4QuantArgs a, 
 //
 // Lane (q, cg) of a wave holds NR rows of 8 columns: 8 NR rows of 64 columns to a wave, and four waves
 // beside each other, so that rows are read in long runs (one above another: gradients of 4096 x 8192
-// 80 us in place of 61, fp32 42.5 in place of 40). A row's block lies in a quad of lanes; a column's in one
-// lane (NR = 32), or in 32 / NR of them, 8 lanes apart.
+// 80 us in place of 61, fp32 42.5 in place of 40). A row's block lies in a quad of lanes; a column's in
+// 32 / NR lanes, 8 lanes apart (NR = 4, 8 or 16; 32 rows of 16-bit elements: the kernel behind this one).
 
 // Eight values to quantize: of x, or of dg and du of h = silu(g) u.
 template <int DT, bool GRAD, bool TAIL, bool PASS> struct Source {
@@ -94,6 +94,7 @@ __device__ __forceinline__ uint32_t max_lane_xor_32(uint32_t v)
 template <int DT, bool GRAD, int NR, bool SR, bool TAIL>
 __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs a, int across)
 {
+    static_assert(NR == 4 || NR == 8 || NR == 16, "a column's block is in two lanes or more");
     constexpr int K = Source<DT, GRAD, TAIL, (NR >= 16)>::K, WR = 8 * NR; // rows of a wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 3, cg = lane & 7;
     const int c0 = ((int)(blockIdx.x % across) * 4 + wave) * 64, c = c0 + cg * 8;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
                 uint32_t amax = 0;
 #pragma unroll
                 for (int r = 0; r < NR; ++r) amax = max_u32(amax, __float_as_uint(v[k][r][i]) & 0x7FFFFFFFu);
-                if constexpr (NR < 32) amax = max_u32(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x128, 0xF, 0xF, true)); // lane ^ 8
+                amax = max_u32(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x128, 0xF, 0xF, true)); // lane ^ 8
                 if constexpr (NR < 16) amax = max_lane_xor_16(amax);
                 if constexpr (NR < 8) amax = max_lane_xor_32(amax);
                 const uint32_t e = mx4_scale(amax);
@@ -153,11 +154,10 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
                     codes[w] = encode8<SR>(t, e, n, 2 * k + 1, a.seed_lo, a.seed_hi);
                 }
                 uint32_t *to = (uint32_t *)(first + i * 128);
-                if constexpr (NR == 32) *(u32x4_t *)to = *(const u32x4_t *)codes;
-                else if constexpr (NR == 16) *(uint64_t *)to = *(const uint64_t *)codes;
+                if constexpr (NR == 16) *(uint64_t *)to = *(const uint64_t *)codes;
                 else if constexpr (NR == 8) *to = codes[0];
                 else ((uint16_t *)to)[part / 4 % 2] = (uint16_t)(part & 4 ? codes[0] >> 16 : codes[0]);
-                if (NR == 32 || part % 32 == 0) zs[i * 8] = (uint8_t)e;
+                if (part % 32 == 0) zs[i * 8] = (uint8_t)e;
             }
         }
     }
