@@ -63,4 +63,11 @@ hipError_t launch_mx4_matmul(const Mx4MatmulArgs &a, hipStream_t st);
 bool mx4_quantizes_rows(int m, int n, int k);
 hipError_t launch_mx4_rows(const Mx4MatmulArgs &a, hipStream_t st); // m <= 16
 
+// The rules of the launches, which tests hold their sizes against: the kernel that products of these
+// sizes take (pieces: of both sums) ...
+enum Mx4Kind { kMx4Rows, kMx4Tile64, kMx4Tile128Deep, kMx4Tile128, kMx4Tile256 };
+int mx4_matmul_kind(int jobs, int m, int n, int pieces, bool gated);
+// ... and the rows to a lane of a quantization along the columns (32: the packed kernel)
+int mx4_quantize_height(int rows, int cols, int dtype, bool sr, bool gradients);
+
 } // namespace mq

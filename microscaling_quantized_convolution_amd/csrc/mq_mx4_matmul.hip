@@ -314,27 +314,25 @@ hipError_t matmul_tiles(const Mx4MatmulArgs &a, hipStream_t st)
     return hipGetLastError();
 }
 
-enum Kind { kRows, kTile64, kTile128Deep, kTile128, kTile256 };
-
 template <int DT, bool GATED>
-hipError_t matmul(const Mx4MatmulArgs &a, Kind kind, hipStream_t st)
+hipError_t matmul(const Mx4MatmulArgs &a, int kind, hipStream_t st)
 {
-    if (kind == kTile256) return matmul_tiles<DT, GATED, 4, 2, 2, 4, 2>(a, st);
-    if (kind == kTile128) return matmul_tiles<DT, GATED, 4, 2, 1, 2, 2>(a, st);
-    if (kind == kTile128Deep) return matmul_tiles<DT, GATED, 4, 2, 1, 2, 4>(a, st);
+    if (kind == kMx4Tile256) return matmul_tiles<DT, GATED, 4, 2, 2, 4, 2>(a, st);
+    if (kind == kMx4Tile128) return matmul_tiles<DT, GATED, 4, 2, 1, 2, 2>(a, st);
+    if (kind == kMx4Tile128Deep) return matmul_tiles<DT, GATED, 4, 2, 1, 2, 4>(a, st);
     if constexpr (GATED) return matmul_tiles<DT, true, 2, 2, 1, 2, 3>(a, st);
     else return matmul_tiles<DT, false, 2, 2, 1, 1, 4>(a, st);
 }
 
 template <int DT>
-hipError_t matmul(const Mx4MatmulArgs &a, Kind kind, hipStream_t st)
+hipError_t matmul(const Mx4MatmulArgs &a, int kind, hipStream_t st)
 {
     return a.gated ? matmul<DT, true>(a, kind, st) : matmul<DT, false>(a, kind, st);
 }
 
-int64_t tiles_of(const Mx4MatmulArgs &a, int bm, int bn)
+int64_t tiles_of(int jobs, int m, int n, int bm, int bn)
 {
-    return (((int64_t)a.m + bm - 1) / bm) * (((int64_t)a.n + bn - 1) / bn) * a.jobs;
+    return (((int64_t)m + bm - 1) / bm) * (((int64_t)n + bn - 1) / bn) * jobs;
 }
 
 // Up to 16 rows, a workgroup takes 16 columns and its waves share the sum; where tiles of 64 columns come
@@ -342,26 +340,25 @@ int64_t tiles_of(const Mx4MatmulArgs &a, int bm, int bn)
 // 8192 7.1, where strips of 16 take 6.4).
 bool rows_kind(int m, int64_t n) { return m <= 16 && n < 12288; }
 
-Kind kind_of(const Mx4MatmulArgs &a)
+} // namespace
+
+int mx4_matmul_kind(int jobs, int m, int n, int pieces, bool gated)
 {
-    const bool g = a.gated;
-    if (rows_kind(a.m, (int64_t)a.n * a.jobs)) return kRows;
+    const auto tiles = [&](int bm, int bn) { return tiles_of(jobs, m, n, bm, bn); };
+    if (rows_kind(m, (int64_t)n * jobs)) return kMx4Rows;
     // 64 x 64 while the chip holds them all at once: 512 x 4096 x 4096 (512 tiles) 9.8 us, 128 x 128 12.4;
     // 1024 x 4096 x 4096 17.4 and 13.9. Gated (twice the weight's rows to a tile): 300 x 1024 on 2700 (215)
     // 9.6 and 11.1, 256 x 4096 on 8192 (512) 17.2 and 15.2.
-    if (tiles_of(a, 64, 64) <= (g ? 256 : 512)) return kTile64;
+    if (tiles(64, 64) <= (gated ? 256 : 512)) return kMx4Tile64;
     // four slots while no CU has two of 128 x 128: 2048 x 2048 x 8192 (256) 23.8 us, with two slots 26.6;
     // 2048 x 4096 x 4096 (512) 25.8 and 22.8
-    if (tiles_of(a, 128, g ? 64 : 128) <= 256) return kTile128Deep;
+    if (tiles(128, gated ? 64 : 128) <= 256) return kMx4Tile128Deep;
     // 256 x 256 one to a CU, or 128 x 128 two to a CU: rounds of the chip, each of so much for a piece
     // and for a tile's beginning and end (in ns, measured at 2 to 64 pieces)
-    const int64_t pieces = a.pieces[0] + a.pieces[1];
-    const int64_t t256 = (tiles_of(a, 256, g ? 128 : 256) + 255) / 256 * (1810 * pieces + 8000);
-    const int64_t t128 = (tiles_of(a, 128, g ? 64 : 128) + 511) / 512 * (1250 * pieces + 3000);
-    return t256 < t128 ? kTile256 : kTile128;
+    const double t256 = (double)((tiles(256, gated ? 128 : 256) + 255) / 256) * (1810.0 * pieces + 8000);
+    const double t128 = (double)((tiles(128, gated ? 64 : 128) + 511) / 512) * (1250.0 * pieces + 3000);
+    return t256 < t128 ? kMx4Tile256 : kMx4Tile128;
 }
-
-} // namespace
 
 bool mx4_quantizes_rows(int m, int n, int k)
 {
@@ -372,13 +369,13 @@ hipError_t launch_mx4_matmul(const Mx4MatmulArgs &given, hipStream_t st)
 {
     if (given.m == 0 || given.n == 0) return hipSuccess;
     Mx4MatmulArgs a = given;
-    const Kind kind = kind_of(a);
-    if (kind == kRows) return launch_mx4_rows(a, st);
+    const int kind = mx4_matmul_kind(a.jobs, a.m, a.n, a.pieces[0] + a.pieces[1], a.gated);
+    if (kind == kMx4Rows) return launch_mx4_rows(a, st);
     // Outputs that would fill the caches, and those of many rounds of tiles, are written past them: other
     // tiles' loads then pass the stores (8192 x 8192 x 4096 to bf16 155 -> 136 us, gated 4096 x 8192 x 4096
     // 151 -> 132, with G and U 174 -> 154; but 8192 x 4096 x 4096, two rounds of 67 MB, 69 -> 72.5).
     const int64_t bytes = (int64_t)a.m * a.n * (a.y[0].dtype == MQ_F32 ? 4 : 2) * (a.jobs + (a.g.p ? 2 : 0));
-    a.through = bytes >= 80 << 20 || (kind == kTile256 && tiles_of(a, 256, a.gated ? 128 : 256) >= 768);
+    a.through = bytes >= 80 << 20 || (kind == kMx4Tile256 && tiles_of(a.jobs, a.m, a.n, 256, a.gated ? 128 : 256) >= 768);
     const int dt = a.y[0].dtype;
     return dt == MQ_BF16 ? matmul<MQ_BF16>(a, kind, st) : (dt == MQ_F16 ? matmul<MQ_F16>(a, kind, st) : matmul<MQ_F32>(a, kind, st));
 }

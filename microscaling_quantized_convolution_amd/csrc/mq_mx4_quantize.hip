@@ -331,12 +331,10 @@ template <int DT, bool SR>
 hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
 {
     if (!grad && !a.col.codes) return rows_alone<DT, SR>(a, st);
-    // the tallest tiles that give each SIMD a wave: taller ones write longer runs of a column's codes
-    const auto waves = [&](int nr) { return ((int64_t)a.rows + 8 * nr - 1) / (8 * nr) * ((a.cols + 63) / 64); };
-    constexpr int TALL = DT != MQ_F32 && !SR ? 32 : 16;
-    if (grad) return waves(8) >= 1024 ? both<DT, true, 8, SR>(a, st) : both<DT, true, 4, SR>(a, st);
-    if (waves(TALL) >= 1024) return both<DT, false, TALL, SR>(a, st);
-    return waves(8) >= 1024 ? both<DT, false, 8, SR>(a, st) : both<DT, false, 4, SR>(a, st);
+    const int height = mx4_quantize_height(a.rows, a.cols, DT, SR, grad);
+    if (grad) return height == 8 ? both<DT, true, 8, SR>(a, st) : both<DT, true, 4, SR>(a, st);
+    if (height >= 16) return both<DT, false, DT != MQ_F32 && !SR ? 32 : 16, SR>(a, st);
+    return height == 8 ? both<DT, false, 8, SR>(a, st) : both<DT, false, 4, SR>(a, st);
 }
 
 hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
@@ -347,6 +345,15 @@ hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
 }
 
 } // namespace
+
+// The tallest tiles that give each SIMD a wave: taller ones write longer runs of a column's codes.
+int mx4_quantize_height(int rows, int cols, int dtype, bool sr, bool gradients)
+{
+    const auto waves = [&](int nr) { return ((int64_t)rows + 8 * nr - 1) / (8 * nr) * (((int64_t)cols + 63) / 64); };
+    const int tall = dtype != MQ_F32 && !sr ? 32 : 16;
+    if (!gradients && waves(tall) >= 1024) return tall;
+    return waves(8) >= 1024 ? 8 : 4;
+}
 
 hipError_t launch_mx4_quantize(const Mx4QuantArgs &a, hipStream_t st) { return quantize(a, false, st); }
 
