@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(Mx4View q, MatView 
         for (int j = 0; j < (int)sizeof(T) / 2; ++j) {
             typedef u32x4_t Any __attribute__((aligned(2)));
             const u32x4_t w = ((const u32x4_t *)v)[j];
-            if (through) store_past((u32x4_t *)to + j, w);
+            if (sizeof(T) == 2 && through) store_past((u32x4_t *)to + j, w);
             else *(Any *)((u32x4_t *)to + j) = w;
         }
     } else {
@@ -365,8 +365,11 @@ hipError_t launch_mx4_dequantize(const Mx4View &q, const MatView &out, hipStream
     const int groups = (q.cols + 7) / 8, width = width_of(groups), across = (groups + width - 1) / width;
     const int64_t grid = ((int64_t)q.rows + 256 / width - 1) / (256 / width) * across;
     if (grid > kMaxGroups) return hipErrorInvalidValue;
-    // what would fill the caches is written past them (8192 x 4096 to bf16 18.0 -> 16.4 us)
-    const bool through = (int64_t)q.rows * q.cols * (out.dtype == MQ_F32 ? 4 : 2) >= 64 << 20;
+    // 16-bit values that would fill the caches are written past them: 8192 x 4096 18.3 -> 16.8 us, 16384 x 4096
+    // 47.8 -> 30.9. (Below, the call alone would gain too, 4096 x 4096 11.2 -> 9.7, but what reads the values next
+    // would lose as much: both together 21.7 -> 23.1.) A thread's 32 bytes of fp32 leave by two stores, each of
+    // every other 16 bytes of a line, which only the caches put together: 16384 x 4096 81 -> 119 us past them.
+    const bool through = out.dtype != MQ_F32 && (int64_t)q.rows * q.cols * 2 >= 64 << 20;
     if (out.dtype == MQ_BF16) mx4_dequantize_kernel<MQ_BF16><<<(uint32_t)grid, 256, 0, st>>>(q, out, through, width, across);
     else if (out.dtype == MQ_F16) mx4_dequantize_kernel<MQ_F16><<<(uint32_t)grid, 256, 0, st>>>(q, out, through, width, across);
     else mx4_dequantize_kernel<MQ_F32><<<(uint32_t)grid, 256, 0, st>>>(q, out, through, width, across);
