@@ -372,10 +372,19 @@ hipError_t launch_mx4_matmul(const Mx4MatmulArgs &given, hipStream_t st)
     const int kind = mx4_matmul_kind(a.jobs, a.m, a.n, a.pieces[0] + a.pieces[1], a.gated);
     if (kind == kMx4Rows) return launch_mx4_rows(a, st);
     // Outputs that would fill the caches, and those of many rounds of tiles, are written past them: other
-    // tiles' loads then pass the stores (8192 x 8192 x 4096 to bf16 155 -> 136 us, gated 4096 x 8192 x 4096
-    // 151 -> 132, with G and U 174 -> 154; but 8192 x 4096 x 4096, two rounds of 67 MB, 69 -> 72.5).
-    const int64_t bytes = (int64_t)a.m * a.n * (a.y[0].dtype == MQ_F32 ? 4 : 2) * (a.jobs + (a.g.p ? 2 : 0));
-    a.through = bytes >= 80 << 20 || (kind == kMx4Tile256 && tiles_of(a.jobs, a.m, a.n, 256, a.gated ? 128 : 256) >= 768);
+    // tiles' loads then pass the stores (8192 x 8192 x 4096 to bf16 155 -> 142 us, 8192 x 8192 x 512 58 -> 41,
+    // gated 4096 x 8192 x 4096 152 -> 138, with G and U 175 -> 158; but 8192 x 4096 x 4096, two rounds of 67
+    // MB, 73 -> 76). Rows that share lines of memory leave them half written: only the caches put these
+    // together (5000 x 4200 x 1000 to fp32 28 us, past them 34; gated 3000 x 5001 x 1000 with G and U 44,
+    // past them 98), until one output alone is far larger than they are, and its sums are long enough to hide it
+    // (8192 x 8191 to bf16, 128 MB: of 512 columns 56 and 66 us, of 1024 68 and 65, of 4096 157 and 149).
+    const int size = a.y[0].dtype == MQ_F32 ? 4 : 2, outputs = a.jobs + (a.g.p ? 2 : 0);
+    const int64_t bytes = (int64_t)a.m * a.n * size * outputs;
+    const auto whole = [&](const MatView &y) { return (reinterpret_cast<uintptr_t>(y.p) | (uint64_t)y.stride * size) % 64 == 0; };
+    if (whole(a.y[0]) && whole(a.y[1]) && whole(a.g) && whole(a.u)) // (those that are not wanted are 0)
+        a.through = bytes >= 80 << 20 || (kind == kMx4Tile256 && tiles_of(a.jobs, a.m, a.n, 256, a.gated ? 128 : 256) >= 768);
+    else
+        a.through = outputs == 1 && bytes >= 112 << 20 && a.pieces[0] + a.pieces[1] >= 4;
     const int dt = a.y[0].dtype;
     return dt == MQ_BF16 ? matmul<MQ_BF16>(a, kind, st) : (dt == MQ_F16 ? matmul<MQ_F16>(a, kind, st) : matmul<MQ_F32>(a, kind, st));
 }

@@ -53,10 +53,12 @@ def grid(seed, rows, cols, dtype, factor=1.0):
     return (v[torch.randint(0, 16, (rows, cols), generator=g, device="cuda")] * factor).to(dtype)
 
 
-def inside(rows, cols, dtype):
-    """Room for an output in the midst of a larger matrix, at no alignment but the elements' own."""
-    big = torch.full((rows + 3, cols + 7), 3.0, dtype=dtype, device="cuda")
-    return big, big[1:1 + rows, 3:3 + cols]
+def inside(rows, cols, dtype, lines=False):
+    """Room for an output in the midst of a larger matrix, at no alignment but the elements' own, or with
+    rows that begin with a line of memory."""
+    around, at = (-cols % 128 + 256, 128) if lines else (7, 3)
+    big = torch.full((rows + 3, cols + around), 3.0, dtype=dtype, device="cuda")
+    return big, big[1:1 + rows, at:at + cols]
 
 
 def check(out, want):
@@ -70,16 +72,19 @@ def kind(m, n, k, jobs=1, gated=False, sums=1):
     return KINDS[matmul_kind(jobs, m, n, sums * -(-k // 256), gated)]
 
 
-# one size to each kernel; the last one's outputs of every type pass the caches
+# one size to each kernel, twice the largest: outputs of 86 MB and more pass the caches where rows begin with a
+# line of memory, those of 172 MB anyhow
+by_lines = pytest.mark.parametrize("lines", [False, True], ids=["any", "lines"])
 PRODUCTS = [("rows", 13, 5001, 700), ("64", 333, 1111, 2001), ("128 deep", 1500, 1900, 700), ("128", 2300, 2900, 300),
             ("256", 4001, 3999, 1001), ("256", 6501, 6603, 1500)]
 
 
 @by_type
+@by_lines
 @pytest.mark.parametrize("name,m,n,k", PRODUCTS)
-def test_matmul(name, m, n, k, dtype):
+def test_matmul(name, m, n, k, lines, dtype):
     assert kind(m, n, k) == name
-    a, b, out = random_held(m, m, k), random_held(n + 1, n, k), inside(m, n, dtype)
+    a, b, out = random_held(m, m, k), random_held(n + 1, n, k), inside(m, n, dtype, lines)
     mq.mq_mx4_matmul(a, b, out[1])
     check(out, product((values(a), values(b))))
 
@@ -109,13 +114,14 @@ GATED = [("rows", 5, 3001, 700, True), ("64", 300, 2001, 700, True), ("128 deep"
 
 
 @by_type
+@by_lines
 @pytest.mark.parametrize("name,m,f,k,keep", GATED)
-def test_gated(name, m, f, k, keep, dtype):
+def test_gated(name, m, f, k, keep, lines, dtype):
     assert kind(m, f, k, gated=True) == name
     x, wg, wu = grid(m, m, k, dtype), random_held(2, f, k), random_held(3, f, k)
     wg.scales -= 6
     wu.scales -= 4
-    h, g, u = (inside(m, f, dtype) for _ in range(3))
+    h, g, u = (inside(m, f, dtype, lines) for _ in range(3))
     ws = mq.mx4_gated_workspace(m, f, k)
     mq.mq_mx4_gated(x, wg, wu, h[1], ws, *((g[1], u[1]) if keep else ()))
     rg, ru = product((x.double(), values(wg))), product((x.double(), values(wu)))
@@ -157,7 +163,8 @@ def test_linear_backward(names, m, n, k, dtype, w_dtype):
 @pytest.mark.parametrize("names,m,f,k", [(("256", "128 deep"), 4001, 500, 3999), (("128 deep", "256"), 1001, 4001, 3999),
                                          (("128", "64"), 3001, 300, 2301), (("rows", "64"), 9, 300, 3001),
                                          (("128 deep", "rows"), 600, 13, 5001)])
-def test_gated_backward(names, m, f, k, dtype, w_dtype):
+@by_lines
+def test_gated_backward(names, m, f, k, lines, dtype, w_dtype):
     """With g of 32 (s = 1, 1 - s = 0 in fp32) or -256 (s = 0) and u of +-2, dg and du are dh times a power of
     two, or 0: exact, and what is quantized is exact too."""
     assert (kind(m, k, f, sums=2), kind(f, k, m, jobs=2)) == names
@@ -167,7 +174,7 @@ def test_gated_backward(names, m, f, k, dtype, w_dtype):
     u[:, 1::3] = -2.0
     x_col, wg_col, wu_col = random_held(2, k, m), random_held(3, k, f), random_held(4, k, f)
     wu_col.scales -= 4  # du is 16 times dg
-    dx, dwg, dwu = inside(m, k, dtype), inside(f, k, w_dtype), inside(f, k, w_dtype)
+    dx, dwg, dwu = inside(m, k, dtype, lines), inside(f, k, w_dtype, lines), inside(f, k, w_dtype, lines)
     mq.mq_mx4_gated_backward(dh, g, u, x_col, wg_col, wu_col, dx[1], dwg[1], dwu[1],
                              mq.mx4_gated_backward_workspace(m, f, k))
     on = (g > 0).double()
