@@ -222,7 +222,7 @@ mq_status mq_mx4_gated(const mq_matrix *x, const mq_mx4 *wg, const mq_mx4 *wu, c
     if (need && (!ws || ws_bytes < need)) return MQ_ERR_WORKSPACE;
     mq::Mx4View row;
     uint8_t *at = static_cast<uint8_t *>(ws);
-    const bool inside = !x_col && mq::mx4_quantizes_rows(m, f, k);
+    const bool inside = !x_col && mq::mx4_takes_rows(m, f, true) && mq::mx4_quantizes_rows(m, f, k);
     const mq_status st = quantize_input(x, x_col, inside, at, row, stream);
     if (st != MQ_OK) return st;
     mq::Mx4MatmulArgs a = matmul_args(row, view(wg), h);

@@ -335,17 +335,12 @@ int64_t tiles_of(int jobs, int m, int n, int bm, int bn)
     return (((int64_t)m + bm - 1) / bm) * (((int64_t)n + bn - 1) / bn) * jobs;
 }
 
-// Up to 16 rows, a workgroup takes 16 columns and its waves share the sum; where tiles of 64 columns come
-// near to one a CU, they read the weight in larger pieces (16 x 4096 on 16384: 8.1 us in place of 11.2; on
-// 8192 7.1, where strips of 16 take 6.4).
-bool rows_kind(int m, int64_t n) { return m <= 16 && n < 12288; }
-
 } // namespace
 
 int mx4_matmul_kind(int jobs, int m, int n, int pieces, bool gated)
 {
     const auto tiles = [&](int bm, int bn) { return tiles_of(jobs, m, n, bm, bn); };
-    if (rows_kind(m, (int64_t)n * jobs)) return kMx4Rows;
+    if (mx4_takes_rows(m, (int64_t)n * jobs, gated)) return kMx4Rows;
     // 64 x 64 while the chip holds them all at once: 512 x 4096 x 4096 (512 tiles) 9.8 us, 128 x 128 12.4;
     // 1024 x 4096 x 4096 17.4 and 13.9. Gated (twice the weight's rows to a tile): 300 x 1024 on 2700 (215)
     // 9.6 and 11.1, 256 x 4096 on 8192 (512) 17.2 and 15.2.
@@ -362,7 +357,7 @@ int mx4_matmul_kind(int jobs, int m, int n, int pieces, bool gated)
 
 bool mx4_quantizes_rows(int m, int n, int k)
 {
-    return rows_kind(m, n) && (int64_t)m * k <= 1 << 14 && (int64_t)m * k * ((n + 15) / 16) <= 1 << 22;
+    return mx4_takes_rows(m, n, false) && (int64_t)m * k <= 1 << 14 && (int64_t)m * k * ((n + 15) / 16) <= 1 << 22;
 }
 
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs &given, hipStream_t st)

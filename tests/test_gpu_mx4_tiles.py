@@ -162,7 +162,7 @@ def test_linear_backward(names, m, n, k, dtype, w_dtype):
 @pytest.mark.parametrize("dtype,w_dtype", [(BF16, BF16), (F16, F32), (F32, F16)], ids=["bf16", "f16", "f32"])
 @pytest.mark.parametrize("names,m,f,k", [(("256", "128 deep"), 4001, 500, 3999), (("128 deep", "256"), 1001, 4001, 3999),
                                          (("128", "64"), 3001, 300, 2301), (("rows", "64"), 9, 300, 3001),
-                                         (("128 deep", "rows"), 600, 13, 5001)])
+                                         (("128 deep", "rows"), 600, 13, 4001)])
 @by_lines
 def test_gated_backward(names, m, f, k, lines, dtype, w_dtype):
     """With g of 32 (s = 1, 1 - s = 0 in fp32) or -256 (s = 0) and u of +-2, dg and du are dh times a power of

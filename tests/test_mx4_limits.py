@@ -43,7 +43,10 @@ def test_kinds():
                        ((1024, 4096, 4096), "128 deep"), ((2048, 2048, 8192), "128 deep"), ((2048, 4096, 4096), "128"),
                        ((4096, 4096, 512), "128"), ((4096, 4096, 4096), "256"), ((8192, 8192, 4096), "256")):
         assert kind(*size) == name, size
-    assert kind(16, 12288, 4096) == "64" and kind(17, 16, 32) == "64"
+    for m, n, gated, name in ((16, 8192, False, "rows"), (16, 8193, False, "64"), (4, 12288, False, "rows"),
+                              (4, 12289, False, "64"), (1, 8192, True, "rows"), (1, 8193, True, "64"), (17, 16, False, "64")):
+        assert kind(m, n, 4096, gated=gated) == name, (m, n, gated)
+    assert kind(13, 4097, 300, jobs=2) == "64"
     assert kind(300, 2700, 1024, gated=True) == "64" and kind(4096, 8192, 4096, gated=True) == "256"
     assert kind(BIG, BIG, BIG) == "256"
 
