@@ -53,16 +53,16 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Mx4QuantArgs a, 
 // Lane (q, cg) of a wave holds NR rows of 8 columns: 8 NR rows of 64 columns to a wave, and four waves
 // beside each other, so that rows are read in long runs (one above another: gradients of 4096 x 8192
 // 80 us in place of 61, fp32 42.5 in place of 40). A row's block lies in a quad of lanes; a column's in
-// 32 / NR lanes, 8 lanes apart (NR = 4, 8 or 16; 32 rows of 16-bit elements: the kernel behind this one).
+// 32 / NR lanes, 8 lanes apart (NR = 4 or 8; 32 rows of 16-bit elements: the kernel behind this one).
 
 // Eight values to quantize: of x, or of dg and du of h = silu(g) u.
-template <int DT, bool GRAD, bool TAIL, bool PASS> struct Source {
+template <int DT, bool GRAD, bool TAIL> struct Source {
     static constexpr int K = GRAD ? 2 : 1;
     static __device__ __forceinline__ void load(const Mx4QuantArgs &a, int64_t r, Reach at, float (*v)[8])
     {
         typedef typename Dense<DT>::T T;
         const auto get = [&](const MatView &m, float *to) {
-            values8<DT, TAIL>(load8<TAIL, PASS>(static_cast<const T *>(m.p) + r * m.stride, at, a.cols), at, to);
+            values8<DT, TAIL>(load8<TAIL>(static_cast<const T *>(m.p) + r * m.stride, at, a.cols), at, to);
         };
         get(a.x, v[0]);
         if constexpr (GRAD) {
@@ -94,8 +94,8 @@ __device__ __forceinline__ uint32_t max_lane_xor_32(uint32_t v)
 template <int DT, bool GRAD, int NR, bool SR, bool TAIL>
 __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs a, int across)
 {
-    static_assert(NR == 4 || NR == 8 || NR == 16, "a column's block is in two lanes or more");
-    constexpr int K = Source<DT, GRAD, TAIL, (NR >= 16)>::K, WR = 8 * NR; // rows of a wave
+    static_assert(NR == 4 || NR == 8, "a column's block is in four lanes or eight");
+    constexpr int K = Source<DT, GRAD, TAIL>::K, WR = 8 * NR; // rows of a wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 3, cg = lane & 7;
     const int c0 = ((int)(blockIdx.x % across) * 4 + wave) * 64, c = c0 + cg * 8;
     const int r0 = (int)(blockIdx.x / across) * WR + q * NR;
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         float t[K][8];
-        Source<DT, GRAD, TAIL, (NR >= 16)>::load(a, min(r0 + r, a.rows - 1), reach, t);
+        Source<DT, GRAD, TAIL>::load(a, min(r0 + r, a.rows - 1), reach, t);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -139,24 +139,18 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
 #pragma unroll
                 for (int r = 0; r < NR; ++r) amax = max_u32(amax, __float_as_uint(v[k][r][i]) & 0x7FFFFFFFu);
                 amax = max_u32(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0x128, 0xF, 0xF, true)); // lane ^ 8
-                if constexpr (NR < 16) amax = max_lane_xor_16(amax);
+                amax = max_lane_xor_16(amax);
                 if constexpr (NR < 8) amax = max_lane_xor_32(amax);
                 const uint32_t e = mx4_scale(amax);
                 if (c + i >= a.cols) continue;
-                constexpr int E = (NR + 7) / 8;
-                uint32_t codes[E];
+                float t[8];
 #pragma unroll
-                for (int w = 0; w < E; ++w) {
-                    const uint64_t n = 4 * ((uint64_t)(c + i) * blocks) + (uint64_t)(r0 / 8 + w);
-                    float t[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) t[j] = v[k][(8 * w + j) % NR][i]; // (NR = 4: twice, in either half's place)
-                    codes[w] = encode8<SR>(t, e, n, 2 * k + 1, a.seed_lo, a.seed_hi);
-                }
+                for (int j = 0; j < 8; ++j) t[j] = v[k][j % NR][i]; // (NR = 4: twice, in either half's place)
+                const uint64_t n = 4 * ((uint64_t)(c + i) * blocks) + (uint64_t)(r0 / 8);
+                const uint32_t codes = encode8<SR>(t, e, n, 2 * k + 1, a.seed_lo, a.seed_hi);
                 uint32_t *to = (uint32_t *)(first + i * 128);
-                if constexpr (NR == 16) *(uint64_t *)to = *(const uint64_t *)codes;
-                else if constexpr (NR == 8) *to = codes[0];
-                else ((uint16_t *)to)[part / 4 % 2] = (uint16_t)(part & 4 ? codes[0] >> 16 : codes[0]);
+                if constexpr (NR == 8) *to = codes;
+                else ((uint16_t *)to)[part / 4 % 2] = (uint16_t)(part & 4 ? codes >> 16 : codes);
                 if (part % 32 == 0) zs[i * 8] = (uint8_t)e;
             }
         }
@@ -333,7 +327,8 @@ hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
     if (!grad && !a.col.codes) return rows_alone<DT, SR>(a, st);
     const int height = mx4_quantize_height(a.rows, a.cols, DT, SR, grad);
     if (grad) return height == 8 ? both<DT, true, 8, SR>(a, st) : both<DT, true, 4, SR>(a, st);
-    if (height >= 16) return both<DT, false, DT != MQ_F32 && !SR ? 32 : 16, SR>(a, st);
+    if constexpr (DT != MQ_F32 && !SR)
+        if (height == 32) return both<DT, false, 32, SR>(a, st);
     return height == 8 ? both<DT, false, 8, SR>(a, st) : both<DT, false, 4, SR>(a, st);
 }
 
@@ -346,12 +341,15 @@ hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
 
 } // namespace
 
-// The tallest tiles that give each SIMD a wave: taller ones write longer runs of a column's codes.
+// Rows to a lane. Packed 16-bit elements: 32, of which a column's codes are runs of 16 bytes, where each SIMD has
+// two waves (8192 x 4096, 2048 waves, 22.4 us, with 8 rows 26.3; 4096 x 4096, 1024 waves, 15.3 and 13.5). Else 8
+// where each SIMD has a wave, 4 below (2048 x 4096 in fp32, 2048 waves of 8, 10.2 and 10.5 us; 1024 x 2048 4.7 and 4.0;
+// stochastic 16.1 and 17.8, 9.3 and 7.1). Tiles of 16 rows of fp32 gain nothing: 8192 x 4096 41.2 us where 8 rows
+// take 38.3, stochastic 59 and 49.
 int mx4_quantize_height(int rows, int cols, int dtype, bool sr, bool gradients)
 {
     const auto waves = [&](int nr) { return ((int64_t)rows + 8 * nr - 1) / (8 * nr) * (((int64_t)cols + 63) / 64); };
-    const int tall = dtype != MQ_F32 && !sr ? 32 : 16;
-    if (!gradients && waves(tall) >= 1024) return tall;
+    if (dtype != MQ_F32 && !sr && !gradients && waves(32) >= 2048) return 32;
     return waves(8) >= 1024 ? 8 : 4;
 }
 

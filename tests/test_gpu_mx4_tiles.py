@@ -186,7 +186,7 @@ def test_gated_backward(names, m, f, k, lines, dtype, w_dtype):
 
 # ---- quantization --------------------------------------------------------------------------------
 
-HEIGHTS = [(70, 65569), (33, 65536), (130, 22001), (300, 513)]
+HEIGHTS = [(70, 131105), (33, 131072), (130, 22001), (300, 513)]
 
 
 def spread(seed, rows, cols, dtype):
@@ -200,9 +200,9 @@ def spread(seed, rows, cols, dtype):
 @pytest.mark.parametrize("rows,cols", HEIGHTS)
 def test_quantize(rows, cols, dtype, sr):
     """Both directions, every byte, at each height of the tiles."""
-    tall = 32 if sr is None and dtype != F32 else 16
+    tall = 32 if sr is None and dtype != F32 else 8
     assert quantize_height(rows, cols, MQ_TYPE[dtype], sr is not None, False) == \
-        {65569: tall, 65536: tall, 22001: 8, 513: 4}[cols]
+        {131105: tall, 131072: tall, 22001: 8, 513: 4}[cols]
     x = spread(rows, rows, cols, dtype)
     row, col = mq.MX4.empty(rows, cols), mq.MX4.empty(cols, rows)
     for q in (row, col):
@@ -229,6 +229,7 @@ def special(rows, cols, dtype):
         top = bits.to(torch.int32).to(torch.uint16).view(dtype)
     x = torch.zeros(rows, cols, dtype=dtype)
     x[:32, :65536] = top
+    x[:32, 65536:131072] = top.flip(1)
     g = torch.Generator().manual_seed(2)
     edges = torch.tensor([.25, .5, .75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 0.0, -0.0])
     below = edges[torch.randint(0, 16, (rows - 32, cols), generator=g)]
@@ -245,7 +246,7 @@ def special(rows, cols, dtype):
 @by_type
 @pytest.mark.parametrize("rows,cols", HEIGHTS[:2])
 def test_quantize_every_value(rows, cols, dtype):
-    assert quantize_height(rows, cols, MQ_TYPE[dtype], False, False) == (16 if dtype == F32 else 32)
+    assert quantize_height(rows, cols, MQ_TYPE[dtype], False, False) == (8 if dtype == F32 else 32)
     x = special(rows, cols, dtype)
     row, col = mq.MX4.empty(rows, cols), mq.MX4.empty(cols, rows)
     mq.mq_mx4_quantize(x.cuda(), row, col)
