@@ -210,6 +210,14 @@ def quantize_linear_weight(weight: torch.Tensor, columns: bool) -> Tuple[MX4, Op
     return row, col
 
 
+class _NoGraph:
+    """The context of a forward pass that no graph records: nothing needs a gradient, nothing is kept."""
+    needs_input_grad = (False,) * 5
+
+    def save_for_backward(self, *tensors):
+        pass
+
+
 class _MXFunction(torch.autograd.Function):
     """What the 4-bit functions share."""
 
@@ -217,9 +225,7 @@ class _MXFunction(torch.autograd.Function):
     def apply(cls, *args):
         # ctx.needs_input_grad asks the inputs alone, so that a parameter needs a gradient also where no
         # graph is recorded: there, nothing is to be made for a backward pass
-        if not torch.is_grad_enabled():
-            args = [a.detach() if isinstance(a, torch.Tensor) else a for a in args]
-        return super().apply(*args)
+        return super().apply(*args) if torch.is_grad_enabled() else cls.forward(_NoGraph(), *args)
 
     @staticmethod
     def save(ctx, matrices: Sequence[Optional[MX4]], *tensors: Optional[torch.Tensor]):
