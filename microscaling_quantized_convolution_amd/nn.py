@@ -346,13 +346,17 @@ class _MXModule(nn.Module):
 
     def _release(self):
         """Let go of the weights held in 4 bits."""
-        self._held: Optional[List[MX4]] = None
-        self._held_of: list = []
-        self._held_at: Optional[Tuple[torch.cuda.Stream, torch.cuda.Event]] = None
+        # the matrices, what they were made of, the stream that made them and an event behind that: in one
+        # piece, which a call on another thread sees whole
+        self._kept: Optional[Tuple[List[MX4], list, torch.cuda.Stream, torch.cuda.Event]] = None
+
+    @property
+    def _held(self) -> Optional[List[MX4]]:
+        return None if self._kept is None else self._kept[0]
 
     def __getstate__(self) -> dict:
         # copies and pickles quantize their own weights
-        return {**self.__dict__, "_held": None, "_held_of": [], "_held_at": None}
+        return {**self.__dict__, "_kept": None}
 
     def train(self, mode: bool = True):
         self._release()
@@ -379,18 +383,19 @@ class _MXModule(nn.Module):
                 # quantized inside the graph: a replay reads the weights as they are then, no memory that is
                 # let go of when they change, and an eager call holds nothing that only a replay fills
                 return None
-            stream = torch.cuda.current_stream()
-            if len(now) != len(self._held_of) or any(a[0] is not b[0] or a[1:] != b[1:]
-                                                     for a, b in zip(now, self._held_of)):
-                self._held = [quantize_linear_weight(w.detach().contiguous(), False)[0] for w in weights]
-                self._held_of, self._held_at = now, (stream, stream.record_event())
-            elif stream != self._held_at[0]:
+            stream, kept = torch.cuda.current_stream(), self._kept
+            if kept is None or any(a[0] is not b[0] or a[1:] != b[1:] for a, b in zip(now, kept[1])):
+                held = [quantize_linear_weight(w.detach().contiguous(), False)[0] for w in weights]
+                self._kept = held, now, stream, stream.record_event()
+                return held
+            held, _, made_on, made = kept
+            if stream != made_on:
                 # another stream than the one that quantized them: it waits for that, and their memory is
                 # not used again before it has read them
-                stream.wait_event(self._held_at[1])
-                for t in (t for q in self._held for t in (q.codes, q.scales)):
+                stream.wait_event(made)
+                for t in (t for q in held for t in (q.codes, q.scales)):
                     t.record_stream(stream)
-        return self._held
+        return held
 
 
 class MXLinear(_MXModule):

@@ -234,3 +234,32 @@ def test_weights_changed_past_their_versions():
         m.up.data.mul_(3.0)
         m.cuda()
         assert torch.equal(m(x), fresh(m, x))
+
+
+def test_two_threads_at_once():
+    """First evaluations on two threads, each on its own stream, with weights that change between them."""
+    import threading
+    m, x = block(256, 512), dense(1, 9, 256, BF16).cuda()
+    streams, got, failed = [torch.cuda.Stream() for _ in range(3)], {}, []
+
+    def run(i, together):
+        try:
+            with torch.no_grad(), torch.cuda.stream(streams[i]):
+                together.wait()
+                got[i] = [m(x) for _ in range(20)]
+        except Exception as e:  # shown by the test, not lost with the thread
+            failed.append(e)
+    for _ in range(10):
+        with torch.no_grad():
+            m.gate.mul_(-1.25)
+        want = fresh(m, x)
+        torch.cuda.synchronize()
+        together = threading.Barrier(len(streams))
+        threads = [threading.Thread(target=run, args=(i, together)) for i in range(len(streams))]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert not failed
+        assert all(torch.equal(y, want) for i in got for y in got[i])
