@@ -280,3 +280,23 @@ def test_gated_backward_stochastic(m, f, height, dtype):
         rounded = ref.rounded(v, seed, d)
         assert not np.array_equal(rounded, v)
         assert torch.equal(got, product((cuda(rounded), values(q))).to(F32)), d
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("which", ["dh", "g", "u"])
+def test_gated_backward_not_finite(which, bad):
+    """One number that is not finite (a G or U past the range of f16, say) makes the sums of its row and of its
+    column NaN, and no others."""
+    m, f, k = 40, 70, 33
+    t = {"dh": grid(1, m, f, F16, 0.25), "g": torch.full((m, f), 32.0, dtype=F16, device="cuda"),
+         "u": torch.full((m, f), 2.0, dtype=F16, device="cuda")}
+    t["dh"][t["dh"] == 0] = 0.5
+    t[which][3, 65] = bad
+    x_col, wg_col, wu_col = random_held(2, k, m), random_held(3, k, f), random_held(4, k, f)
+    dx, dwg, dwu = (torch.empty(r, k, device="cuda") for r in (m, f, f))
+    mq.mq_mx4_gated_backward(t["dh"], t["g"], t["u"], x_col, wg_col, wu_col, dx, dwg, dwu,
+                             mq.mx4_gated_backward_workspace(m, f, k))
+    rows = lambda n, *at: torch.tensor([i in at for i in range(n)], device="cuda")[:, None].expand(n, k)
+    assert torch.equal(torch.isnan(dx), rows(m, 3)) and torch.isfinite(dx[4:]).all()
+    assert torch.equal(torch.isnan(dwg), rows(f, 65)) and torch.isfinite(dwg[:65]).all()
+    assert torch.equal(torch.isnan(dwu), rows(f, *([] if which == "u" else [65])))
