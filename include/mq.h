@@ -570,6 +570,8 @@ size_t mq_mx4_scales_bytes(int32_t rows, int32_t cols);
  * magnitude of a block,
  *   e    = the smallest byte with amax <= 6 * 2^(e-127), but in [2, 252]
  *   code = CastE2M1(x * 2^(127-e))
+ * (the scale is rounded up, so that nothing but amax past 6 * 2^125 saturates; the OCP microscaling
+ * text takes the largest power of two up to amax / 4 and lets what lies past 6 of it saturate).
  * CastE2M1 is to nearest, ties to the even code, saturating at 6 (MQ_RNE), or stochastic (MQ_SR): up
  * from the neighbour below in magnitude iff u < frac * 65536, where frac is the distance to it in
  * steps and u a 16-bit draw: of element j (of 32) of block t = row * ceil(cols / 32) + block, the
@@ -627,7 +629,8 @@ mq_status mq_mx4_linear_backward(const mq_matrix *dy, const mq_mx4 *x_col, const
  * mq_mx4_gated: h = silu(G) * U with G = Q(x) wg^T, U = Q(x) wu^T, silu(z) = z / (1 + exp(-z));
  * the two products and the activation stay in fp32, h is rounded once.
  * x: M x K, wg and wu: F x K, h: M x F. g, u: both null, or M x F of h's type: receive G and U,
- * rounded, for the backward pass. x_col: as for mq_mx4_linear.
+ * rounded, for the backward pass (in f16, one that rounds past 65504 becomes an infinity, and makes the
+ * gradients of its blocks NaN). x_col: as for mq_mx4_linear.
  * Errors: as mq_mx4_matmul.
  */
 size_t mq_mx4_gated_workspace_bytes(int32_t m, int32_t f, int32_t k);

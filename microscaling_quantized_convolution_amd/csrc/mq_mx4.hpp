@@ -61,9 +61,9 @@ hipError_t launch_mx4_dequantize(const Mx4View &q, const MatView &out, hipStream
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs &a, hipStream_t st);
 // Up to 16 rows, a workgroup takes 16 columns and its waves share the sum, while all of the launch's are there
 // at once, two to a CU (n <= 8192; behind that, tiles of 64 columns, which read the weight in larger pieces).
-// 4096 columns, us: 16 rows on 8192 7.0 (tiles 7.4), on 10240 9.0 (7.5); gated, 4 rows on 8192 11.3 (12.4), on
-// 9216 13.8 (12.5). Up to 4 rows the strips of a third workgroup still keep up: 1 row on 12288 7.3 (7.5), of 16384
-// columns 20.6 (22.0), 4 rows 21.8 (22.1), on 16384 9.3 (8.0); gated 1 row on 9216 13.4 (12.3).
+// 4096 columns, us: 16 rows on 8192 7.1 (tiles 7.5), on 10240 9.0 (7.5); gated, with the quantization, 4 rows on
+// 8192 11.5 (12.4), on 9216 13.9 (12.5). Plain products of up to 4 rows keep up with a third workgroup: 1 row on
+// 12288 7.3 (7.5), of 16384 columns 20.6 (22.0), 4 rows 21.7 (22.0); on 16384 9.3 (8.0).
 inline bool mx4_takes_rows(int m, int64_t n, bool gated) { return m <= 16 && n <= (m <= 4 && !gated ? 12288 : 8192); }
 // whether launch_mx4_matmul takes these m rows dense, and quantizes them itself (where it takes rows)
 bool mx4_quantizes_rows(int m, int n, int k);

@@ -12,20 +12,19 @@
 // instruction's rows and the tokens its columns: a lane's accumulators are then runs of four
 // columns of one output row.
 //
-// Tiles, and the launches' times (us, bf16 out unless said otherwise):
+// Tiles, and the launches' times (us, replayed from graphs, bf16 out; m x n x k):
 //   64 x 64, 4 slots, two workgroups a CU     small outputs: latency counts, and the number of workgroups.
-//                                             256 x 4096 x 4096 7.6 (128 x 128 12.2, 256 x 256 26)
-//   128 x 128, 4 slots                        up to one tile to a CU: 1024 x 4096 x 4096 14 (2 slots 16)
-//   128 x 128, 2 slots, two workgroups a CU   one's stores under the other's products: 4096 x 4096 x 512 12.7
-//   256 x 256, 2 slots                        8192 x 8192 x 4096 136 (4.0 PFLOP/s), x 16384 505 (4.35; before
-//                                             outputs passed the caches)
-// Bound at 256 x 256, for each piece of 1.81 us: the matrix instructions 0.98, but on random
-// data the clock falls, and products with their LDS reads alone take 1.47 (1.12 on zeros); the 68 KB of a piece 0.98 where two pieces are on their way, 1.36 where one is
-// and 0.6 from L2. A third slot has no room beside 64 KB, smaller tiles load more (256 x 128 with three
-// slots: 45 us at 4096 x 4096 x 4096 against 37). Scales by loads of their own to registers cost 0.29;
-// a piece's loads spread over its products arrive too late (524 to 559 us). Persistent workgroups that
-// load the next tile before they store this one gained nothing: stores to memory were the limit, and
-// writing large outputs past the caches is what moved it.
+//                                             256 x 4096 x 4096 7.9 (128 x 128 12.6, 256 x 256 26)
+//   128 x 128, 4 slots                        up to one tile to a CU: 1024 x 4096 x 4096 15.1 (2 slots 15.9)
+//   128 x 128, 2 slots, two workgroups a CU   one's stores under the other's products: 4096 x 4096 x 512 13.1
+//   256 x 256, 2 slots                        8192 x 8192 x 4096 144 (3.8 PFLOP/s), x 16384 504 (4.36)
+// Bound at 256 x 256, for each piece of 1.81 us: the matrix instructions 0.98 (8.8 PFLOP/s on all CUs), but
+// on random data the clock falls, and products with their LDS reads alone take 1.47 (1.12 on zeros); the 68 KB of
+// a piece 0.98 where two pieces are on their way, 1.36 where one is and 0.6 from L2. A third slot has no room
+// beside 64 KB, smaller tiles load more (256 x 128 with three slots: 45 us at 4096 x 4096 x 4096 against 37).
+// Scales by loads of their own to registers cost 0.29; a piece's loads spread over its products arrive too
+// late (524 to 559 us). Persistent workgroups that load the next tile before they store this one gained
+// nothing: stores to memory were the limit, and writing large outputs past the caches is what moved it.
 #include "mq_mx4_device.hpp"
 
 #include <type_traits>
@@ -147,7 +146,7 @@ __global__ void __launch_bounds__(WM * WN * 64, WM * WN == 4 && (WM * TM + WN * 
     constexpr int A = 0, B = STAGES * BM * 128, Z = B + STAGES * BN * 128, LDS = Z + STAGES * ZR * 8;
     __shared__ __align__(256) uint8_t lds[LDS];
     static_assert(BM % (W * 8) == 0 && BN % (W * 8) == 0, "the waves' shares are whole");
-    static_assert(LA % 2 == 0 && LB % 2 == 0, "");
+    static_assert(LA % 2 == 0 && LB % 2 == 0, "every other load takes its blocks 64 bytes on");
     static_assert(BM / 32 % LZ == 0 && ON / 32 % LZ == 0, "a wave's scales are of one operand");
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, h = lane >> 5, wm = wave / WN, wn = wave % WN;
@@ -341,15 +340,16 @@ int mx4_matmul_kind(int jobs, int m, int n, int pieces, bool gated)
 {
     const auto tiles = [&](int bm, int bn) { return tiles_of(jobs, m, n, bm, bn); };
     if (mx4_takes_rows(m, (int64_t)n * jobs, gated)) return kMx4Rows;
-    // 64 x 64 while the chip holds them all at once: 512 x 4096 x 4096 (512 tiles) 9.8 us, 128 x 128 12.4;
-    // 1024 x 4096 x 4096 17.4 and 13.9. Gated (twice the weight's rows to a tile): 300 x 1024 on 2700 (215)
-    // 9.6 and 11.1, 256 x 4096 on 8192 (512) 17.2 and 15.2.
+    // 64 x 64 while the chip holds them all at once: 512 x 4096 x 4096 (512 tiles) 10.7 us, 128 x 128 12.8;
+    // 1024 x 4096 x 4096 19.1 and 15.1. Gated (twice the weight's rows to a tile), with the quantization: 300 x
+    // 1024 on 2700 (215) 7.7 and 8.6, 256 x 4096 on 8192 (512) 19.2 and 17.4.
     if (tiles(64, 64) <= (gated ? 256 : 512)) return kMx4Tile64;
-    // four slots while no CU has two of 128 x 128: 2048 x 2048 x 8192 (256) 23.8 us, with two slots 26.6;
-    // 2048 x 4096 x 4096 (512) 25.8 and 22.8
+    // four slots while no CU has two of 128 x 128: 2048 x 2048 x 8192 (256) 24.9 us, with two slots 27.1;
+    // 2048 x 4096 x 4096 (512) 27.4 and 23.7
     if (tiles(128, gated ? 64 : 128) <= 256) return kMx4Tile128Deep;
     // 256 x 256 one to a CU, or 128 x 128 two to a CU: rounds of the chip, each of so much for a piece
-    // and for a tile's beginning and end (in ns, measured at 2 to 64 pieces)
+    // and for a tile's beginning and end (in ns, measured at 2 to 64 pieces): 2048 x 4096 x 4096 28.4 and
+    // 23.7 us, 4096 x 4096 x 512 13.4 and 13.1, 5000 x 3000 x 4096 36.1 and 43.2, 4096 x 4096 x 16384 131 and 158
     const double t256 = (double)((tiles(256, gated ? 128 : 256) + 255) / 256) * (1810.0 * pieces + 8000);
     const double t128 = (double)((tiles(128, gated ? 64 : 128) + 511) / 512) * (1250.0 * pieces + 3000);
     return t256 < t128 ? kMx4Tile256 : kMx4Tile128;
@@ -367,12 +367,12 @@ hipError_t launch_mx4_matmul(const Mx4MatmulArgs &given, hipStream_t st)
     const int kind = mx4_matmul_kind(a.jobs, a.m, a.n, a.pieces[0] + a.pieces[1], a.gated);
     if (kind == kMx4Rows) return launch_mx4_rows(a, st);
     // Outputs that would fill the caches, and those of many rounds of tiles, are written past them: other
-    // tiles' loads then pass the stores (8192 x 8192 x 4096 to bf16 155 -> 142 us, 8192 x 8192 x 512 58 -> 41,
-    // gated 4096 x 8192 x 4096 152 -> 138, with G and U 175 -> 158; but 8192 x 4096 x 4096, two rounds of 67
-    // MB, 73 -> 76). Rows that share lines of memory leave them half written: only the caches put these
-    // together (5000 x 4200 x 1000 to fp32 28 us, past them 34; gated 3000 x 5001 x 1000 with G and U 44,
+    // tiles' loads then pass the stores (8192 x 8192 x 4096 to bf16 155 -> 144 us, 8192 x 8192 x 512 57 -> 41,
+    // gated 4096 x 8192 x 4096 152 -> 139, with G and U 176 -> 159; but 8192 x 4096 x 4096, two rounds of 67
+    // MB, 75 -> 78). Rows that share lines of memory leave them half written: only the caches put these
+    // together (5000 x 4200 x 1000 to fp32 32 us, past them 36; gated 3000 x 5001 x 1000 with G and U 46,
     // past them 98), until one output alone is far larger than they are, and its sums are long enough to hide it
-    // (8192 x 8191 to bf16, 128 MB: of 512 columns 56 and 66 us, of 1024 68 and 65, of 4096 157 and 149).
+    // (8192 x 8191 to bf16, 134 MB: of 512 columns 57 and 66 us, of 1024 69 and 66, of 4096 158 and 152).
     const int size = a.y[0].dtype == MQ_F32 ? 4 : 2, outputs = a.jobs + (a.g.p ? 2 : 0);
     const int64_t bytes = (int64_t)a.m * a.n * size * outputs;
     const auto whole = [&](const MatView &y) { return (reinterpret_cast<uintptr_t>(y.p) | (uint64_t)y.stride * size) % 64 == 0; };

@@ -4,10 +4,10 @@
 // byte, and 32 codes of 4 bits. Every kernel reads its input once: where rows and columns are wanted,
 // a wave holds a tile of 64 columns in registers and takes the blocks of both directions from them.
 //
-// Bound by memory: 8192 x 4096 along both directions 22 us from bf16 (103 MB, 4.7 TB/s) and 40 from fp32
-// (170 MB, 4.2), rows alone 14.5 (85 MB, 5.9); gradients of 4096 x 8192 61 us (272 MB, 4.5 TB/s). Small ones by a wave's own length: 500 x
-// 1000 4.5 us with 4 rows to a lane, 9 with 32. Stochastic rounding (a Philox call to 8 elements and
-// direction) takes 8192 x 4096 bf16 to 51 us.
+// Bound by memory: 8192 x 4096 along both directions 22 us from bf16 (103 MB, 4.6 TB/s) and 38 from fp32
+// (170 MB, 4.5), rows alone 14.7 (85 MB, 5.8); gradients of 4096 x 8192 65 us (272 MB, 4.2 TB/s). Small ones by a
+// wave's own length: 500 x 1000 3.9 us with 4 rows to a lane, 8.5 with 32. Stochastic rounding (a Philox call
+// to 8 elements and direction) takes 8192 x 4096 bf16 to 45 us.
 #include "mq_mx4_device.hpp"
 
 namespace mq {
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Mx4QuantArgs a, 
 //
 // Lane (q, cg) of a wave holds NR rows of 8 columns: 8 NR rows of 64 columns to a wave, and four waves
 // beside each other, so that rows are read in long runs (one above another: gradients of 4096 x 8192
-// 80 us in place of 61, fp32 42.5 in place of 40). A row's block lies in a quad of lanes; a column's in
+// 80 us in place of 61). A row's block lies in a quad of lanes; a column's in
 // 32 / NR lanes, 8 lanes apart (NR = 4 or 8; 32 rows of 16-bit elements: the kernel behind this one).
 
 // Eight values to quantize: of x, or of dg and du of h = silu(g) u.
@@ -290,7 +290,8 @@ template <int DT, bool SR>
 hipError_t rows_alone(const Mx4QuantArgs &a, hipStream_t st)
 {
     const int groups = a.row.pieces() * 32, width = width_of(groups), across = (groups + width - 1) / width;
-    // four rows to a thread hide the loads' latency, where that leaves a workgroup for every CU
+    // four rows to a thread hide the loads' latency, where that leaves two workgroups for every CU: 1024 x 4096 bf16
+    // 3.9 -> 3.4 us, 8192 x 4096 15.4 -> 14.7 (fp32, longer loads, 5.1 and 5.2, 29.6 and 31.2); 256 x 4096 2.7 and 2.9
     const bool four = (int64_t)across * a.rows * width >= 4 * 256 * 512;
     const int per = 256 / width * (four ? 4 : 1);
     const int64_t grid = ((int64_t)a.rows + per - 1) / per * across;
@@ -342,10 +343,10 @@ hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
 } // namespace
 
 // Rows to a lane. Packed 16-bit elements: 32, of which a column's codes are runs of 16 bytes, where each SIMD has
-// two waves (8192 x 4096, 2048 waves, 22.4 us, with 8 rows 26.3; 4096 x 4096, 1024 waves, 15.3 and 13.5). Else 8
-// where each SIMD has a wave, 4 below (2048 x 4096 in fp32, 2048 waves of 8, 10.2 and 10.5 us; 1024 x 2048 4.7 and 4.0;
-// stochastic 16.1 and 17.8, 9.3 and 7.1). Tiles of 16 rows of fp32 gain nothing: 8192 x 4096 41.2 us where 8 rows
-// take 38.3, stochastic 59 and 49.
+// two waves (8192 x 4096, 2048 waves, 22.3 us, with 8 rows 26.4; 4096 x 4096, 1024 waves, 15.3 and 13.5). Else 8
+// where each SIMD has a wave, 4 below (2048 x 4096 bf16, 2048 waves of 8, 8.3 and 9.2 us, stochastic 16.1 and 17.8;
+// 1024 x 2048 4.5 and 4.1, stochastic 9.3 and 7.1). Tiles of 16 rows of fp32 gain nothing: 8192 x 4096 41.2 us where
+// 8 rows take 38.3, stochastic 59 and 49.
 int mx4_quantize_height(int rows, int cols, int dtype, bool sr, bool gradients)
 {
     const auto waves = [&](int nr) { return ((int64_t)rows + 8 * nr - 1) / (8 * nr) * (((int64_t)cols + 63) / 64); };

@@ -5,11 +5,12 @@
 // time, straight into the operand's registers (16x16x128: a lane's 16 bytes are one block, four blocks
 // of a row lie beside each other), and their sums are added in LDS, in the waves' order. Where the
 // input is small the workgroup quantizes it itself, into LDS, while the weights are on their way: one
-// launch, 4096 columns on 4096 rows 4.9 us replayed in place of 6.7. Every workgroup does it, so the
-// limit is on all of them together (4 rows on 11000: 15.4 us, in a launch of its own 14.0).
-// 13 x 8192 on 5120 rows: 9 us of 22.6 MB (2.5 TB/s; 64-column tiles 11); gated 4 x 4096 on 11000: 11 us
-// of 48 MB (4.4 TB/s). Fewer waves with more pieces each where workgroups are many: 16 waves to each of
-// 1024 workgroups take 12.6 us where 4 take 9.9.
+// launch, 4096 columns on 4096 rows 5.1 us replayed in place of 6.0. Every workgroup does it, so the
+// limit is on all of them together (4 rows of 4096 on 4096 7.0 us, in a launch of its own 6.5, which costs the
+// host as much; on 11000 14.2 and 10.4).
+// 13 x 8192 on 5120 rows: 10 us of 22.6 MB (2.2 TB/s; 64-column tiles 12); gated 4 x 4096 on 8192: 9.5 us of
+// 36 MB (3.8 TB/s). Fewer waves with more pieces each where workgroups are many: 16 waves to each of 1024
+// workgroups take 12.6 us where 4 take 9.9.
 #include "mq_mx4_device.hpp"
 
 namespace mq {

@@ -22,10 +22,12 @@ layers * step`` with ``step`` counted by the module (one per training forward), 
 reproducible, and no two layers or steps share a stream of random bits where every layer of a model
 has a number of its own in 0 .. ``layers`` - 1. An ``MXGatedMLP`` takes two: block i of ``layers``
 blocks is numbers 2i and 2i + 1 of 2 ``layers``. ``number_layers`` numbers a model of several kinds.
+A captured step replays the seeds that it was captured with.
 
 In eval mode with ``cache_weight=True`` the weight is quantized once and reused until the
 parameter changes (its version counter moves): the inference path then quantizes only
-activations.
+activations. (The modules on 4 bits: until one of the other changes that ``_MXModule`` names,
+too, and not in a captured graph, which quantizes the weight in every replay.)
 
 ``MXLinear`` and ``MXGatedMLP`` are the linear layer and the gated feed-forward block of a
 transformer on microscaled 4-bit operands (E2M1, a power-of-two scale per 32 elements along the
