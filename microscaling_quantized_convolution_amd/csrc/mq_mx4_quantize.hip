@@ -56,13 +56,13 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Mx4QuantArgs a, 
 // 32 / NR lanes, 8 lanes apart (NR = 4 or 8; 32 rows of 16-bit elements: the kernel behind this one).
 
 // Eight values to quantize: of x, or of dg and du of h = silu(g) u.
-template <int DT, bool GRAD, bool TAIL> struct Source {
+template <int DT, bool GRAD, bool TAIL, bool PASS> struct Source {
     static constexpr int K = GRAD ? 2 : 1;
     static __device__ __forceinline__ void load(const Mx4QuantArgs &a, int64_t r, Reach at, float (*v)[8])
     {
         typedef typename Dense<DT>::T T;
         const auto get = [&](const MatView &m, float *to) {
-            values8<DT, TAIL>(load8<TAIL>(static_cast<const T *>(m.p) + r * m.stride, at, a.cols), at, to);
+            values8<DT, TAIL>(load8<TAIL, PASS>(static_cast<const T *>(m.p) + r * m.stride, at, a.cols), at, to);
         };
         get(a.x, v[0]);
         if constexpr (GRAD) {
@@ -91,11 +91,11 @@ __device__ __forceinline__ uint32_t max_lane_xor_32(uint32_t v)
     return max_u32(s[0], s[1]);
 }
 
-template <int DT, bool GRAD, int NR, bool SR, bool TAIL>
+template <int DT, bool GRAD, int NR, bool SR, bool TAIL, bool PASS>
 __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs a, int across)
 {
     static_assert(NR == 4 || NR == 8, "a column's block is in four lanes or eight");
-    constexpr int K = Source<DT, GRAD, TAIL>::K, WR = 8 * NR; // rows of a wave
+    constexpr int K = Source<DT, GRAD, TAIL, PASS>::K, WR = 8 * NR; // rows of a wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 3, cg = lane & 7;
     const int c0 = ((int)(blockIdx.x % across) * 4 + wave) * 64, c = c0 + cg * 8;
     const int r0 = (int)(blockIdx.x / across) * WR + q * NR;
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(256, 2) mx4_quantize_both_kernel(Mx4QuantArgs 
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         float t[K][8];
-        Source<DT, GRAD, TAIL>::load(a, min(r0 + r, a.rows - 1), reach, t);
+        Source<DT, GRAD, TAIL, PASS>::load(a, min(r0 + r, a.rows - 1), reach, t);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -312,13 +312,25 @@ hipError_t both(const Mx4QuantArgs &a, hipStream_t st)
     const int cols = a.row.codes ? a.row.pieces() * 256 : a.cols, across = (cols + 255) / 256;
     const int64_t grid = ((int64_t)a.rows + 255) / 256 * (32 / NR) * across; // whole pieces of columns
     if (grid > kMaxGroups) return hipErrorInvalidValue;
-    const auto run = [&](auto tail) {
-        constexpr bool TAIL = decltype(tail)::value;
+    const auto run = [&](auto tail, auto pass) {
+        constexpr bool TAIL = decltype(tail)::value, PASS = decltype(pass)::value;
         if constexpr (NR == 32) mx4_quantize_packed_kernel<DT, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, across);
-        else mx4_quantize_both_kernel<DT, GRAD, NR, SR, TAIL><<<(uint32_t)grid, 256, 0, st>>>(a, across);
+        else mx4_quantize_both_kernel<DT, GRAD, NR, SR, TAIL, PASS><<<(uint32_t)grid, 256, 0, st>>>(a, across);
     };
-    if (a.cols % 8) run(Int<1>{});
-    else run(Int<0>{});
+    if constexpr (NR == 8 && !GRAD && (DT == MQ_F32 || SR)) { // (others of that size take the packed kernel)
+        // Large inputs of whole lines are read past the caches, which are then left to the codes and to what follows:
+        // fp32, with both results read back, 4096 x 4096 46.8 -> 43.5 us, 16384 x 4096 150 -> 135, though alone 71
+        // -> 73. Smaller ones may be in the caches already (2048 x 4096 23.8 and 25.2); lines that two rows share
+        // are read twice past them (3000 x 3001 30.7 and 36.0). Gradients, of three inputs, lose (102 and 110).
+        const int64_t size = DT == MQ_F32 ? 4 : 2;
+        const bool whole = (reinterpret_cast<uintptr_t>(a.x.p) | (uint64_t)(a.x.stride * size)) % 64 == 0 && a.cols % 8 == 0;
+        if (whole && (int64_t)a.rows * a.cols * size >= 64 << 20) {
+            run(Int<0>{}, Int<1>{});
+            return hipGetLastError();
+        }
+    }
+    if (a.cols % 8) run(Int<1>{}, Int<0>{});
+    else run(Int<0>{}, Int<0>{});
     return hipGetLastError();
 }
 
@@ -343,14 +355,15 @@ hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
 } // namespace
 
 // Rows to a lane. Packed 16-bit elements: 32, of which a column's codes are runs of 16 bytes, where each SIMD has
-// two waves (8192 x 4096, 2048 waves, 22.3 us, with 8 rows 26.4; 4096 x 4096, 1024 waves, 15.3 and 13.5). Else 8
+// a wave (8192 x 4096, 2048 waves, 22.3 us, with 8 rows 26.4; 4096 x 4096, 1024 waves, alone 15.3 and 13.5, but with
+// both results read back 36.9 and 39.9: its loads pass the caches, and leave them to what follows). Else 8
 // where each SIMD has a wave, 4 below (2048 x 4096 bf16, 2048 waves of 8, 8.3 and 9.2 us, stochastic 16.1 and 17.8;
 // 1024 x 2048 4.5 and 4.1, stochastic 9.3 and 7.1). Tiles of 16 rows of fp32 gain nothing: 8192 x 4096 41.2 us where
 // 8 rows take 38.3, stochastic 59 and 49.
 int mx4_quantize_height(int rows, int cols, int dtype, bool sr, bool gradients)
 {
     const auto waves = [&](int nr) { return ((int64_t)rows + 8 * nr - 1) / (8 * nr) * (((int64_t)cols + 63) / 64); };
-    if (dtype != MQ_F32 && !sr && !gradients && waves(32) >= 2048) return 32;
+    if (dtype != MQ_F32 && !sr && !gradients && waves(32) >= 1024) return 32;
     return waves(8) >= 1024 ? 8 : 4;
 }
 

@@ -53,7 +53,7 @@ def test_kinds():
 
 def test_heights():
     for case, rows in (((8192, 4096, mq.MQ_BF16, False, False), 32), ((8192, 4096, mq.MQ_F32, False, False), 8),
-                       ((8192, 4096, mq.MQ_F16, True, False), 8), ((4096, 4096, mq.MQ_BF16, False, False), 8), ((500, 1000, mq.MQ_F16, False, False), 4),
+                       ((8192, 4096, mq.MQ_F16, True, False), 8), ((4096, 4096, mq.MQ_BF16, False, False), 32), ((4095, 4032, mq.MQ_BF16, False, False), 8), ((500, 1000, mq.MQ_F16, False, False), 4),
                        ((300, 2700, mq.MQ_F16, False, True), 4), ((4096, 8192, mq.MQ_BF16, True, True), 8),
                        ((BIG, BIG, mq.MQ_BF16, False, False), 32)):
         assert quantize_height(*case) == rows, case
