@@ -4,8 +4,8 @@
 // byte, and 32 codes of 4 bits. Every kernel reads its input once: where rows and columns are wanted,
 // a wave holds a tile of 64 columns in registers and takes the blocks of both directions from them.
 //
-// Bound by memory: 8192 x 4096 along both directions 22 us from bf16 (103 MB, 4.6 TB/s) and 38 from fp32
-// (170 MB, 4.5), rows alone 14.7 (85 MB, 5.8); gradients of 4096 x 8192 65 us (272 MB, 4.2 TB/s). Small ones by a
+// Bound by memory: 8192 x 4096 along both directions 22 us from bf16 (103 MB, 4.6 TB/s) and 39 from fp32
+// (170 MB, 4.4), rows alone 14.7 (85 MB, 5.8); gradients of 4096 x 8192 65 us (272 MB, 4.2 TB/s). Small ones by a
 // wave's own length: 500 x 1000 3.9 us with 4 rows to a lane, 8.5 with 32. Stochastic rounding (a Philox call
 // to 8 elements and direction) takes 8192 x 4096 bf16 to 45 us.
 #include "mq_mx4_device.hpp"
@@ -358,8 +358,8 @@ hipError_t quantize(const Mx4QuantArgs &a, bool grad, hipStream_t st)
 // a wave (8192 x 4096, 2048 waves, 22.3 us, with 8 rows 26.4; 4096 x 4096, 1024 waves, alone 15.3 and 13.5, but with
 // both results read back 36.9 and 39.9: its loads pass the caches, and leave them to what follows). Else 8
 // where each SIMD has a wave, 4 below (2048 x 4096 bf16, 2048 waves of 8, 8.3 and 9.2 us, stochastic 16.1 and 17.8;
-// 1024 x 2048 4.5 and 4.1, stochastic 9.3 and 7.1). Tiles of 16 rows of fp32 gain nothing: 8192 x 4096 41.2 us where
-// 8 rows take 38.3, stochastic 59 and 49.
+// 1024 x 2048 4.5 and 4.1, stochastic 9.3 and 7.1). Tiles of 16 rows of fp32 gain nothing: 12288 x 4096 59.2 us where
+// 8 rows take 56.3, 3584 x 4096 19.8 and 13.7, with both results read back 107 and 104, 40.7 and 41.0.
 int mx4_quantize_height(int rows, int cols, int dtype, bool sr, bool gradients)
 {
     const auto waves = [&](int nr) { return ((int64_t)rows + 8 * nr - 1) / (8 * nr) * (((int64_t)cols + 63) / 64); };
