@@ -339,6 +339,10 @@ class _MXModule(nn.Module):
     another takes its place, or the module is moved, cast, or told ``train()`` or ``eval()`` (changes through
     ``.data`` are not counted: they need one of these)."""
 
+    # the matrices, what they were made of, the stream that made them and an event behind that: in one
+    # piece, which a call on another thread sees whole
+    _kept: Optional[Tuple[List[MX4], list, torch.cuda.Stream, torch.cuda.Event]] = None
+
     def __init__(self, layer_index: int, layers: int, seed_base: int, cache_weight: bool):
         super().__init__()
         self.layer_index, self.layers, self.seed_base = layer_index, layers, seed_base
@@ -348,9 +352,7 @@ class _MXModule(nn.Module):
 
     def _release(self):
         """Let go of the weights held in 4 bits."""
-        # the matrices, what they were made of, the stream that made them and an event behind that: in one
-        # piece, which a call on another thread sees whole
-        self._kept: Optional[Tuple[List[MX4], list, torch.cuda.Stream, torch.cuda.Event]] = None
+        self._kept = None
 
     @property
     def _held(self) -> Optional[List[MX4]]:

@@ -1,6 +1,7 @@
 """GPU tests of what the 4-bit modules keep from one call to the next, and from the forward pass to the
 backward pass: copies, other streams, captured graphs, weights that change, memory."""
 import copy
+import gc
 import io
 import pickle
 
@@ -94,6 +95,7 @@ def test_backward_frees_what_it_kept():
     """A step's activations are freed by its backward pass, also while the outputs are still held."""
     m, x = mqnn.MXGatedMLP(256, 4096).cuda(), dense(1, 2048, 256, BF16).cuda().requires_grad_()
     m(x).sum().backward()  # gradients are there from now on
+    gc.collect()  # nothing of earlier tests is freed between the readings
     torch.cuda.synchronize()
     before = torch.cuda.memory_allocated()
     y = m(x)
@@ -254,7 +256,7 @@ def test_two_threads_at_once():
             m.gate.mul_(-1.25)
         want = fresh(m, x)
         torch.cuda.synchronize()
-        together = threading.Barrier(len(streams))
+        together = threading.Barrier(len(streams), timeout=30)
         threads = [threading.Thread(target=run, args=(i, together)) for i in range(len(streams))]
         for t in threads:
             t.start()

@@ -86,3 +86,18 @@ def test_seeds_of_one_kind():
         m = torch.nn.Sequential(*(make(i) for i in range(4)))
         drawn = seeds(m, 3)
         assert sorted(drawn) == list(range(3, 3 + 12 * each))
+
+
+def test_modules_pickle_without_held_weights():
+    """A module's pickle has its parameters, numbers and steps alone, and one made without the rest is whole."""
+    m = mqnn.MXGatedMLP(32, 64, 1, 3, 7, cache_weight=True)
+    m.step, m.down.step = 4, 5
+    m._kept = [object()], [], None, None
+    other = pickle.loads(pickle.dumps(m))
+    assert other._held is None and other.down._held is None and m._held is not None
+    assert (other.step, other.down.step, other.cache_weight) == (4, 5, True)
+    assert all(torch.equal(a, b) for a, b in zip(m.parameters(), other.parameters()))
+    del other.__dict__["_kept"]
+    assert other._held is None and other.eval()._held is None
+    m.train()
+    assert m._held is None
